@@ -1,9 +1,12 @@
-"""GB300-native fused linear selected-token log-probability.
+"""GB300-native fused linear selected-token log-probability, and the operators
+around it: token embedding, layer norm, dropout.
 
 The computation lives in ``liblinear_logp.so`` (sm_103a CUDA kernels behind the
-C ABI of ``include/linear_logp.h``); this package only marshals PyTorch tensors
+C ABI of the headers in ``include/``); this package only marshals PyTorch tensors
 into that ABI.  Build the library with ``lm_head_selected_gb300.build.build()``.
 """
+from .drop import dropout, dropout_bwd, dropout_fwd  # noqa: F401
+from .embed import embedding, embedding_bwd, embedding_fwd  # noqa: F401
 from .fused import (  # noqa: F401
     fused_logp,
     fused_logp_bwd,
@@ -11,6 +14,7 @@ from .fused import (  # noqa: F401
     fused_logp_fwd,
     fused_logp_fwd_indexed,
 )
+from .norm import layer_norm, layer_norm_bwd, layer_norm_fwd  # noqa: F401
 from .ops import (  # noqa: F401
     IGNORE_INDEX,
     bwd_workspace_bytes,

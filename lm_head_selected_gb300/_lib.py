@@ -61,6 +61,17 @@ EXPORTED_FUSED = (
     "fused_logp_fwd_indexed",
     "fused_logp_bwd_indexed",
 )
+# include/embedding.h, include/layer_norm.h, include/dropout.h (operators around the head, same library)
+EXPORTED_OPERATORS = (
+    "embedding_fwd",
+    "embedding_bwd_workspace_bytes",
+    "embedding_bwd",
+    "layer_norm_fwd",
+    "layer_norm_bwd_workspace_bytes",
+    "layer_norm_bwd",
+    "dropout_fwd",
+    "dropout_bwd",
+)
 DEVICE_SELFTEST_CODE = 6
 LLP_ERR_SCRATCH_LIMIT = -8
 
@@ -174,6 +185,23 @@ def load() -> ctypes.CDLL:
         lib.fused_logp_bwd_indexed.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _p, _i64, _p, _i64, _p, _p,
                                                _size, _p]
         lib.fused_logp_bwd_indexed.restype = ctypes.c_int
+        _i, _u64, _f32, _f64 = ctypes.c_int, ctypes.c_uint64, ctypes.c_float, ctypes.c_double
+        lib.embedding_fwd.argtypes = [_p, _p, _i, _i64, _i64, _i64, _f32, _i64, _p, _p]
+        lib.embedding_fwd.restype = _i
+        lib.embedding_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        lib.embedding_bwd_workspace_bytes.restype = _size
+        lib.embedding_bwd.argtypes = [_p, _p, _i64, _i, _i64, _i64, _i64, _f32, _i64, _i, _p, _p, _size, _p]
+        lib.embedding_bwd.restype = _i
+        lib.layer_norm_fwd.argtypes = [_p, _i64, _i, _i64, _i64, _p, _p, _i, _f32, _p, _p, _p, _p]
+        lib.layer_norm_fwd.restype = _i
+        lib.layer_norm_bwd_workspace_bytes.argtypes = [_i64, _i64]
+        lib.layer_norm_bwd_workspace_bytes.restype = _size
+        lib.layer_norm_bwd.argtypes = [_p, _i64, _p, _i64, _i, _i64, _i64, _p, _p, _p, _i, _p, _p, _p, _p, _size, _p]
+        lib.layer_norm_bwd.restype = _i
+        lib.dropout_fwd.argtypes = [_p, _p, _i, _i64, _f64, _u64, _u64, _p, _p, _p]
+        lib.dropout_fwd.restype = _i
+        lib.dropout_bwd.argtypes = [_p, _i, _i64, _f64, _u64, _u64, _p, _p, _p]
+        lib.dropout_bwd.restype = _i
         _lib = lib
         return lib
 

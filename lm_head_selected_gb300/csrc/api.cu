@@ -8,7 +8,10 @@
 #include <mutex>
 #include <vector>
 
+#include "dropout.h"
+#include "embedding.h"
 #include "fused_logp.h"
+#include "layer_norm.h"
 #include "linear_logp.h"
 #include "llp_internal.h"
 #include "sm103_ptx.cuh"
@@ -1215,6 +1218,172 @@ int fused_logp_bwd_indexed(const float* grad_logp, const float* row_max, const f
                                                reinterpret_cast<const long long*>(targets), ignore_index, grad_logp,
                                                row_max, log_sum, sel.mask, grad_logits, vec, s);
   return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+// ----------------------------------------------------------------------------
+// Operators around the head (include/embedding.h, layer_norm.h, dropout.h).
+// ----------------------------------------------------------------------------
+static constexpr int64_t kMaxOpD = int64_t(1) << 24;
+
+static bool dtype_ok(int dtype) {
+  return dtype == llp::kDtypeBF16 || dtype == llp::kDtypeF32 || dtype == llp::kDtypeF16;
+}
+static uintptr_t dtype_bytes(int dtype) { return dtype == llp::kDtypeF32 ? 4 : 2; }
+// Rows of D elements, `stride` apart, N of them.
+static bool row_stride_ok(int64_t N, int64_t D, int64_t stride) {
+  return (N <= 1 && stride >= 0) || stride == 0 || (stride >= D && product_ok(N, stride));
+}
+
+static int embedding_shapes(int dtype, int64_t N, int64_t V, int64_t D) {
+  if (!dtype_ok(dtype) || N < 0 || V < 1 || D < 1 || N > kLim31 || V > kLim31 || D >= kMaxOpD)
+    return LLP_ERR_BAD_SHAPE;
+  return LLP_OK;
+}
+
+int embedding_fwd(const int64_t* tokens, const void* weight, int dtype, int64_t N, int64_t V, int64_t D, float scale,
+                  int64_t ignore_index, void* out, void* stream) {
+  int st = embedding_shapes(dtype, N, V, D);
+  if (st != LLP_OK) return st;
+  if (N == 0) return LLP_OK;
+  if (tokens == nullptr || weight == nullptr || out == nullptr) return LLP_ERR_NULL_POINTER;
+  if (!aligned(tokens, 8) || !aligned(weight, dtype_bytes(dtype)) || !aligned(out, dtype_bytes(dtype)))
+    return LLP_ERR_MISALIGNED;
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  llp::EmbeddingParams p = {reinterpret_cast<const long long*>(tokens), static_cast<int>(N), static_cast<int>(V),
+                            static_cast<int>(D), dtype, scale, ignore_index};
+  const cudaError_t e = llp::launch_embedding_fwd(p, weight, out, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) {
+  if (N <= 0 || embedding_shapes(llp::kDtypeF32, N, V, D) != LLP_OK) return 0;
+  return llp::embedding_bwd_workspace(N, V, D);
+}
+
+int embedding_bwd(const int64_t* tokens, const void* grad_out, int64_t grad_out_row_stride, int dtype, int64_t N,
+                  int64_t V, int64_t D, float scale, int64_t ignore_index, int accumulate, void* grad_weight,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int st = embedding_shapes(dtype, N, V, D);
+  if (st != LLP_OK) return st;
+  if (!row_stride_ok(N, D, grad_out_row_stride)) return LLP_ERR_BAD_SHAPE;
+  if (N == 0 && accumulate) return LLP_OK;
+  if (grad_weight == nullptr) return LLP_ERR_NULL_POINTER;
+  if (!aligned(grad_weight, dtype_bytes(dtype))) return LLP_ERR_MISALIGNED;
+  if (N > 0) {
+    if (tokens == nullptr || grad_out == nullptr || workspace == nullptr) return LLP_ERR_NULL_POINTER;
+    if (!aligned(tokens, 8) || !aligned(grad_out, dtype_bytes(dtype)) || !aligned(workspace, 16))
+      return LLP_ERR_MISALIGNED;
+    if (workspace_bytes < embedding_bwd_workspace_bytes(N, V, D)) return LLP_ERR_WORKSPACE_TOO_SMALL;
+  }
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const size_t bytes = static_cast<size_t>(V) * static_cast<size_t>(D) * dtype_bytes(dtype);
+    return llp::note_cuda(cudaMemsetAsync(grad_weight, 0, bytes, s)) == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+  }
+  llp::EmbeddingParams p = {reinterpret_cast<const long long*>(tokens), static_cast<int>(N), static_cast<int>(V),
+                            static_cast<int>(D), dtype, scale, ignore_index};
+  const cudaError_t e =
+      llp::launch_embedding_bwd(p, grad_out, grad_out_row_stride, accumulate != 0, grad_weight, workspace, s);
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+static int layer_norm_shapes(int dtype, int param_dtype, int64_t N, int64_t D) {
+  if (!dtype_ok(dtype) || (param_dtype != dtype && param_dtype != llp::kDtypeF32)) return LLP_ERR_BAD_SHAPE;
+  if (N < 0 || D < 1 || N > kLim31 || D >= kMaxOpD) return LLP_ERR_BAD_SHAPE;
+  return LLP_OK;
+}
+
+int layer_norm_fwd(const void* x, int64_t x_row_stride, int dtype, int64_t N, int64_t D, const void* weight,
+                   const void* bias, int param_dtype, float eps, void* y, float* mean, float* rstd, void* stream) {
+  int st = layer_norm_shapes(dtype, param_dtype, N, D);
+  if (st != LLP_OK) return st;
+  if (!row_stride_ok(N, D, x_row_stride) || !(eps >= 0.f && eps <= 3.4e38f)) return LLP_ERR_BAD_SHAPE;
+  if (N == 0) return LLP_OK;
+  if (x == nullptr || y == nullptr || mean == nullptr || rstd == nullptr) return LLP_ERR_NULL_POINTER;
+  const uintptr_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ps) || !aligned(bias, ps) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return LLP_ERR_MISALIGNED;
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  llp::LayerNormParams p = {x, nullptr, weight, bias, x_row_stride, 0, static_cast<int>(N), static_cast<int>(D),
+                            dtype, param_dtype, eps};
+  const cudaError_t e = llp::launch_layer_norm_fwd(p, y, mean, rstd, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+size_t layer_norm_bwd_workspace_bytes(int64_t N, int64_t D) {
+  if (N <= 0 || layer_norm_shapes(llp::kDtypeF32, llp::kDtypeF32, N, D) != LLP_OK) return 0;
+  return llp::layer_norm_bwd_workspace(N, D);
+}
+
+int layer_norm_bwd(const void* grad_y, int64_t grad_y_row_stride, const void* x, int64_t x_row_stride, int dtype,
+                   int64_t N, int64_t D, const float* mean, const float* rstd, const void* weight, int param_dtype,
+                   void* grad_x, void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  int st = layer_norm_shapes(dtype, param_dtype, N, D);
+  if (st != LLP_OK) return st;
+  if (!row_stride_ok(N, D, x_row_stride) || !row_stride_ok(N, D, grad_y_row_stride)) return LLP_ERR_BAD_SHAPE;
+  const bool want_params = grad_weight != nullptr || grad_bias != nullptr;
+  if (grad_x == nullptr && !want_params) return LLP_OK;
+  if (N == 0 && !want_params) return LLP_OK;
+  const uintptr_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  if (!aligned(grad_weight, ps) || !aligned(grad_bias, ps)) return LLP_ERR_MISALIGNED;
+  if (N > 0) {
+    if (grad_y == nullptr || x == nullptr || mean == nullptr || rstd == nullptr) return LLP_ERR_NULL_POINTER;
+    if (want_params && workspace == nullptr) return LLP_ERR_NULL_POINTER;
+    if (!aligned(grad_y, es) || !aligned(x, es) || !aligned(grad_x, es) || !aligned(weight, ps) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || (want_params && !aligned(workspace, 16)))
+      return LLP_ERR_MISALIGNED;
+    if (want_params && workspace_bytes < layer_norm_bwd_workspace_bytes(N, D)) return LLP_ERR_WORKSPACE_TOO_SMALL;
+  }
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    void* const outs[2] = {grad_weight, grad_bias};
+    for (void* o : outs) {
+      if (o != nullptr && llp::note_cuda(cudaMemsetAsync(o, 0, static_cast<size_t>(D) * ps, s)) != cudaSuccess)
+        return fail_cuda(__LINE__);
+    }
+    return LLP_OK;
+  }
+  llp::LayerNormParams p = {x, grad_y, weight, nullptr, x_row_stride, grad_y_row_stride, static_cast<int>(N),
+                            static_cast<int>(D), dtype, param_dtype, 0.f};
+  const cudaError_t e =
+      llp::launch_layer_norm_bwd(p, mean, rstd, grad_x, grad_weight, grad_bias, workspace, dev->num_sms, s);
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+static int dropout_call(const void* x, const void* residual, int dtype, int64_t count, double p, uint64_t seed,
+                        uint64_t offset, const int64_t* device_offset, void* y, void* stream) {
+  if (!dtype_ok(dtype) || count < 0 || count >= kLim62 || !(p >= 0.0 && p <= 1.0)) return LLP_ERR_BAD_SHAPE;
+  if (count == 0) return LLP_OK;
+  if (x == nullptr || y == nullptr) return LLP_ERR_NULL_POINTER;
+  const uintptr_t es = dtype_bytes(dtype);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(residual, es) || !aligned(device_offset, 8))
+    return LLP_ERR_MISALIGNED;
+  DeviceInit* dev = nullptr;
+  const int st = init_device(&dev);
+  if (st != LLP_OK) return st;
+  const uint32_t T = static_cast<uint32_t>(p * 65536.0 + 0.5);
+  llp::DropoutParams d = {x, residual, y, count, dtype, T, T < 65536 ? 65536.f / static_cast<float>(65536 - T) : 0.f,
+                          seed, offset, reinterpret_cast<const long long*>(device_offset)};
+  const cudaError_t e = llp::launch_dropout(d, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+int dropout_fwd(const void* x, const void* residual, int dtype, int64_t count, double p, uint64_t seed,
+                uint64_t offset, const int64_t* device_offset, void* y, void* stream) {
+  return dropout_call(x, residual, dtype, count, p, seed, offset, device_offset, y, stream);
+}
+
+int dropout_bwd(const void* grad_y, int dtype, int64_t count, double p, uint64_t seed, uint64_t offset,
+                const int64_t* device_offset, void* grad_x, void* stream) {
+  return dropout_call(grad_y, nullptr, dtype, count, p, seed, offset, device_offset, grad_x, stream);
 }
 
 // One thread waits, with the production wait code, on a barrier that nothing

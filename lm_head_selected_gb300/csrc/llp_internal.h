@@ -268,4 +268,49 @@ cudaError_t launch_segment_sum(const float* part, int nseg, long long count, __n
                                cudaStream_t s, int f16 = 0);
 cudaError_t launch_bias_sum(const float* gb_part, int nblocks, int V, float* out, cudaStream_t s);
 
+// Token embedding (embedding.cu): lookup, and the table's gradient by sorted
+// tokens.  `stride`: elements between rows of grad_out.
+struct EmbeddingParams {
+  const long long* tokens;
+  int N, V, D;
+  int dtype;
+  float scale;
+  long long ignore_index;
+};
+cudaError_t launch_embedding_fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStream_t s);
+size_t embedding_bwd_workspace(long long N, long long V, long long D);
+cudaError_t launch_embedding_bwd(const EmbeddingParams& p, const void* grad_out, long long stride, int accumulate,
+                                 void* grad_weight, void* workspace, cudaStream_t s);
+
+// Layer norm (layer_norm.cu).  gy is the backward's upstream gradient; weight
+// and bias may be null.  gx, gw, gb may each be null.
+struct LayerNormParams {
+  const void* x;
+  const void* gy;
+  const void* weight;
+  const void* bias;
+  long long x_stride, gy_stride;  // elements between rows
+  int N, D;
+  int dtype, param_dtype;
+  float eps;
+};
+cudaError_t launch_layer_norm_fwd(const LayerNormParams& p, void* y, float* mean, float* rstd, cudaStream_t s);
+size_t layer_norm_bwd_workspace(long long N, long long D);
+cudaError_t launch_layer_norm_bwd(const LayerNormParams& p, const float* mean, const float* rstd, void* gx, void* gw,
+                                  void* gb, void* workspace, int num_sms, cudaStream_t s);
+
+// Dropout (dropout.cu): y = (16-bit lane >= threshold ? x * scale : 0) + residual.
+struct DropoutParams {
+  const void* x;
+  const void* residual;  // may be null
+  void* y;
+  long long count;
+  int dtype;
+  uint32_t threshold;
+  float scale;
+  uint64_t seed, offset;
+  const long long* device_offset;  // may be null; added to offset
+};
+cudaError_t launch_dropout(const DropoutParams& p, int num_sms, cudaStream_t s);
+
 }  // namespace llp

@@ -1,0 +1,107 @@
+"""PyTorch-facing wrappers of dropout (include/dropout.h).
+
+Argument marshalling only; the computation runs in ``liblinear_logp.so``.  The
+mask is a function of (seed, offset, element index): nothing is stored, and the
+backward draws it again.  Tensors are bf16, fp16 or fp32, contiguous, on a CUDA
+device.
+"""
+from __future__ import annotations
+
+from typing import Optional, Union
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .ops import _dtype_code, _out, _raw_stream, on_tensor_device
+
+_MASK64 = (1 << 64) - 1
+Offset = Union[int, torch.Tensor]
+
+
+def _check(x: torch.Tensor, name: str):
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _dtype_code(x, name)
+
+
+def _counter(seed: int, offset: Offset, device):
+    """(seed, host offset, device pointer or None)."""
+    if not isinstance(offset, torch.Tensor):
+        return int(seed) & _MASK64, int(offset) & _MASK64, None
+    if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
+        raise ValueError("offset must be an int, or one int64 on the inputs' device")
+    return int(seed) & _MASK64, 0, offset.data_ptr()
+
+
+def _probability(p: float) -> float:
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must lie in [0, 1], got {p}")
+    return p
+
+
+@on_tensor_device
+def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + (kept ? x / (1 - p) : 0), p rounded to a multiple of 2^-16.  ``offset`` numbers
+    the mask under one seed; as an int64 tensor on the device it is read when the kernel
+    runs, so that a captured graph can advance it between replays.  ``out`` may be x or
+    residual itself."""
+    code = _check(x, "x")
+    dev = x.device
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        if residual.device != dev or not residual.is_contiguous():
+            raise ValueError("residual must be contiguous, on x's device")
+    seed, off, off_ptr = _counter(seed, offset, dev)
+    p = _probability(p)
+    y = _out(out, x.shape, x.dtype, dev)
+    st = _lib.load().dropout_fwd(x.data_ptr(), None if residual is None else residual.data_ptr(), code, x.numel(), p,
+                                 seed, off, off_ptr, y.data_ptr(), _raw_stream(dev))
+    _lib.check("dropout_fwd", st)
+    return y
+
+
+@on_tensor_device
+def dropout_bwd(grad_y: torch.Tensor, p: float, seed: int, offset: Offset = 0,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grad_x = kept ? grad_y / (1 - p) : 0 under the forward's p, seed and offset."""
+    code = _check(grad_y, "grad_y")
+    dev = grad_y.device
+    seed, off, off_ptr = _counter(seed, offset, dev)
+    p = _probability(p)
+    gx = _out(out, grad_y.shape, grad_y.dtype, dev)
+    st = _lib.load().dropout_bwd(grad_y.data_ptr(), code, grad_y.numel(), p, seed, off, off_ptr, gx.data_ptr(),
+                                 _raw_stream(dev))
+    _lib.check("dropout_bwd", st)
+    return gx
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        ctx.p, ctx.seed = p, seed
+        if isinstance(offset, torch.Tensor):
+            ctx.save_for_backward(offset)
+        else:
+            ctx.offset = offset
+        return dropout_fwd(x, p, seed, offset, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y):
+        offset = ctx.saved_tensors[0] if ctx.saved_tensors else ctx.offset
+        gx = dropout_bwd(grad_y.contiguous(), ctx.p, ctx.seed, offset) if ctx.needs_input_grad[0] else None
+        return gx, grad_y if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: Offset = 0,
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + dropout(x, p), with autograd.  x and residual may have any shape (one
+    and the same); elements are numbered row-major."""
+    r = None if residual is None else residual.contiguous()
+    return _Dropout.apply(x.contiguous(), r, _probability(p), int(seed), offset)

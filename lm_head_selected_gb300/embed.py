@@ -1,0 +1,98 @@
+"""PyTorch-facing wrappers of the token embedding (include/embedding.h).
+
+Argument marshalling only; the computation runs in ``liblinear_logp.so``.
+tokens are int64, the table [V, D] bf16, fp16 or fp32, contiguous, on a CUDA
+device.  A token that equals ``ignore_index`` or lies outside [0, V) gives a
+zero row and gets no gradient.  ("Feat/nemotron h lm head logprob cuda",
+summary: untied embedding lookup with a sorted-segment deterministic
+grad_weight; here the sums are fp32.)
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .ops import IGNORE_INDEX, _dtype_code, _need, _need_rows, _out, _raw_stream, _workspace, on_tensor_device
+
+
+def _check_table(table: torch.Tensor, name: str):
+    if not isinstance(table, torch.Tensor) or table.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
+    _dtype_code(table, name)
+    _need(table, name, table.dtype, table.device, 2)
+    if table.shape[0] < 1 or table.shape[1] < 1:
+        raise ValueError(f"{name} must have at least one row and one column, got {tuple(table.shape)}")
+
+
+@on_tensor_device
+def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, ignore_index: int = IGNORE_INDEX,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """scale * weight[tokens], [N, D] in the table's dtype (the product in fp32, rounded once)."""
+    _check_table(weight, "weight")
+    _need(tokens, "tokens", torch.int64, weight.device, 1)
+    N, (V, D) = tokens.shape[0], weight.shape
+    out = _out(out, (N, D), weight.dtype, weight.device)
+    st = _lib.load().embedding_fwd(tokens.data_ptr(), weight.data_ptr(), _dtype_code(weight, "weight"), N, V, D,
+                                   float(scale), int(ignore_index), out.data_ptr(), _raw_stream(weight.device))
+    _lib.check("embedding_fwd", st)
+    return out
+
+
+@on_tensor_device
+def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, scale: float = 1.0,
+                  ignore_index: int = IGNORE_INDEX, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the table, [num_rows, D] in grad_out's dtype: row v is scale times the
+    sum of the rows of grad_out whose token is v, in ascending order, in fp32.
+
+    With ``accumulate`` the sums are added to ``out`` (required then), and rows that no
+    token names are neither read nor written: the form for a table tied to the LM head,
+    after ``linear_logp_bwd`` has written the head's gradient.  grad_out's rows may have
+    any stride."""
+    if not isinstance(grad_out, torch.Tensor) or grad_out.device.type != "cuda":
+        raise ValueError("grad_out must be a CUDA tensor; this op has no CPU path")
+    dev = grad_out.device
+    code = _dtype_code(grad_out, "grad_out")
+    stride = _need_rows(grad_out, "grad_out", dev)
+    _need(tokens, "tokens", torch.int64, dev, 1)
+    N, D = grad_out.shape
+    V = int(num_rows)
+    if tokens.shape[0] != N:
+        raise ValueError("tokens must have one entry per row of grad_out")
+    if V < 1 or D < 1:
+        raise ValueError("the table must have at least one row and one column")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: pass it")
+    out = _out(out, (V, D), grad_out.dtype, dev)
+    lib = _lib.load()
+    ws = _workspace(lib.embedding_bwd_workspace_bytes(N, V, D), dev, workspace)
+    st = lib.embedding_bwd(tokens.data_ptr(), grad_out.data_ptr(), stride, code, N, V, D, float(scale),
+                           int(ignore_index), int(bool(accumulate)), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                           _raw_stream(dev))
+    _lib.check("embedding_bwd", st)
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale, ignore_index):
+        ctx.save_for_backward(tokens)
+        ctx.rows, ctx.scale, ctx.ignore_index = weight.shape[0], scale, ignore_index
+        return embedding_fwd(tokens, weight, scale, ignore_index)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        tokens, = ctx.saved_tensors
+        g = grad_out if grad_out.stride(1) == 1 else grad_out.contiguous()
+        return None, embedding_bwd(g, tokens, ctx.rows, ctx.scale, ctx.ignore_index), None, None
+
+
+def embedding(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+              ignore_index: int = IGNORE_INDEX) -> torch.Tensor:
+    """scale * weight[tokens] with autograd: tokens [...] int64, weight [V, D] -> [..., D]."""
+    out = _Embedding.apply(tokens.reshape(-1).contiguous(), weight, float(scale), int(ignore_index))
+    return out.reshape(*tokens.shape, weight.shape[1])

@@ -62,6 +62,45 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, 
         raise ValueError(f"{name} must be contiguous")
 
 
+_DTYPE_CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
+    return code
+
+
+def _need_rows(t: torch.Tensor, name: str, device: torch.device) -> int:
+    """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got shape {tuple(t.shape)}")
+    N, D = t.shape
+    if D > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    stride = t.stride(0)
+    if N > 1 and 0 < stride < D:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return stride if N > 1 else D
+
+
+def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _check_inputs(hidden, weight, targets, bias, temperature, allow_f16=False):
     if not isinstance(hidden, torch.Tensor) or hidden.device.type != "cuda":
         raise ValueError("hidden must be a CUDA tensor; this op has no CPU path")
