@@ -20,8 +20,8 @@
  * Conventions as in linear_logp.h: device pointers, caller-owned buffers, work
  * enqueued on `stream`, arguments checked before anything is enqueued, the
  * same LLP_* status codes.  Tensors are contiguous, `count` elements of bf16
- * (dtype 0), fp32 (dtype 1) or fp16 (dtype 2), rounded once from fp32; count <
- * 2^62.  Element alignment suffices; 16-byte aligned tensors move fastest.  y
+ * (dtype 0), fp32 (dtype 1) or fp16 (dtype 2), rounded once from fp32; count <=
+ * 2^40.  Element alignment suffices; 16-byte aligned tensors move fastest.  y
  * may be x or residual itself.  count == 0 is a no-op.
  */
 #ifndef DROPOUT_H_

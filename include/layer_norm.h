@@ -14,10 +14,10 @@
  *     grad_bias[d]   = sum_n grad_y[n, d]
  *
  * Sums and statistics are fp32 (the variance from the centred values), each
- * output is rounded once.  The order of a row's sums depends on D, the types
- * and the tensors' alignment alone, so y, mean, rstd and grad_x rows are
- * bitwise the same for any batch; grad_weight / grad_bias are bitwise
- * reproducible for a given input on a given GPU model.
+ * output is rounded once.  The order of a row's sums depends on D and the types
+ * alone, so y, mean, rstd and grad_x rows are bitwise the same for any batch,
+ * layout and run; the order of grad_weight / grad_bias's sums depends on N, D
+ * and the types, so they are bitwise the same in every run.
  *
  * Conventions as in linear_logp.h: device pointers, caller-owned buffers, work
  * enqueued on `stream`, arguments checked before anything is enqueued, the
@@ -26,7 +26,7 @@
  * param_dtype: the same as dtype, or fp32.  weight and bias may each be NULL
  * (1 and 0).  The rows of x and grad_y start row_stride elements apart (D when
  * contiguous; 0 repeats one row); outputs are contiguous.  Element alignment
- * suffices; 16-byte aligned rows move fastest.  N < 2^31, 1 <= D < 2^24.
+ * suffices; 16-byte aligned rows move fastest.  N < 2^31, 1 <= D < 2^22.
  */
 #ifndef LAYER_NORM_H_
 #define LAYER_NORM_H_

@@ -21,7 +21,7 @@ LIB_NAME = "liblinear_logp.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "gh_small.cu", "logits.cu", "indexed.cu",
-           "embedding.cu", "layer_norm.cu", "dropout.cu"]
+           "embedding.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu", "dropout.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
                 "-I", INCLUDE, "-I", CSRC]

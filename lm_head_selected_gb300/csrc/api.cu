@@ -113,7 +113,7 @@ int init_device(DeviceInit** out) {
     if (major != 10 || minor != 3) {
       d.status = LLP_ERR_UNSUPPORTED_DEVICE;
     } else if (llp::fwd_setup(&d.caps) != cudaSuccess || llp::bwd_setup(&d.caps) != cudaSuccess ||
-               llp::small_grad_hidden_setup() != cudaSuccess ||
+               llp::small_grad_hidden_setup() != cudaSuccess || llp::embedding_setup() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status_ptr), g_status_word) != cudaSuccess) {
       d.status = fail_cuda(__LINE__);
     } else {
@@ -1223,7 +1223,7 @@ int fused_logp_bwd_indexed(const float* grad_logp, const float* row_max, const f
 // ----------------------------------------------------------------------------
 // Operators around the head (include/embedding.h, layer_norm.h, dropout.h).
 // ----------------------------------------------------------------------------
-static constexpr int64_t kMaxOpD = int64_t(1) << 24;
+static constexpr int64_t kMaxOpD = int64_t(1) << 22;
 
 static bool dtype_ok(int dtype) {
   return dtype == llp::kDtypeBF16 || dtype == llp::kDtypeF32 || dtype == llp::kDtypeF16;
@@ -1266,7 +1266,7 @@ int embedding_bwd(const int64_t* tokens, const void* grad_out, int64_t grad_out_
                   void* workspace, size_t workspace_bytes, void* stream) {
   int st = embedding_shapes(dtype, N, V, D);
   if (st != LLP_OK) return st;
-  if (!row_stride_ok(N, D, grad_out_row_stride)) return LLP_ERR_BAD_SHAPE;
+  if (!row_stride_ok(N, D, grad_out_row_stride) || N * D > (int64_t(1) << 44)) return LLP_ERR_BAD_SHAPE;
   if (N == 0 && accumulate) return LLP_OK;
   if (grad_weight == nullptr) return LLP_ERR_NULL_POINTER;
   if (!aligned(grad_weight, dtype_bytes(dtype))) return LLP_ERR_MISALIGNED;
@@ -1354,13 +1354,15 @@ int layer_norm_bwd(const void* grad_y, int64_t grad_y_row_stride, const void* x,
   llp::LayerNormParams p = {x, grad_y, weight, nullptr, x_row_stride, grad_y_row_stride, static_cast<int>(N),
                             static_cast<int>(D), dtype, param_dtype, 0.f};
   const cudaError_t e =
-      llp::launch_layer_norm_bwd(p, mean, rstd, grad_x, grad_weight, grad_bias, workspace, dev->num_sms, s);
+      llp::launch_layer_norm_bwd(p, mean, rstd, grad_x, grad_weight, grad_bias, workspace, s);
   return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
 }
 
+static constexpr int64_t kMaxDropout = int64_t(1) << 40;
+
 static int dropout_call(const void* x, const void* residual, int dtype, int64_t count, double p, uint64_t seed,
                         uint64_t offset, const int64_t* device_offset, void* y, void* stream) {
-  if (!dtype_ok(dtype) || count < 0 || count >= kLim62 || !(p >= 0.0 && p <= 1.0)) return LLP_ERR_BAD_SHAPE;
+  if (!dtype_ok(dtype) || count < 0 || count > kMaxDropout || !(p >= 0.0 && p <= 1.0)) return LLP_ERR_BAD_SHAPE;
   if (count == 0) return LLP_OK;
   if (x == nullptr || y == nullptr) return LLP_ERR_NULL_POINTER;
   const uintptr_t es = dtype_bytes(dtype);

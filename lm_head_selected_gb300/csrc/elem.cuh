@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "llp_internal.h"
 
 namespace llp {
@@ -80,5 +82,34 @@ struct Elem<kDtypeF32> {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
 };
+
+// A unit is what one thread moves at a time: a 16-byte vector, or one element
+// where rows are not 16-byte aligned.
+template <int DT, bool VEC>
+struct Unit {
+  using T = typename Elem<DT>::T;
+  static constexpr int W = VEC ? Elem<DT>::W : 1;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
+  static __device__ __forceinline__ Raw load(const T* p) {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p));
+    else return __ldg(p);
+  }
+  static __device__ __forceinline__ Raw zero() {
+    if constexpr (VEC) return make_uint4(0, 0, 0, 0);
+    else return Elem<DT>::put(0.f);
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[W]) {
+    if constexpr (VEC) Elem<DT>::unpack(r, v);
+    else v[0] = Elem<DT>::get(r);
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[W]) {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(p) = Elem<DT>::pack(v);
+    else *p = Elem<DT>::put(v[0]);
+  }
+  static __device__ __forceinline__ void store_raw(T* p, const Raw& r) { *reinterpret_cast<Raw*>(p) = r; }
+};
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline int elem_bytes(int dtype) { return dtype == kDtypeF32 ? 4 : 2; }
 
 }  // namespace llp

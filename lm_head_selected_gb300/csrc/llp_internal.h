@@ -277,6 +277,7 @@ struct EmbeddingParams {
   float scale;
   long long ignore_index;
 };
+cudaError_t embedding_setup();
 cudaError_t launch_embedding_fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStream_t s);
 size_t embedding_bwd_workspace(long long N, long long V, long long D);
 cudaError_t launch_embedding_bwd(const EmbeddingParams& p, const void* grad_out, long long stride, int accumulate,
@@ -297,7 +298,7 @@ struct LayerNormParams {
 cudaError_t launch_layer_norm_fwd(const LayerNormParams& p, void* y, float* mean, float* rstd, cudaStream_t s);
 size_t layer_norm_bwd_workspace(long long N, long long D);
 cudaError_t launch_layer_norm_bwd(const LayerNormParams& p, const float* mean, const float* rstd, void* gx, void* gw,
-                                  void* gb, void* workspace, int num_sms, cudaStream_t s);
+                                  void* gb, void* workspace, cudaStream_t s);
 
 // Dropout (dropout.cu): y = (16-bit lane >= threshold ? x * scale : 0) + residual.
 struct DropoutParams {
