@@ -20,7 +20,7 @@ Offset = Union[int, torch.Tensor]
 
 
 def _check(x: torch.Tensor, name: str):
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -61,7 +61,7 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residu
     p = _probability(p)
     y = _out(out, x.shape, x.dtype, dev)
     st = _lib.load().dropout_fwd(x.data_ptr(), None if residual is None else residual.data_ptr(), code, x.numel(), p,
-                                 seed, off, off_ptr, y.data_ptr(), _raw_stream(dev))
+                                 seed, off, off_ptr, y.data_ptr(), _raw_stream(dev.index))
     _lib.check("dropout_fwd", st)
     return y
 
@@ -76,7 +76,7 @@ def dropout_bwd(grad_y: torch.Tensor, p: float, seed: int, offset: Offset = 0,
     p = _probability(p)
     gx = _out(out, grad_y.shape, grad_y.dtype, dev)
     st = _lib.load().dropout_bwd(grad_y.data_ptr(), code, grad_y.numel(), p, seed, off, off_ptr, gx.data_ptr(),
-                                 _raw_stream(dev))
+                                 _raw_stream(dev.index))
     _lib.check("dropout_bwd", st)
     return gx
 

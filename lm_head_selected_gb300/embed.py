@@ -18,25 +18,23 @@ from . import _lib
 from .ops import IGNORE_INDEX, _dtype_code, _need, _need_rows, _out, _raw_stream, _workspace, on_tensor_device
 
 
-def _check_table(table: torch.Tensor, name: str):
-    if not isinstance(table, torch.Tensor) or table.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
-    _dtype_code(table, name)
-    _need(table, name, table.dtype, table.device, 2)
-    if table.shape[0] < 1 or table.shape[1] < 1:
-        raise ValueError(f"{name} must have at least one row and one column, got {tuple(table.shape)}")
-
-
 @on_tensor_device
 def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, ignore_index: int = IGNORE_INDEX,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * weight[tokens], [N, D] in the table's dtype (the product in fp32, rounded once)."""
-    _check_table(weight, "weight")
-    _need(tokens, "tokens", torch.int64, weight.device, 1)
-    N, (V, D) = tokens.shape[0], weight.shape
-    out = _out(out, (N, D), weight.dtype, weight.device)
-    st = _lib.load().embedding_fwd(tokens.data_ptr(), weight.data_ptr(), _dtype_code(weight, "weight"), N, V, D,
-                                   float(scale), int(ignore_index), out.data_ptr(), _raw_stream(weight.device))
+    if not isinstance(weight, torch.Tensor) or not weight.is_cuda:
+        raise ValueError("weight must be a CUDA tensor; this op has no CPU path")
+    dev = weight.device
+    code = _dtype_code(weight, "weight")
+    _need(weight, "weight", weight.dtype, dev, 2)
+    _need(tokens, "tokens", torch.int64, dev, 1)
+    V, D = weight.shape
+    if V < 1 or D < 1:
+        raise ValueError(f"weight must have at least one row and one column, got {(V, D)}")
+    N = tokens.shape[0]
+    out = _out(out, (N, D), weight.dtype, dev)
+    st = _lib.load().embedding_fwd(tokens.data_ptr(), weight.data_ptr(), code, N, V, D, scale, ignore_index,
+                                   out.data_ptr(), _raw_stream(dev.index))
     _lib.check("embedding_fwd", st)
     return out
 
@@ -52,7 +50,7 @@ def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, s
     token names are neither read nor written: the form for a table tied to the LM head,
     after ``linear_logp_bwd`` has written the head's gradient.  grad_out's rows may have
     any stride."""
-    if not isinstance(grad_out, torch.Tensor) or grad_out.device.type != "cuda":
+    if not isinstance(grad_out, torch.Tensor) or not grad_out.is_cuda:
         raise ValueError("grad_out must be a CUDA tensor; this op has no CPU path")
     dev = grad_out.device
     code = _dtype_code(grad_out, "grad_out")
@@ -69,9 +67,8 @@ def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, s
     out = _out(out, (V, D), grad_out.dtype, dev)
     lib = _lib.load()
     ws = _workspace(lib.embedding_bwd_workspace_bytes(N, V, D), dev, workspace)
-    st = lib.embedding_bwd(tokens.data_ptr(), grad_out.data_ptr(), stride, code, N, V, D, float(scale),
-                           int(ignore_index), int(bool(accumulate)), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                           _raw_stream(dev))
+    st = lib.embedding_bwd(tokens.data_ptr(), grad_out.data_ptr(), stride, code, N, V, D, scale, ignore_index,
+                           bool(accumulate), out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
     _lib.check("embedding_bwd", st)
     return out
 

@@ -18,7 +18,7 @@ EPS = 1e-5
 
 
 def _check_x(x: torch.Tensor):
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor; this op has no CPU path")
     code = _dtype_code(x, "x")
     stride = _need_rows(x, "x", x.device)
@@ -30,7 +30,7 @@ def _check_x(x: torch.Tensor):
 def _check_param(t: Optional[torch.Tensor], name: str, x: torch.Tensor, other: Optional[torch.Tensor]):
     if t is None:
         return
-    if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
+    if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
         raise TypeError(f"{name} must be a tensor of x's dtype or fp32")
     _need(t, name, t.dtype if other is None else other.dtype, x.device, 1)
     if t.shape[0] != x.shape[1]:
@@ -52,11 +52,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     N, D = x.shape
     param = weight if weight is not None else bias
     y = _out(out, (N, D), x.dtype, dev)
-    stats = torch.empty((2, N), dtype=torch.float32, device=dev)
-    mean, rstd = stats.unbind(0)
+    mean = torch.empty(N, dtype=torch.float32, device=dev)
+    rstd = torch.empty(N, dtype=torch.float32, device=dev)
     st = _lib.load().layer_norm_fwd(x.data_ptr(), stride, code, N, D, _ptr(weight), _ptr(bias),
-                                    code if param is None else _dtype_code(param, "weight"), float(eps),
-                                    y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev))
+                                    code if param is None else _dtype_code(param, "weight"), eps, y.data_ptr(),
+                                    mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev.index))
     _lib.check("layer_norm_fwd", st)
     return y, mean, rstd
 
@@ -92,7 +92,7 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
         ws = _workspace(lib.layer_norm_bwd_workspace_bytes(N, D), dev, workspace)
     st = lib.layer_norm_bwd(grad_y.data_ptr(), gy_stride, x.data_ptr(), stride, code, N, D, mean.data_ptr(),
                             rstd.data_ptr(), _ptr(weight), code if pdt == x.dtype else 1, _ptr(gx), _ptr(gw),
-                            _ptr(gb), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(dev))
+                            _ptr(gb), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(dev.index))
     _lib.check("layer_norm_bwd", st)
     return gx, gw, gb
 

@@ -74,6 +74,8 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
 
 def _need_rows(t: torch.Tensor, name: str, device: torch.device) -> int:
     """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.is_contiguous() and t.device == device:
+        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -97,8 +99,9 @@ def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.d
     return out
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle by device index, without the Stream object that
+# torch.cuda.current_stream() builds around it (3 us on the host).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check_inputs(hidden, weight, targets, bias, temperature, allow_f16=False):
