@@ -114,6 +114,7 @@ int init_device(DeviceInit** out) {
       d.status = LLP_ERR_UNSUPPORTED_DEVICE;
     } else if (llp::fwd_setup(&d.caps) != cudaSuccess || llp::bwd_setup(&d.caps) != cudaSuccess ||
                llp::small_grad_hidden_setup() != cudaSuccess || llp::embedding_setup() != cudaSuccess ||
+               llp::layer_norm_fwd_setup() != cudaSuccess || llp::layer_norm_bwd_setup() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status_ptr), g_status_word) != cudaSuccess) {
       d.status = fail_cuda(__LINE__);
     } else {

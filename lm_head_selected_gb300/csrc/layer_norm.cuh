@@ -5,114 +5,170 @@
 
 namespace llp {
 
-// The thread layout of a row: LANES threads own it together, lane l the units l,
-// l + LANES, ... (K of them).  A unit is W = 16 bytes of elements when D is whole
-// vectors, else one element.  The layout, and with it the order of every sum,
-// depends on D and the types alone; `al` only chooses between one 16-byte access
-// and W single ones.
+// Two fp32 values in one register pair, for the packed fp32 instructions.
+using F2 = float2;
+__device__ __forceinline__ F2 f2(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ F2 f2(float a) { return make_float2(a, a); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float sum2(F2 a) { return __fadd_rn(a.x, a.y); }
+
+// A row is D elements in `units` 16-byte vectors of W; the last one may be ragged.
+
 template <int DT, int W>
-struct RowUnit {
-  using T = typename Elem<DT>::T;
-  // W elements at p, as fp32
-  static __device__ __forceinline__ void load(const T* p, bool al, float (&v)[W]) {
-    if constexpr (W == 1) {
-      v[0] = Elem<DT>::get(__ldg(p));
-    } else if constexpr (W == Elem<DT>::W) {
-      if (al) {
-        Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), v);
-      } else {
+__device__ __forceinline__ void unpack2(const uint4& r, F2 (&v)[W / 2]) {
+  float f[W];
+  Elem<DT>::unpack(r, f);
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = Elem<DT>::get(__ldg(p + i));
-      }
-    } else {  // fp32 parameters next to 16-bit rows: two vectors
-      static_assert(DT == kDtypeF32 && W == 8, "");
-      if (al) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      } else {
+  for (int i = 0; i < W / 2; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT, int W>
+__device__ __forceinline__ uint4 pack2(const F2 (&v)[W / 2]) {
+  float f[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = __ldg(p + i);
-      }
-    }
-  }
-  // W elements kept as stored (16 bytes, or one element) until they are needed
-  using Raw = typename std::conditional<W == 1, T, uint4>::type;
-  static __device__ __forceinline__ Raw load_raw(const T* p, bool al) {
-    if constexpr (W == 1) {
-      return __ldg(p);
-    } else {
-      static_assert(W == Elem<DT>::W, "");
-      if (al) return __ldg(reinterpret_cast<const uint4*>(p));
-      float v[W];
+  for (int i = 0; i < W / 2; ++i) f[2 * i] = v[i].x, f[2 * i + 1] = v[i].y;
+  return Elem<DT>::pack(f);
+}
+
+// AL: rows are whole vectors, 16-byte aligned, and so are the parameters (a template
+// parameter: as a run-time flag it cost the aligned kernels the predicated-off
+// instructions of the other form, 1.5 times the time).
+
+// W parameters from `src`, those at or past `n` reading as `none`.
+template <int PT, int W, bool AL>
+__device__ __forceinline__ void load_params(const typename Elem<PT>::T* src, int n, float none, F2 (&v)[W / 2]) {
+  float f[W];
+  if constexpr (AL) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = Elem<DT>::get(__ldg(p + i));
-      return Elem<DT>::pack(v);  // exact: the values are of this type
-    }
-  }
-  static __device__ __forceinline__ Raw zero() {
-    if constexpr (W == 1) return Elem<DT>::put(0.f);
-    else return make_uint4(0, 0, 0, 0);
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[W]) {
-    if constexpr (W == 1) v[0] = Elem<DT>::get(r);
-    else Elem<DT>::unpack(r, v);
-  }
-  static __device__ __forceinline__ void store(T* p, bool al, const float (&v)[W]) {
-    if constexpr (W == 1) {
-      *p = Elem<DT>::put(v[0]);
-    } else {
-      if (al) {
-        *reinterpret_cast<uint4*>(p) = Elem<DT>::pack(v);
-      } else {
+    for (int i = 0; i < W / Elem<PT>::W; ++i)
+      Elem<PT>::unpack(__ldg(reinterpret_cast<const uint4*>(src) + i),
+                       *reinterpret_cast<float(*)[Elem<PT>::W]>(f + i * Elem<PT>::W));
+  } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) p[i] = Elem<DT>::put(v[i]);
-      }
-    }
+    for (int i = 0; i < W; ++i) f[i] = i < n ? Elem<PT>::get(__ldg(src + i)) : none;
   }
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+
+__device__ __forceinline__ void copy_async(void* slot, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* slot, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// One vector of a row into shared memory: asynchronously when it is 16-byte aligned, else its
+// first n <= W elements one by one.
+template <int DT, bool AL>
+__device__ __forceinline__ void copy_vector(uint4* slot, const typename Elem<DT>::T* p, int n) {
+  constexpr int W = Elem<DT>::W;
+  if constexpr (AL) {
+    copy_async(slot, p);
+  } else if constexpr (DT == kDtypeF32) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) copy_async4(reinterpret_cast<float*>(slot) + i, p + i);
+  } else {
+    uint16_t v[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + i) : 0;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[2 * i] | static_cast<uint32_t>(v[2 * i + 1]) << 16;
+    *slot = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <int DT, bool AL>
+__device__ __forceinline__ void store_vector(typename Elem<DT>::T* p, const uint4& v, int n) {
+  constexpr int W = Elem<DT>::W;
+  if constexpr (AL) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else {
+    float f[W];
+    Elem<DT>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) p[i] = Elem<DT>::put(f[i]);
+  }
+}
+
+// Sums of a and b over the `warps` (1, 2, 4, 8 or 16) warps of a group (named barrier `id`),
+// the same bits in every thread.  After one exchange the lower half of each warp sums a
+// and the upper half b, so that both take little more than the shuffles of one; the warps
+// meet in sm[2][16].
+__device__ __forceinline__ void group_sums(float& a, float& b, float* sm, int warp, int warps, int id) {
+  const int lane = threadIdx.x & 31;
+  const bool upper = lane >= 16;
+  float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (warps > 1) {
+    float* const half = sm + (lane & 16);
+    if ((lane & 15) == 0) half[warp] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
+    v = half[lane & (warps - 1)];
+    for (int off = warps / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  }
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// The parameters of the row's columns as a CTA keeps them: in fp32, so that a row need not
+// convert them again, as W / 4 arrays of `units` float4s (the first four columns of every
+// vector, then the others), so that neighbouring threads read neighbouring vectors.
+template <int PT, int W, bool AL>
+__device__ __forceinline__ void keep_params(float4* kept, const typename Elem<PT>::T* src, float none, int D) {
+  const int units = (D + W - 1) / W;
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    F2 v[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) v[i] = f2(none);
+    if (src != nullptr) load_params<PT, W, AL>(src + u * W, min(D - u * W, W), 0.f, v);
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) kept[i * units + u] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+  }
+}
+
+constexpr int kPipeSMs = 152;     // SMs that the persistent grids are made for
+constexpr int kPipeUnits = 1024;  // vectors of the widest row of the one-pass kernels
+
+// Contiguous ranges of rows for `all` takers.
+struct RowRanges {
+  int base, extra;  // rows of each; the first `extra` have one more
 };
-
-// NaN payloads may change in an unaligned load_raw; nothing else.
-
-// Waits for the LANES threads of a row (a whole number of warps) that share the
-// named barrier `id`.
-template <int LANES>
-__device__ __forceinline__ void row_barrier(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(LANES) : "memory");
+inline RowRanges row_ranges(int N, long long all) {
+  return {static_cast<int>(N / all), static_cast<int>(N % all)};
+}
+__device__ __forceinline__ void row_range(const RowRanges& r, int q, unsigned& r0, unsigned& r1) {
+  r0 = static_cast<unsigned>(q) * r.base + min(q, r.extra);
+  r1 = r0 + r.base + (q < r.extra ? 1 : 0);
 }
 
-// Sums of M values over the LANES threads of a row, the same bits in each of them:
-// butterflies within the warp, then the warps in ascending order through `sm`
-// (LANES / 32 * M floats, not used again before the next row_barrier of the row).
-template <int LANES, int M>
-__device__ __forceinline__ void row_sum(float (&v)[M], float* sm, int id) {
-#pragma unroll
-  for (int off = (LANES < 32 ? LANES : 32) / 2; off >= 1; off >>= 1)
-#pragma unroll
-    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], off);
-  if constexpr (LANES > 32) {
-    constexpr int WARPS = LANES / 32;
-    const int w = (threadIdx.x % LANES) >> 5;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int m = 0; m < M; ++m) sm[w * M + m] = v[m];
-    }
-    row_barrier<LANES>(id);
-#pragma unroll
-    for (int m = 0; m < M; ++m) v[m] = 0.f;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i)
-#pragma unroll
-      for (int m = 0; m < M; ++m) v[m] += sm[i * M + m];
-  }
-}
-
-// Sum over a CTA of THREADS threads, in the same order.
+// Fixed-order sum over a CTA of THREADS threads: butterflies, then the warps in ascending order.
 template <int THREADS>
 __device__ __forceinline__ float cta_sum(float v, float* sm) {
-  float a[1] = {v};
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   __syncthreads();
-  row_sum<THREADS, 1>(a, sm, 0);
-  return a[0];
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = sm[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v += sm[w];
+  return v;
 }
 
 }  // namespace llp

@@ -3,162 +3,180 @@
 //   grad_x      = rstd * (a - sum a / D - h * (sum a h) / D)
 //   grad_weight = sum over rows of grad_y * h,   grad_bias = sum over rows of grad_y
 //
-// One pass over grad_y and x gives all three: LANES threads own a row at a time,
-// hold it in registers while the two row sums are joined, and write grad_x; the
-// columns a thread owns are the same for every row, so it keeps their share of
-// the two column sums in registers too.  The next row's loads are in flight
-// meanwhile.  The grid is fixed by the sizes; every group of LANES threads takes
-// the rows group, group + groups, ...; a second launch joins the CTAs' column
-// sums in ascending order.  Rows beyond the register layouts take three kernels.
+// One pass over grad_y and x gives all three.  A group of warps owns a row at a time,
+// up to three vectors per thread: it holds the row in registers while its two sums
+// are joined, writes grad_x, and as a thread's columns are the same in every row it
+// keeps their share of the column sums in registers too.  Few threads with several
+// vectors each, because the instructions of the sums (shuffles, a barrier, the
+// exchange between the warps) weigh as much as those of a vector and the issue of
+// instructions is what bounds this kernel next to memory.  Each thread copies the
+// vectors it will use itself, with cp.async into its own slots of a ring of rows, so
+// that nothing but the sums makes threads wait for one another and the rows to come
+// are in flight whatever the registers hold.  A second launch joins the CTAs' column
+// sums in ascending order.  Rows beyond 1024 vectors take three plain kernels.
 #include "layer_norm.cuh"
 
 namespace llp {
 
 namespace {
 
-constexpr int kMaxParts = 608;  // partial column sums: CTAs of the row pass (4 per SM)
+constexpr int kBwdWarps = 16;  // of a CTA, one per SM: 128 registers per thread
+constexpr int kBwdStages = 4;  // rows of the ring
 
 // part: [gridDim.x][2][D], the CTA's column sums of grad_y * h and of grad_y; null to skip them.
-template <int DT, int PT, int W, int LANES, int K>
-__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) layer_norm_bwd_kernel(
-    LayerNormParams p, bool al, const float* __restrict__ mean, const float* __restrict__ rstd,
+// K = ceil(units / (32 * warps)): only a thread's last vector may lie past the row's end.
+template <int DT, int PT, int K, bool AL>
+__global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
+    LayerNormParams p, int warps, RowRanges ranges, const float* __restrict__ mean, const float* __restrict__ rstd,
     typename Elem<DT>::T* __restrict__ gx, float* __restrict__ part) {
-  using U = RowUnit<DT, W>;
-  using P = RowUnit<PT, W>;
-  constexpr int THREADS = LANES < 256 ? 256 : LANES;
-  constexpr int GROUPS = THREADS / LANES;
-  __shared__ float sm[2][GROUPS * (LANES / 32) * 2];
+  using T = typename Elem<DT>::T;
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = kBwdStages;
+  extern __shared__ uint4 ring[];  // [STAGES][2][K][threads]: grad_y and x; then the weight
+  __shared__ float red[2][kBwdWarps][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const int units = p.D / W;
-  const typename U::T* xb = static_cast<const typename U::T*>(p.x);
-  const typename U::T* gb = static_cast<const typename U::T*>(p.gy);
-  const typename P::T* wb = static_cast<const typename P::T*>(p.weight);
-  const long long step = static_cast<long long>(gridDim.x) * GROUPS;
-  const float inv = 1.f / static_cast<float>(p.D);
-
-  float wv[K][W], aw[K][W], ab[K][W];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int u = lane + k * LANES;
-#pragma unroll
-    for (int i = 0; i < W; ++i) wv[k][i] = 1.f, aw[k][i] = ab[k][i] = 0.f;
-    if (wb != nullptr && u < units) P::load(wb + u * W, al, wv[k]);
-  }
-  typename U::Raw xr[K], gr[K];
-  float m = 0.f, r = 0.f;
-  auto fetch = [&](long long n) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int u = lane + k * LANES;
-      const bool on = n < p.N && u < units;
-      gr[k] = on ? U::load_raw(gb + n * p.gy_stride + static_cast<size_t>(u) * W, al) : U::zero();
-      xr[k] = on ? U::load_raw(xb + n * p.x_stride + static_cast<size_t>(u) * W, al) : U::zero();
-    }
-    if (n < p.N) m = __ldg(mean + n), r = __ldg(rstd + n);
-  };
-  long long n = static_cast<long long>(blockIdx.x) * GROUPS + group;
-  fetch(n);
-  for (int odd = 0; n < p.N; n += step, odd ^= 1) {
-    typename U::Raw xc[K], gc[K];
-    const float mc = m, rc = r;
-#pragma unroll
-    for (int k = 0; k < K; ++k) xc[k] = xr[k], gc[k] = gr[k];
-    fetch(n + step);
-    float s[2] = {0.f, 0.f};
-    float h[K][W], a[K][W];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const bool on = lane + k * LANES < units;
-      U::unpack(xc[k], h[k]);
-      U::unpack(gc[k], a[k]);
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        h[k][i] = on ? (h[k][i] - mc) * rc : 0.f;
-        aw[k][i] = fmaf(a[k][i], h[k][i], aw[k][i]);
-        ab[k][i] += a[k][i];
-        a[k][i] *= wv[k][i];
-        s[0] += a[k][i];
-        s[1] = fmaf(a[k][i], h[k][i], s[1]);
-      }
-    }
-    row_sum<LANES, 2>(s, sm[odd] + group * (LANES / 32) * 2, 1 + group);
-    if (gx != nullptr) {
-      const float s0 = s[0] * inv, s1 = s[1] * inv;
-      typename U::T* out = gx + static_cast<size_t>(n) * p.D;
+  const int threads = blockDim.x, lane = threadIdx.x & 31;
+  const int group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
+  const int groups = (threads >> 5) / warps;
+  const int units = (p.D + W - 1) / W;
+  const int first = 32 * warp + lane, width = 32 * warps;  // this thread's vectors: first + k * width
+  const int last = first + (K - 1) * width;
+  const bool tail = last < units;
+  const int tail_n = min(p.D - last * W, W);  // elements of the last vector
+  unsigned r0, r1;
+  row_range(ranges, blockIdx.x * groups + group, r0, r1);
+  const T* gsrc = static_cast<const T*>(p.gy) + static_cast<long long>(r0) * p.gy_stride + first * W;
+  const T* xsrc = static_cast<const T*>(p.x) + static_cast<long long>(r0) * p.x_stride + first * W;
+  uint4* const mine = ring + threadIdx.x;
+  const int pitch = 2 * K * threads;  // of a stage
+  // what no copy writes stays 0: grad_y past the row's end adds nothing to any sum
+  if (!AL || !tail)
+    for (int i = 0; i < 2 * STAGES; ++i) mine[(i * K + K - 1) * threads] = make_uint4(0, 0, 0, 0);
+  unsigned next = r0;
+  auto issue = [&](uint4* slot) {  // the next row, if there is one
+    if (next < r1) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = lane + k * LANES;
-        if (u < units) {
+        if (k < K - 1 || tail) {
+          copy_vector<DT, AL>(slot + k * threads, gsrc + k * width * W, k < K - 1 ? W : tail_n);
+          copy_vector<DT, AL>(slot + (K + k) * threads, xsrc + k * width * W, k < K - 1 ? W : tail_n);
+        }
+      }
+      gsrc += p.gy_stride;
+      xsrc += p.x_stride;
+      ++next;
+    }
+    copy_commit();
+  };
 #pragma unroll
-          for (int i = 0; i < W; ++i) a[k][i] = (fmaf(-h[k][i], s1, a[k][i]) - s0) * rc;
-          U::store(out + static_cast<size_t>(u) * W, al, a[k]);
+  for (int s = 0; s < STAGES - 1; ++s) issue(mine + s * pitch);
+  float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
+  keep_params<PT, W, AL>(kept, static_cast<const typename Elem<PT>::T*>(p.weight), 1.f, p.D);
+  // lane l holds the statistics of row 32 b + l of the group's range, and of the next 32
+  auto stats = [&](const float* s, unsigned i) { return r0 + i + lane < r1 ? __ldg(s + r0 + i + lane) : 0.f; };
+  float m_next = stats(mean, 0), s_next = stats(rstd, 0), m_lane = 0.f, s_lane = 0.f;
+  F2 aw[K][H], ab[K][H];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < H; ++i) aw[k][i] = ab[k][i] = f2(0.f);
+  const float inv = 1.f / static_cast<float>(p.D);
+  T* out = gx == nullptr ? nullptr : gx + static_cast<size_t>(r0) * p.D + first * W;
+  __syncthreads();  // the weight is kept
+  int stage = 0;
+  for (unsigned n = r0; n < r1; ++n) {
+    const unsigned i0 = (n - r0) & 31;
+    if (i0 == 0) {
+      m_lane = m_next, s_lane = s_next;
+      m_next = stats(mean, n - r0 + 32), s_next = stats(rstd, n - r0 + 32);
+    }
+    const float sc = __shfl_sync(0xffffffffu, s_lane, i0);
+    // h = x * rstd - mean * rstd in one step: its error stays below that of a rounding of mean
+    const float ms = -__shfl_sync(0xffffffffu, m_lane, i0) * sc;
+    copy_wait<STAGES - 2>();
+    const uint4* const slot = mine + stage * pitch;
+    F2 a[K][H], h[K][H], t0 = f2(0.f), t1 = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      unpack2<DT, W>(slot[k * threads], a[k]);
+      unpack2<DT, W>(slot[(K + k) * threads], h[k]);
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const float4 w = k < K - 1 || tail ? kept[q * units + first + k * width] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+          h[k][i] = fma2(h[k][i], f2(sc), f2(ms));
+          ab[k][i] = add2(ab[k][i], a[k][i]);
+          aw[k][i] = fma2(a[k][i], h[k][i], aw[k][i]);
+          a[k][i] = mul2(a[k][i], i == 2 * q ? f2(w.x, w.y) : f2(w.z, w.w));
+          t0 = add2(t0, a[k][i]);
+          t1 = fma2(a[k][i], h[k][i], t1);
         }
       }
     }
+    issue(mine + (stage == 0 ? STAGES - 1 : stage - 1) * pitch);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    float s0 = sum2(t0), s1 = sum2(t1);
+    group_sums(s0, s1, red[n & 1][group], warp, warps, 1 + group);
+    if (out != nullptr) {
+      // rstd * (a - s0 / D - h * s1 / D)
+      const float c0 = -s0 * inv * sc, c1 = -s1 * inv * sc;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k < K - 1 || tail) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) a[k][i] = fma2(a[k][i], f2(sc), fma2(h[k][i], f2(c1), f2(c0)));
+          store_vector<DT, AL>(out + k * width * W, pack2<DT, W>(a[k]), k < K - 1 ? W : tail_n);
+        }
+      }
+      out += p.D;
+    }
   }
   if (part == nullptr) return;
-  if constexpr (GROUPS > 1) {  // the CTA's groups in ascending order
-    __shared__ float join[2 * LANES * K * W];
-    for (int g = 1; g < GROUPS; ++g) {
-      __syncthreads();
-      if (group == g) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            join[(k * W + i) * LANES + lane] = aw[k][i];
-            join[((K + k) * W + i) * LANES + lane] = ab[k][i];
-          }
-      }
-      __syncthreads();
-      if (group == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            aw[k][i] += join[(k * W + i) * LANES + lane];
-            ab[k][i] += join[((K + k) * W + i) * LANES + lane];
-          }
-      }
-    }
-    if (group != 0) return;
-  }
-  float* pw = part + static_cast<size_t>(blockIdx.x) * 2 * p.D;
+  copy_wait<0>();
+  __syncthreads();
+  // the CTA's column sums: its groups in ascending order, through the ring's memory
+  float* const join = reinterpret_cast<float*>(ring);  // [groups][2][units * W]
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = lane + k * LANES;
-    if (u < units) {
+    if (k < K - 1 || tail) {
+      F2* const o = reinterpret_cast<F2*>(join + (group * 2 * units + first + k * width) * W);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        pw[static_cast<size_t>(u) * W + i] = aw[k][i];
-        pw[p.D + static_cast<size_t>(u) * W + i] = ab[k][i];
-      }
+      for (int i = 0; i < H; ++i) o[i] = aw[k][i], o[units * H + i] = ab[k][i];
     }
+  }
+  __syncthreads();
+  float* const sum = part + static_cast<size_t>(blockIdx.x) * 2 * p.D;
+  for (int c = threadIdx.x; c < 2 * p.D; c += threads) {
+    const int at = c < p.D ? c : units * W + c - p.D;
+    float s = join[at];
+    for (int g = 1; g < groups; ++g) s += join[g * 2 * units * W + at];
+    sum[c] = s;
   }
 }
 
-// 32 of the 2 D column sums per CTA; warp w adds the parts w, w + 8, ..., then the warps
+// 32 of the 2 D column sums per CTA; warp w adds the parts w, w + 32, ..., then the warps
 // are joined in ascending order.
+constexpr int kJoinWarps = 32;
+
 template <int PT>
-__global__ void __launch_bounds__(256) layer_norm_join_kernel(const float* __restrict__ part, int parts, int D,
+__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ part, int parts, int D,
                                                               typename Elem<PT>::T* __restrict__ gw,
                                                               typename Elem<PT>::T* __restrict__ gb) {
-  __shared__ float sm[8][32];
+  __shared__ float sm[kJoinWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < 2 * D) {
 #pragma unroll 8
-    for (int i = warp; i < parts; i += 8) s += __ldcg(part + static_cast<size_t>(i) * 2 * D + c);
+    for (int i = warp; i < parts; i += kJoinWarps) s += __ldcg(part + static_cast<size_t>(i) * 2 * D + c);
   }
   sm[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= 2 * D) return;
   s = sm[0][lane];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) s += sm[w][lane];
+  for (int w = 1; w < kJoinWarps; ++w) s += sm[w][lane];
   if (c < D) {
     if (gw != nullptr) gw[c] = Elem<PT>::put(s);
   } else {
@@ -240,7 +258,7 @@ cudaError_t join(const LayerNormParams& p, const Grads& o, int parts, cudaStream
   using T = typename Elem<PT>::T;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((2 * p.D + 31) / 32);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -251,16 +269,18 @@ cudaError_t join(const LayerNormParams& p, const Grads& o, int parts, cudaStream
                                       static_cast<T*>(o.gw), static_cast<T*>(o.gb)));
 }
 
-template <int DT, int PT, int W, int LANES, int K>
-cudaError_t rows(const LayerNormParams& p, bool al, const Grads& o, cudaStream_t s) {
-  constexpr int THREADS = LANES < 256 ? 256 : LANES;
-  constexpr int GROUPS = THREADS / LANES;
-  constexpr int PER_SM = THREADS <= 256 ? 4 : THREADS <= 512 ? 2 : 1;
+template <int DT, int PT, int K>
+cudaError_t rows(const LayerNormParams& p, int warps, bool al, const Grads& o, cudaStream_t s) {
+  const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
+  int groups = kBwdWarps / warps;
+  const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
+  const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
+  const int threads = 32 * warps * groups;
+  const size_t smem = (static_cast<size_t>(kBwdStages) * 2 * K * threads + units * (Elem<DT>::W / 4)) * 16;
   const bool params = o.gw != nullptr || o.gb != nullptr;
-  const long long want = (static_cast<long long>(p.N) + GROUPS - 1) / GROUPS;
-  const int grid = static_cast<int>(want < 152 * PER_SM ? want : 152 * PER_SM);
-  layer_norm_bwd_kernel<DT, PT, W, LANES, K><<<grid, THREADS, 0, s>>>(
-      p, al, o.mean, o.rstd, static_cast<typename Elem<DT>::T*>(o.gx), params ? o.part : nullptr);
+  const auto kernel = al ? layer_norm_bwd_kernel<DT, PT, K, true> : layer_norm_bwd_kernel<DT, PT, K, false>;
+  kernel<<<grid, threads, smem, s>>>(p, warps, row_ranges(p.N, static_cast<long long>(grid) * groups), o.mean, o.rstd,
+                                     static_cast<typename Elem<DT>::T*>(o.gx), params ? o.part : nullptr);
   const cudaError_t e = launch_result();
   return e != cudaSuccess || !params ? e : join<PT>(p, o, grid, s);
 }
@@ -283,30 +303,51 @@ cudaError_t wide(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
 template <int DT, int PT>
 cudaError_t run(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
   constexpr int W = Elem<DT>::W;
-  const bool al = aligned16(p.x) && (p.x_stride * elem_bytes(DT)) % 16 == 0 && aligned16(p.gy) &&
+  const bool al = p.D % W == 0 && aligned16(p.x) && (p.x_stride * elem_bytes(DT)) % 16 == 0 && aligned16(p.gy) &&
                   (p.gy_stride * elem_bytes(DT)) % 16 == 0 && aligned16(o.gx) && aligned16(p.weight);
-  if (p.D % W == 0) {
-    const int units = p.D / W;
-    if (units <= 32) return rows<DT, PT, W, 32, 1>(p, al, o, s);
-    if (units <= 128) return rows<DT, PT, W, 128, 1>(p, al, o, s);
-    if (units <= 256) return rows<DT, PT, W, 256, 1>(p, al, o, s);
-    if (units <= 384) return rows<DT, PT, W, 384, 1>(p, al, o, s);
-    if (units <= 512) return rows<DT, PT, W, 512, 1>(p, al, o, s);
-    if (units <= 768) return rows<DT, PT, W, 384, 2>(p, al, o, s);
-    if (units <= 1024) return rows<DT, PT, W, 512, 2>(p, al, o, s);
-    if (units <= 2048) return rows<DT, PT, W, 1024, 2>(p, al, o, s);
-  } else {
-    if (p.D <= 256) return rows<DT, PT, 1, 32, 8>(p, al, o, s);
-    if (p.D <= 1024) return rows<DT, PT, 1, 256, 4>(p, al, o, s);
-    if (p.D <= 4096) return rows<DT, PT, 1, 512, 8>(p, al, o, s);
+  const int units = (p.D + W - 1) / W;
+  if (units <= kPipeUnits) {
+    int warps = 1;
+    while (96 * warps < units) warps *= 2;
+    const int K = (units + 32 * warps - 1) / (32 * warps);
+    if (K == 1) return rows<DT, PT, 1>(p, warps, al, o, s);
+    if (K == 2) return rows<DT, PT, 2>(p, warps, al, o, s);
+    return rows<DT, PT, 3>(p, warps, al, o, s);
   }
   return wide<DT, PT>(p, o, s);
 }
 
+template <int DT, int PT, int K>
+cudaError_t allow() {
+  const int bytes = 226 * 1024;  // K = 3: 192 KB of the ring, 24 KB of the weight
+  const cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, true>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes - 4096));
+  return e != cudaSuccess ? e
+                          : note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes - 4096));
+}
+
+template <int DT, int PT>
+cudaError_t setup() {
+  cudaError_t e = allow<DT, PT, 1>();
+  if (e == cudaSuccess) e = allow<DT, PT, 2>();
+  if (e == cudaSuccess) e = allow<DT, PT, 3>();
+  return e;
+}
+
 }  // namespace
 
+cudaError_t layer_norm_bwd_setup() {
+  cudaError_t e = setup<kDtypeF32, kDtypeF32>();
+  if (e == cudaSuccess) e = setup<kDtypeBF16, kDtypeF32>();
+  if (e == cudaSuccess) e = setup<kDtypeBF16, kDtypeBF16>();
+  if (e == cudaSuccess) e = setup<kDtypeF16, kDtypeF32>();
+  if (e == cudaSuccess) e = setup<kDtypeF16, kDtypeF16>();
+  return e;
+}
+
 size_t layer_norm_bwd_workspace(long long N, long long D) {
-  const long long parts = N < kMaxParts ? N : kMaxParts;
+  const long long parts = N < kPipeSMs ? N : kPipeSMs;
   return static_cast<size_t>(parts) * 2 * D * sizeof(float);
 }
 

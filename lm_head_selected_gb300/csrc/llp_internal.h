@@ -296,6 +296,8 @@ struct LayerNormParams {
   float eps;
 };
 cudaError_t launch_layer_norm_fwd(const LayerNormParams& p, void* y, float* mean, float* rstd, cudaStream_t s);
+cudaError_t layer_norm_fwd_setup();
+cudaError_t layer_norm_bwd_setup();
 size_t layer_norm_bwd_workspace(long long N, long long D);
 cudaError_t launch_layer_norm_bwd(const LayerNormParams& p, const float* mean, const float* rstd, void* gx, void* gw,
                                   void* gb, void* workspace, cudaStream_t s);
