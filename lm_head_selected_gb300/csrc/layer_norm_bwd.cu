@@ -9,32 +9,44 @@
 // keeps their share of the column sums in registers too.  Few threads with several
 // vectors each, because the instructions of the sums (shuffles, a barrier, the
 // exchange between the warps) weigh as much as those of a vector and the issue of
-// instructions is what bounds this kernel next to memory.  Each thread copies the
-// vectors it will use itself, with cp.async into its own slots of a ring of rows, so
-// that nothing but the sums makes threads wait for one another and the rows to come
-// are in flight whatever the registers hold.  A second launch joins the CTAs' column
-// sums in ascending order.  Rows beyond 1024 vectors take three plain kernels.
+// instructions is what bounds this kernel next to memory: at 65600 rows of 2688 bf16
+// one vector per thread takes 256 us (80 registers, two rows at once), two 213, three
+// 171.  Each thread copies the vectors it will use itself, with cp.async into its own
+// slots of a ring of rows, so that nothing but the sums makes threads wait for one
+// another and the rows to come are in flight whatever the registers hold.  Group q of
+// G takes the rows q, q + G, ...: the rows under way at one time are neighbours
+// (contiguous ranges instead: 190 us).  A second launch joins the CTAs' column sums in
+// ascending order.  Rows beyond 1024 vectors take three plain kernels.
+//
+// Measured, bf16, three tensors of traffic: 16384 x 4096 68 us (5.9 TB/s, 87% of the
+// measured copy peak), 65600 x 2688 171 us (91%), 16384 x 2688 51 us (76%: 5 us are the
+// join and the two launches' ends).
 #include "layer_norm.cuh"
 
 namespace llp {
 
 namespace {
 
-constexpr int kBwdWarps = 16;  // of a CTA, one per SM: 128 registers per thread
-constexpr int kBwdStages = 4;  // rows of the ring
+constexpr int kBwdThreads = 512;  // of a CTA, one per SM: 128 registers per thread
+template <bool AL>
+struct BwdRing {
+  static constexpr int STAGES = AL ? 4 : 3;  // rows
+};
 
 // part: [gridDim.x][2][D], the CTA's column sums of grad_y * h and of grad_y; null to skip them.
 // K = ceil(units / (32 * warps)): only a thread's last vector may lie past the row's end.
 template <int DT, int PT, int K, bool AL>
-__global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
-    LayerNormParams p, int warps, RowRanges ranges, const float* __restrict__ mean, const float* __restrict__ rstd,
+__global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
+    LayerNormParams p, int warps, const float* __restrict__ mean, const float* __restrict__ rstd,
     typename Elem<DT>::T* __restrict__ gx, float* __restrict__ part) {
   using T = typename Elem<DT>::T;
-  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = kBwdStages;
-  extern __shared__ uint4 ring[];  // [STAGES][2][K][threads]: grad_y and x; then the weight
-  __shared__ float red[2][kBwdWarps][32];
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = BwdRing<AL>::STAGES;
+  using S = Slot<DT, AL>;
+  extern __shared__ uint4 ring[];  // [STAGES][2][K][threads]: grad_y and x; then the weight; then the slots' fifth words
+  __shared__ float red[2][kBwdThreads / 32][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int threads = blockDim.x, lane = threadIdx.x & 31;
+  constexpr int threads = kBwdThreads;
+  const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
   const int groups = (threads >> 5) / warps;
   const int units = (p.D + W - 1) / W;
@@ -42,38 +54,42 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
   const int last = first + (K - 1) * width;
   const bool tail = last < units;
   const int tail_n = min(p.D - last * W, W);  // elements of the last vector
-  unsigned r0, r1;
-  row_range(ranges, blockIdx.x * groups + group, r0, r1);
+  // this group's rows: r0, r0 + step, ...
+  const unsigned step = gridDim.x * groups, r0 = blockIdx.x * groups + group, r1 = p.N;
   const T* gsrc = static_cast<const T*>(p.gy) + static_cast<long long>(r0) * p.gy_stride + first * W;
   const T* xsrc = static_cast<const T*>(p.x) + static_cast<long long>(r0) * p.x_stride + first * W;
+  const T* const glo = static_cast<const T*>(p.gy);
+  const T* const xlo = static_cast<const T*>(p.x);
+  const T* const ghi = glo + static_cast<long long>(p.N - 1) * p.gy_stride + p.D;
+  const T* const xhi = xlo + static_cast<long long>(p.N - 1) * p.x_stride + p.D;
   uint4* const mine = ring + threadIdx.x;
-  const int pitch = 2 * K * threads;  // of a stage
+  constexpr int pitch = 2 * K * threads;  // of a stage
+  float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
+  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + W / 4 * units) + threadIdx.x;
   // what no copy writes stays 0: grad_y past the row's end adds nothing to any sum
   if (!AL || !tail)
     for (int i = 0; i < 2 * STAGES; ++i) mine[(i * K + K - 1) * threads] = make_uint4(0, 0, 0, 0);
-  unsigned next = r0;
-  auto issue = [&](uint4* slot) {  // the next row, if there is one
-    if (next < r1) {
+  auto issue = [&](unsigned n, int stage) {  // row n, the next one, if there is one
+    if (n < r1) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (k < K - 1 || tail) {
-          copy_vector<DT, AL>(slot + k * threads, gsrc + k * width * W, k < K - 1 ? W : tail_n);
-          copy_vector<DT, AL>(slot + (K + k) * threads, xsrc + k * width * W, k < K - 1 ? W : tail_n);
+          const int g = stage * pitch + k * threads, x = g + K * threads, n = k < K - 1 ? W : tail_n;
+          S::copy(mine + g, fifth + g, gsrc + k * width * W, n, glo, ghi);
+          S::copy(mine + x, fifth + x, xsrc + k * width * W, n, xlo, xhi);
         }
       }
-      gsrc += p.gy_stride;
-      xsrc += p.x_stride;
-      ++next;
+      gsrc += step * p.gy_stride;
+      xsrc += step * p.x_stride;
     }
     copy_commit();
   };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(mine + s * pitch);
-  float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
+  for (int s = 0; s < STAGES - 1; ++s) issue(r0 + s * step, s);
   keep_params<PT, W, AL>(kept, static_cast<const typename Elem<PT>::T*>(p.weight), 1.f, p.D);
-  // lane l holds the statistics of row 32 b + l of the group's range, and of the next 32
-  auto stats = [&](const float* s, unsigned i) { return r0 + i + lane < r1 ? __ldg(s + r0 + i + lane) : 0.f; };
-  float m_next = stats(mean, 0), s_next = stats(rstd, 0), m_lane = 0.f, s_lane = 0.f;
+  // lane l holds the statistics of the group's row 32 b + l, and of the next 32
+  auto stats = [&](const float* s, unsigned n) { return n + lane * step < r1 ? __ldg(s + n + lane * step) : 0.f; };
+  float m_next = stats(mean, r0), s_next = stats(rstd, r0), m_lane = 0.f, s_lane = 0.f;
   F2 aw[K][H], ab[K][H];
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -83,22 +99,25 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
   T* out = gx == nullptr ? nullptr : gx + static_cast<size_t>(r0) * p.D + first * W;
   __syncthreads();  // the weight is kept
   int stage = 0;
-  for (unsigned n = r0; n < r1; ++n) {
-    const unsigned i0 = (n - r0) & 31;
+  unsigned i = 0;  // rows taken
+  for (unsigned n = r0; n < r1; n += step, ++i) {
+    const unsigned i0 = i & 31;
     if (i0 == 0) {
       m_lane = m_next, s_lane = s_next;
-      m_next = stats(mean, n - r0 + 32), s_next = stats(rstd, n - r0 + 32);
+      m_next = stats(mean, n + 32 * step), s_next = stats(rstd, n + 32 * step);
     }
     const float sc = __shfl_sync(0xffffffffu, s_lane, i0);
     // h = x * rstd - mean * rstd in one step: its error stays below that of a rounding of mean
     const float ms = -__shfl_sync(0xffffffffu, m_lane, i0) * sc;
     copy_wait<STAGES - 2>();
-    const uint4* const slot = mine + stage * pitch;
+    const bool gshift = S::shifted(glo + static_cast<long long>(n) * p.gy_stride);
+    const bool xshift = S::shifted(xlo + static_cast<long long>(n) * p.x_stride);
     F2 a[K][H], h[K][H], t0 = f2(0.f), t1 = f2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack2<DT, W>(slot[k * threads], a[k]);
-      unpack2<DT, W>(slot[(K + k) * threads], h[k]);
+      const int g = stage * pitch + k * threads, x = g + K * threads, left = k < K - 1 ? W : tail_n;
+      unpack2<DT, W>(S::read(mine + g, fifth + g, gshift, left), a[k]);
+      unpack2<DT, W>(S::read(mine + x, fifth + x, xshift, left), h[k]);
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
         const float4 w = k < K - 1 || tail ? kept[q * units + first + k * width] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -113,10 +132,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
         }
       }
     }
-    issue(mine + (stage == 0 ? STAGES - 1 : stage - 1) * pitch);
+    issue(n + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     float s0 = sum2(t0), s1 = sum2(t1);
-    group_sums(s0, s1, red[n & 1][group], warp, warps, 1 + group);
+    group_sums(s0, s1, red[i & 1][group], warp, warps, 1 + group);
     if (out != nullptr) {
       // rstd * (a - s0 / D - h * s1 / D)
       const float c0 = -s0 * inv * sc, c1 = -s1 * inv * sc;
@@ -125,10 +144,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) layer_norm_bwd_kernel(
         if (k < K - 1 || tail) {
 #pragma unroll
           for (int i = 0; i < H; ++i) a[k][i] = fma2(a[k][i], f2(sc), fma2(h[k][i], f2(c1), f2(c0)));
-          store_vector<DT, AL>(out + k * width * W, pack2<DT, W>(a[k]), k < K - 1 ? W : tail_n);
+          S::store(out + k * width * W, pack2<DT, W>(a[k]), k < K - 1 ? W : tail_n);
         }
       }
-      out += p.D;
+      out += static_cast<size_t>(step) * p.D;
     }
   }
   if (part == nullptr) return;
@@ -272,15 +291,15 @@ cudaError_t join(const LayerNormParams& p, const Grads& o, int parts, cudaStream
 template <int DT, int PT, int K>
 cudaError_t rows(const LayerNormParams& p, int warps, bool al, const Grads& o, cudaStream_t s) {
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
-  int groups = kBwdWarps / warps;
+  const int groups = kBwdThreads / 32 / warps;  // warps is 1, 2, 4, 8 or 16
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
-  const int threads = 32 * warps * groups;
-  const size_t smem = (static_cast<size_t>(kBwdStages) * 2 * K * threads + units * (Elem<DT>::W / 4)) * 16;
+  const size_t slots = static_cast<size_t>(al ? BwdRing<true>::STAGES : BwdRing<false>::STAGES) * 2 * K * kBwdThreads;
+  const size_t smem = slots * (al ? 16 : Slot<DT, false>::BYTES) + static_cast<size_t>(units) * (Elem<DT>::W / 4) * 16;
   const bool params = o.gw != nullptr || o.gb != nullptr;
   const auto kernel = al ? layer_norm_bwd_kernel<DT, PT, K, true> : layer_norm_bwd_kernel<DT, PT, K, false>;
-  kernel<<<grid, threads, smem, s>>>(p, warps, row_ranges(p.N, static_cast<long long>(grid) * groups), o.mean, o.rstd,
-                                     static_cast<typename Elem<DT>::T*>(o.gx), params ? o.part : nullptr);
+  kernel<<<grid, kBwdThreads, smem, s>>>(p, warps, o.mean, o.rstd, static_cast<typename Elem<DT>::T*>(o.gx),
+                                         params ? o.part : nullptr);
   const cudaError_t e = launch_result();
   return e != cudaSuccess || !params ? e : join<PT>(p, o, grid, s);
 }
@@ -307,8 +326,10 @@ cudaError_t run(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
                   (p.gy_stride * elem_bytes(DT)) % 16 == 0 && aligned16(o.gx) && aligned16(p.weight);
   const int units = (p.D + W - 1) / W;
   if (units <= kPipeUnits) {
+    // three vectors per thread, two where ragged rows need registers of their own
+    const int most = p.D % W == 0 ? 96 : 64;
     int warps = 1;
-    while (96 * warps < units) warps *= 2;
+    while (most * warps < units) warps *= 2;
     const int K = (units + 32 * warps - 1) / (32 * warps);
     if (K == 1) return rows<DT, PT, 1>(p, warps, al, o, s);
     if (K == 2) return rows<DT, PT, 2>(p, warps, al, o, s);
@@ -319,12 +340,12 @@ cudaError_t run(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
 
 template <int DT, int PT, int K>
 cudaError_t allow() {
-  const int bytes = 226 * 1024;  // K = 3: 192 KB of the ring, 24 KB of the weight
+  const int bytes = 222 * 1024;  // K = 3: 192 KB of the ring, 24 KB of the weight
   const cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes - 4096));
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   return e != cudaSuccess ? e
                           : note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes - 4096));
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
 }
 
 template <int DT, int PT>

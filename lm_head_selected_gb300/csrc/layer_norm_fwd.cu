@@ -1,15 +1,18 @@
 // Layer norm over the last dimension: y = (x - mean) * rstd * weight + bias.
 //
-// A warp owns a row (a quarter of a warp a very short one, up to four warps a wide
-// one) and reads it once: the row stays in registers while its mean and then its
-// centred second moment are summed, two reductions without cancellation.  Up to 11
-// vectors per lane keep the reductions' instructions few against the row's own, and a
-// row that one warp owns needs no barrier.  Each lane copies its vectors of the next
-// row with cp.async into its own slots of shared memory meanwhile; the parameters lie
-// there too, in fp32.  With a row spread over six warps, two vectors per lane, the
-// exchange between the warps set the pace: 36.4 us against %FWD% at 16384 rows of
-// 2688.  Rows beyond 1024 vectors are read three times by one CTA each (from L2 after
-// the first).
+// A group of warps owns a row at a time, up to three vectors per thread, and reads it
+// once: the row stays in registers while its mean and then its centred second moment
+// are summed, two reductions without cancellation.  The rows to come are in flight
+// meanwhile: each thread copies the vectors it will use itself, with cp.async into its
+// own slots of a ring of rows; the parameters lie in shared memory too, in fp32.  Group
+// q of G takes the rows q, q + G, ...: the rows under way at one time are neighbours.
+// Rows beyond 1024 vectors are read three times by one CTA each (from L2 after the
+// first).
+//
+// Bound by memory, both ways.  Measured, bf16: 16384 x 2688 30.2 us (5.8 TB/s, 86% of
+// the measured copy peak; an elementwise kernel of the same traffic takes 30.0), 65600 x
+// 2688 112 us (93%).  One vector per thread, with six warps to a row, took 36.4 us, one
+// warp to a row with eleven 32.6, contiguous ranges of rows 31.1 and 121.
 #include "layer_norm.cuh"
 
 namespace llp {
@@ -18,114 +21,114 @@ namespace {
 
 template <int K>
 struct FwdShape {
-  static constexpr int WARPS = K <= 4 ? 32 : K <= 6 ? 24 : 16;  // of a CTA, one per SM: 64, 80 or 128 registers
+  static constexpr int THREADS = K <= 2 ? 1024 : 768;  // of a CTA, one per SM: 64 or 80 registers
 };
+constexpr int kFwdStages = 3;  // rows of the ring
 
-// LANES: lanes of a row's warps that own a row (8 or 32); `warps` warps per row.
-template <int DT, int PT, int K, int LANES, bool AL>
-__global__ void __launch_bounds__(32 * FwdShape<K>::WARPS, 1) layer_norm_fwd_kernel(
-    LayerNormParams p, int warps, RowRanges ranges, typename Elem<DT>::T* __restrict__ y,
+// K = ceil(units / (32 * warps)): only a lane's last vector may lie past the row's end.
+template <int DT, int PT, int K, bool AL>
+__global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel(
+    LayerNormParams p, int warps, int groups, typename Elem<DT>::T* __restrict__ y,
     float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   using T = typename Elem<DT>::T;
   using P = typename Elem<PT>::T;
-  constexpr int W = Elem<DT>::W, H = W / 2;
-  extern __shared__ uint4 slots[];  // [2][K][threads], then weight and bias [W / 4][units] float4 each
-  __shared__ float red[2][FwdShape<K>::WARPS];
-  const int threads = blockDim.x, lane = threadIdx.x & (LANES - 1);
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = kFwdStages;
+  using S = Slot<DT, AL>;
+  extern __shared__ uint4 ring[];  // [STAGES][K][threads]; then weight and bias; then the slots' fifth words
+  __shared__ float red[2][FwdShape<K>::THREADS / 32];
+  constexpr int threads = FwdShape<K>::THREADS;
+  const int lane = threadIdx.x & 31;
+  const int group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
   const int units = (p.D + W - 1) / W;
-  const int group = LANES < 32 ? threadIdx.x / LANES : (threadIdx.x >> 5) / warps;
-  const int warp = LANES < 32 ? 0 : (threadIdx.x >> 5) - group * warps;
-  const int first = warp * K * LANES + lane;  // this lane's vectors: first + k * LANES
-  const int groups = LANES < 32 ? threads / LANES : (threads >> 5) / warps;
-  unsigned r0, r1;
-  row_range(ranges, blockIdx.x * groups + group, r0, r1);
+  const int first = 32 * warp + lane, width = 32 * warps;  // this lane's vectors: first + k * width
+  const int last = first + (K - 1) * width;
+  const bool tail = last < units;
+  const int tail_n = min(p.D - last * W, W);  // elements of the last vector
+  // this group's rows: r0, r0 + step, ...; none when there are more groups than named barriers
+  const unsigned step = gridDim.x * groups, r0 = blockIdx.x * groups + group, r1 = group < groups ? p.N : 0;
   const T* src = static_cast<const T*>(p.x) + static_cast<long long>(r0) * p.x_stride + first * W;
-  uint4* const mine = slots + threadIdx.x;
-  auto valid = [&](int k) { return min(p.D - (first + k * LANES) * W, W); };  // elements of vector k
-  for (int i = 0; i < 2 * K; ++i) mine[i * threads] = make_uint4(0, 0, 0, 0);  // what no copy writes stays 0
-  unsigned next = r0;
-  auto issue = [&](int b) {  // the next row, if there is one
-    if (next < r1) {
+  const T* const lo = static_cast<const T*>(p.x);
+  const T* const hi = lo + static_cast<long long>(p.N - 1) * p.x_stride + p.D;
+  uint4* const mine = ring + threadIdx.x;
+  constexpr int pitch = K * threads;  // of a stage
+  float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
+  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + W / 2 * units) + threadIdx.x;
+  if (!AL || !tail)  // what no copy writes stays 0
+    for (int i = 0; i < STAGES; ++i) mine[(i * K + K - 1) * threads] = make_uint4(0, 0, 0, 0);
+  auto issue = [&](unsigned n, int stage) {  // row n, the next one, if there is one
+    if (n < r1) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (first + k * LANES < units)
-          copy_vector<DT, AL>(mine + (b * K + k) * threads, src + k * LANES * W, valid(k));
-      src += p.x_stride;
-      ++next;
+        if (k < K - 1 || tail)
+          S::copy(mine + stage * pitch + k * threads, fifth + stage * pitch + k * threads, src + k * width * W,
+                  k < K - 1 ? W : tail_n, lo, hi);
+      src += step * p.x_stride;
     }
     copy_commit();
   };
-  issue(0);
-  float4* const kept = reinterpret_cast<float4*>(slots + 2 * K * threads);
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(r0 + s * step, s);
   keep_params<PT, W, AL>(kept, static_cast<const P*>(p.weight), 1.f, p.D);
   keep_params<PT, W, AL>(kept + W / 4 * units, static_cast<const P*>(p.bias), 0.f, p.D);
   __syncthreads();
   const float inv = 1.f / static_cast<float>(p.D);
-  // sum over the row's lanes: butterflies, then its warps in ascending order
+  // sum over the group: butterflies, then over its warps
   auto row_sum = [&](float v, float* sm) {
 #pragma unroll
-    for (int off = LANES / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (LANES == 32 && warps > 1) {
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (warps > 1) {
       if (lane == 0) sm[group * warps + warp] = v;
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
-      v = sm[group * warps];
-      for (int w = 1; w < warps; ++w) v += sm[group * warps + w];
+      v = sm[group * warps + (lane & (warps - 1))];
+      for (int off = warps / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     }
     return v;
   };
   T* out = y + static_cast<size_t>(r0) * p.D + first * W;
-  // the lanes of a warp stay together: its groups' ranges differ by one row at most
-  unsigned rounds = r1 - r0;
-  if (LANES < 32) rounds = __reduce_max_sync(0xffffffffu, rounds);
-  for (unsigned i = 0; i < rounds; ++i) {
-    const int b = i & 1;
-    issue(b ^ 1);
-    copy_wait<1>();
-    F2 x[K][H], t[H];
+  int stage = 0;
+  for (unsigned n = r0; n < r1; n += step) {
+    copy_wait<STAGES - 2>();
+    const int at = stage * pitch;
+    const bool shift = S::shifted(lo + static_cast<long long>(n) * p.x_stride);
+    F2 x[K][H], t[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack2<DT, W>(mine[(b * K + k) * threads], x[k]);
+      unpack2<DT, W>(S::read(mine + at + k * threads, fifth + at + k * threads, shift, k < K - 1 ? W : tail_n), x[k]);
 #pragma unroll
-      for (int h = 0; h < H; ++h) t[h] = k == 0 ? x[k][h] : add2(t[h], x[k][h]);
+      for (int i = 0; i < H; ++i) t[i & 1] = add2(t[i & 1], x[k][i]);
     }
-#pragma unroll
-    for (int h = 1; h < H; ++h) t[0] = add2(t[0], t[h]);
-    const float mean = row_sum(sum2(t[0]), red[0]) * inv;
+    issue(n + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    const float mean = row_sum(sum2(add2(t[0], t[1])), red[0]) * inv;
+    t[0] = t[1] = f2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float m = first + k * LANES < units ? -mean : 0.f;  // past the row's end x is and stays 0
+      const float m = k < K - 1 || tail ? -mean : 0.f;  // past the row's end x is and stays 0
 #pragma unroll
-      for (int h = 0; h < H; ++h) x[k][h] = add2(x[k][h], f2(m));
-      if constexpr (!AL) {  // a ragged last vector
-        const int n = valid(k);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          x[k][h] = f2(2 * h < n ? x[k][h].x : 0.f, 2 * h + 1 < n ? x[k][h].y : 0.f);
+      for (int i = 0; i < H; ++i) {
+        x[k][i] = add2(x[k][i], f2(m));
+        if constexpr (!AL) {  // a ragged last vector
+          if (k == K - 1) x[k][i] = f2(2 * i < tail_n ? x[k][i].x : 0.f, 2 * i + 1 < tail_n ? x[k][i].y : 0.f);
+        }
+        t[i & 1] = fma2(x[k][i], x[k][i], t[i & 1]);
       }
-#pragma unroll
-      for (int h = 0; h < H; ++h) t[h] = k == 0 ? mul2(x[k][h], x[k][h]) : fma2(x[k][h], x[k][h], t[h]);
     }
-#pragma unroll
-    for (int h = 1; h < H; ++h) t[0] = add2(t[0], t[h]);
     // rsqrtf is within two units in the last place
-    const float rstd = rsqrtf(fmaf(row_sum(sum2(t[0]), red[1]), inv, p.eps));
-    const unsigned n = r0 + i;
-    if (LANES < 32 && n >= r1) continue;
-    const F2 sc = f2(rstd);
+    const float rstd = rsqrtf(fmaf(row_sum(sum2(add2(t[0], t[1])), red[1]), inv, p.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = first + k * LANES;
-      if (u < units) {
+      if (k < K - 1 || tail) {
+        const int u = first + k * width;
 #pragma unroll
         for (int q = 0; q < W / 4; ++q) {
           const float4 w = kept[q * units + u], c = kept[(W / 4 + q) * units + u];
-          x[k][2 * q] = fma2(mul2(x[k][2 * q], sc), f2(w.x, w.y), f2(c.x, c.y));
-          x[k][2 * q + 1] = fma2(mul2(x[k][2 * q + 1], sc), f2(w.z, w.w), f2(c.z, c.w));
+          x[k][2 * q] = fma2(mul2(x[k][2 * q], f2(rstd)), f2(w.x, w.y), f2(c.x, c.y));
+          x[k][2 * q + 1] = fma2(mul2(x[k][2 * q + 1], f2(rstd)), f2(w.z, w.w), f2(c.z, c.w));
         }
-        store_vector<DT, AL>(out + k * LANES * W, pack2<DT, W>(x[k]), valid(k));
+        S::store(out + k * width * W, pack2<DT, W>(x[k]), k < K - 1 ? W : tail_n);
       }
     }
-    out += p.D;
+    out += static_cast<size_t>(step) * p.D;
     if (first == 0) {
       mean_out[n] = mean;
       rstd_out[n] = rstd;
@@ -171,61 +174,53 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_fwd_wide_kernel(Layer
   }
 }
 
-template <int DT, int PT, int K, int LANES = 32>
-cudaError_t rows(const LayerNormParams& p, int warps, void* y, float* mean, float* rstd, cudaStream_t s) {
-  constexpr int W = Elem<DT>::W;
-  const int units = (p.D + W - 1) / W;
-  const bool al = p.D % W == 0 && aligned16(p.x) && (p.x_stride * elem_bytes(DT)) % 16 == 0 && aligned16(y) &&
-                  aligned16(p.weight) && aligned16(p.bias);
-  const auto kernel = al ? layer_norm_fwd_kernel<DT, PT, K, LANES, true> : layer_norm_fwd_kernel<DT, PT, K, LANES, false>;
-  const int groups = LANES < 32 ? FwdShape<K>::WARPS * (32 / LANES) : FwdShape<K>::WARPS / warps;
-  const int threads = LANES < 32 ? 32 * FwdShape<K>::WARPS : 32 * warps * groups;
-  const size_t smem = (static_cast<size_t>(2) * K * threads + 2 * (W / 4) * static_cast<size_t>(units)) * 16;
+template <int DT, int PT, int K>
+cudaError_t rows(const LayerNormParams& p, int warps, bool al, void* y, float* mean, float* rstd, cudaStream_t s) {
+  using Shape = FwdShape<K>;
+  const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
+  int groups = Shape::THREADS / 32 / warps;
+  if (warps > 1 && groups > 15) groups = 15;  // named barriers 1 .. 15
+  const size_t smem = static_cast<size_t>(kFwdStages) * K * Shape::THREADS * (al ? 16 : Slot<DT, false>::BYTES) +
+                      static_cast<size_t>(Elem<DT>::W / 2) * units * 16;
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
-  kernel<<<grid, threads, smem, s>>>(
-      p, warps, row_ranges(p.N, static_cast<long long>(grid) * groups),
-      static_cast<typename Elem<DT>::T*>(y), mean, rstd);
+  const auto kernel = al ? layer_norm_fwd_kernel<DT, PT, K, true> : layer_norm_fwd_kernel<DT, PT, K, false>;
+  kernel<<<grid, Shape::THREADS, smem, s>>>(p, warps, groups, static_cast<typename Elem<DT>::T*>(y), mean, rstd);
   return launch_result();
 }
 
-// Vectors per lane: few lanes with many vectors, see above; more than one warp per row
-// where they would not fit its registers.
 template <int DT, int PT>
 cudaError_t run(const LayerNormParams& p, void* y, float* mean, float* rstd, cudaStream_t s) {
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
-  if (units <= 8) return rows<DT, PT, 1, 8>(p, 1, y, mean, rstd, s);
-  if (units <= 32) return rows<DT, PT, 1>(p, 1, y, mean, rstd, s);
-  if (units <= 64) return rows<DT, PT, 2>(p, 1, y, mean, rstd, s);
-  if (units <= 128) return rows<DT, PT, 4>(p, 1, y, mean, rstd, s);
-  if (units <= 192) return rows<DT, PT, 6>(p, 1, y, mean, rstd, s);
-  if (units <= 256) return rows<DT, PT, 8>(p, 1, y, mean, rstd, s);
-  if (units <= 352) return rows<DT, PT, 11>(p, 1, y, mean, rstd, s);
-  if (units <= kPipeUnits) return rows<DT, PT, 8>(p, units <= 512 ? 2 : 4, y, mean, rstd, s);
+  const bool al = p.D % Elem<DT>::W == 0 && aligned16(p.x) && (p.x_stride * elem_bytes(DT)) % 16 == 0 &&
+                  aligned16(y) && aligned16(p.weight) && aligned16(p.bias);
+  if (units <= kPipeUnits) {
+    int warps = 1;
+    while (96 * warps < units) warps *= 2;
+    const int K = (units + 32 * warps - 1) / (32 * warps);
+    if (K == 1) return rows<DT, PT, 1>(p, warps, al, y, mean, rstd, s);
+    if (K == 2) return rows<DT, PT, 2>(p, warps, al, y, mean, rstd, s);
+    return rows<DT, PT, 3>(p, warps, al, y, mean, rstd, s);
+  }
   layer_norm_fwd_wide_kernel<DT, PT><<<p.N, kWideThreads, 0, s>>>(p, static_cast<typename Elem<DT>::T*>(y), mean, rstd);
   return launch_result();
 }
 
-constexpr int kFwdSmem = 220 * 1024;  // most that a layout above takes
-
-template <int DT, int PT, int K, int LANES = 32>
+template <int DT, int PT, int K>
 cudaError_t allow() {
-  const cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_fwd_kernel<DT, PT, K, LANES, true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem));
+  const int bytes = 220 * 1024;  // more than any layout takes
+  const cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_fwd_kernel<DT, PT, K, true>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   return e != cudaSuccess ? e
-                          : note_cuda(cudaFuncSetAttribute(layer_norm_fwd_kernel<DT, PT, K, LANES, false>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem));
+                          : note_cuda(cudaFuncSetAttribute(layer_norm_fwd_kernel<DT, PT, K, false>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
 }
 
 template <int DT, int PT>
 cudaError_t setup() {
-  cudaError_t e = allow<DT, PT, 1, 8>();
-  if (e == cudaSuccess) e = allow<DT, PT, 1>();
+  cudaError_t e = allow<DT, PT, 1>();
   if (e == cudaSuccess) e = allow<DT, PT, 2>();
-  if (e == cudaSuccess) e = allow<DT, PT, 4>();
-  if (e == cudaSuccess) e = allow<DT, PT, 6>();
-  if (e == cudaSuccess) e = allow<DT, PT, 8>();
-  if (e == cudaSuccess) e = allow<DT, PT, 11>();
+  if (e == cudaSuccess) e = allow<DT, PT, 3>();
   return e;
 }
 
