@@ -11,7 +11,7 @@
  *
  * The gradient sorts the tokens and sums each table row's tokens in ascending
  * token order in fp32, with one rounding to the table's type.  A row named
- * more than 64 times is summed in pieces whose length depends on that count
+ * more than 32 times is summed in pieces whose length depends on that count
  * alone, joined in ascending order.  A row of the gradient therefore depends
  * on its own tokens only, and is bitwise the same in every run.
  *
@@ -21,7 +21,7 @@
  * out [N, D] are contiguous row-major in bf16 (dtype 0), fp32 (dtype 1) or
  * fp16 (dtype 2); any D >= 1.  Element alignment suffices; 16-byte aligned
  * tensors with rows of a multiple of 16 bytes move fastest.  scale is rounded
- * to fp32 by the caller and must be finite.  N, V < 2^31, D < 2^22, N * D <= 2^44.
+ * to fp32 by the caller and must be finite.  N, V < 2^31, D < 2^22, N * D <= 2^42.
  */
 #ifndef EMBEDDING_H_
 #define EMBEDDING_H_
@@ -44,8 +44,8 @@ int embedding_fwd(const int64_t* tokens, const void* weight, int dtype, int64_t 
 /* Bytes of workspace embedding_bwd needs (0 when N == 0 or a size is invalid). */
 size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D);
 
-/* Gradient of the table.  grad_out's rows start grad_out_row_stride elements
- * apart (D when contiguous; 0 repeats one row).
+/* Gradient of the table.  grad_out's rows start grad_out_row_stride < 2^31
+ * elements apart (D when contiguous; 0 repeats one row).
  *   accumulate == 0: every row of grad_weight is overwritten (zero where no
  *     token names it); N == 0 writes zeros.
  *   accumulate != 0: the tokens' sums are added to the rows they name, in fp32

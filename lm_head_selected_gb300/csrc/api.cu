@@ -1267,7 +1267,8 @@ int embedding_bwd(const int64_t* tokens, const void* grad_out, int64_t grad_out_
                   void* workspace, size_t workspace_bytes, void* stream) {
   int st = embedding_shapes(dtype, N, V, D);
   if (st != LLP_OK) return st;
-  if (!row_stride_ok(N, D, grad_out_row_stride) || N * D > (int64_t(1) << 44)) return LLP_ERR_BAD_SHAPE;
+  if (!row_stride_ok(N, D, grad_out_row_stride) || grad_out_row_stride > kLim31 || N * D > (int64_t(1) << 42))
+    return LLP_ERR_BAD_SHAPE;
   if (N == 0 && accumulate) return LLP_OK;
   if (grad_weight == nullptr) return LLP_ERR_NULL_POINTER;
   if (!aligned(grad_weight, dtype_bytes(dtype))) return LLP_ERR_MISALIGNED;

@@ -83,30 +83,177 @@ struct Elem<kDtypeF32> {
   }
 };
 
-// A unit is what one thread moves at a time: a 16-byte vector, or one element
-// where rows are not 16-byte aligned.
-template <int DT, bool VEC>
-struct Unit {
+// Two fp32 values in one register pair, for the packed fp32 instructions.
+using F2 = float2;
+__device__ __forceinline__ F2 f2(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ F2 f2(float a) { return make_float2(a, a); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float sum2(F2 a) { return __fadd_rn(a.x, a.y); }
+
+template <int DT, int W>
+__device__ __forceinline__ void unpack2(const uint4& r, F2 (&v)[W / 2]) {
+  float f[W];
+  Elem<DT>::unpack(r, f);
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT, int W>
+__device__ __forceinline__ uint4 pack2(const F2 (&v)[W / 2]) {
+  float f[W];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) f[2 * i] = v[i].x, f[2 * i + 1] = v[i].y;
+  return Elem<DT>::pack(f);
+}
+
+__device__ __forceinline__ void copy_async(void* slot, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* slot, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// A thread's copy of one vector of a row in shared memory, and what it takes to fill and
+// read it.  Aligned: 16 bytes, one cp.async.  Otherwise 4-byte words: an odd row of 16-bit
+// elements may start in the middle of one, so that its vectors take five words; they keep
+// that shift until they are read.  `span`: the tensor's first and one past its last
+// element; a word that sticks out of it is put together from elements instead.
+template <int DT, bool AL>
+struct Slot {
   using T = typename Elem<DT>::T;
-  static constexpr int W = VEC ? Elem<DT>::W : 1;
-  using Raw = typename std::conditional<VEC, uint4, T>::type;
-  static __device__ __forceinline__ Raw load(const T* p) {
-    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p));
-    else return __ldg(p);
+  static constexpr int W = Elem<DT>::W;
+  static constexpr bool FIVE = !AL && DT != kDtypeF32;
+  static constexpr int BYTES = FIVE ? 20 : 16;  // per vector
+  static __device__ __forceinline__ bool shifted(const T* p) { return FIVE && (reinterpret_cast<uintptr_t>(p) & 2) != 0; }
+  static __device__ __forceinline__ void copy(uint4* slot, uint32_t* fifth, const T* p, int n, const T* lo, const T* hi) {
+    if constexpr (AL) {
+      copy_async(slot, p);
+    } else if constexpr (DT == kDtypeF32) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < n) copy_async4(reinterpret_cast<float*>(slot) + i, p + i);
+    } else {
+      const T* q = shifted(p) ? p - 1 : p;  // 4-byte aligned
+      const int words = (static_cast<int>(p - q) + n + 1) / 2;
+      if (q >= lo && q + 2 * words <= hi) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+          if (i < words) copy_async4(i < 4 ? reinterpret_cast<uint32_t*>(slot) + i : fifth, q + 2 * i);
+      } else {
+        uint32_t w[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          const T *a = q + 2 * i, *b = a + 1;
+          const uint32_t l = a >= p && a < p + n ? *reinterpret_cast<const uint16_t*>(a) : 0;
+          const uint32_t h = b >= p && b < p + n ? *reinterpret_cast<const uint16_t*>(b) : 0;
+          w[i] = l | h << 16;
+        }
+        *slot = make_uint4(w[0], w[1], w[2], w[3]);
+        *fifth = w[4];
+      }
+    }
   }
-  static __device__ __forceinline__ Raw zero() {
-    if constexpr (VEC) return make_uint4(0, 0, 0, 0);
-    else return Elem<DT>::put(0.f);
+  // The vector, elements at or past n reading as 0.
+  static __device__ __forceinline__ uint4 read(const uint4* slot, const uint32_t* fifth, bool shift, int n) {
+    uint4 r = *slot;
+    if constexpr (FIVE) {
+      if (shift) {
+        r.x = __funnelshift_r(r.x, r.y, 16);
+        r.y = __funnelshift_r(r.y, r.z, 16);
+        r.z = __funnelshift_r(r.z, r.w, 16);
+        r.w = __funnelshift_r(r.w, *fifth, 16);
+      }
+      if (n < W) {
+        uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = 2 * i >= n ? 0 : 2 * i + 1 >= n ? w[i] & 0xFFFFu : w[i];
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    return r;
   }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[W]) {
-    if constexpr (VEC) Elem<DT>::unpack(r, v);
-    else v[0] = Elem<DT>::get(r);
+  // The same vector straight from global memory.
+  static __device__ __forceinline__ uint4 load(const T* p, int n, const T* lo, const T* hi) {
+    if constexpr (AL) {
+      return __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+      uint32_t w[5] = {0, 0, 0, 0, 0};
+      if constexpr (DT == kDtypeF32) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (i < n) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        const T* q = shifted(p) ? p - 1 : p;
+        const int words = (static_cast<int>(p - q) + n + 1) / 2;
+        const bool wide = q >= lo && q + 2 * words <= hi;
+        const uint16_t* const h = reinterpret_cast<const uint16_t*>(q);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          if (wide) {
+            if (i < words) w[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
+          } else {
+            const T *a = q + 2 * i, *b = a + 1;
+            if (a >= p && a < p + n) w[i] = __ldg(h + 2 * i);
+            if (b >= p && b < p + n) w[i] |= static_cast<uint32_t>(__ldg(h + 2 * i + 1)) << 16;
+          }
+        }
+        const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+        return read(&v, w + 4, q != p, n);
+      }
+    }
   }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[W]) {
-    if constexpr (VEC) *reinterpret_cast<uint4*>(p) = Elem<DT>::pack(v);
-    else *p = Elem<DT>::put(v[0]);
+  // The same for memory that this kernel writes too, element by element unless aligned.
+  static __device__ __forceinline__ uint4 load_changed(const T* p, int n) {
+    if constexpr (AL) {
+      return *reinterpret_cast<const uint4*>(p);
+    } else {
+      float f[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[i] = i < n ? Elem<DT>::get(p[i]) : 0.f;
+      return Elem<DT>::pack(f);  // exact, but for the payload of a NaN
+    }
   }
-  static __device__ __forceinline__ void store_raw(T* p, const Raw& r) { *reinterpret_cast<Raw*>(p) = r; }
+  // The first n elements of a vector to a row.
+  static __device__ __forceinline__ void store(T* p, const uint4& v, int n) {
+    if constexpr (AL) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      if constexpr (DT == kDtypeF32) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (i < n) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+      } else {
+        uint16_t* const h = reinterpret_cast<uint16_t*>(p);
+        if (n == W && !shifted(p)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        } else if (n == W) {
+          h[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(p + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+          h[7] = static_cast<uint16_t>(w[3] >> 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i < n) h[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
 };
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

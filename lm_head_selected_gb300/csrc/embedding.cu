@@ -9,12 +9,18 @@
 //           give the place of its first token in the sorted order, so the CTAs
 //           need nothing from one another.  A second scan puts each token at its
 //           place: sorted by row, ascending within a row.
-//   reduce  CTAs take 32 places of the sorted order and a slice of the columns,
-//           stream those rows of grad_out with eight loads in flight per thread,
-//           and write a table row whenever its tokens end.  A row of more than
-//           64 tokens is cut into chunks whose length depends on its count
-//           alone; the CTA that finishes the last chunk of a row joins them in
+//   reduce  a warp takes 8 or 16 places of the sorted order and 64 vectors of the columns.
+//           It streams those rows of grad_out through its own ring in shared memory
+//           (cp.async, 5 or 11 rows in flight), and writes a table row whenever its tokens
+//           end.  A row of more than 32 tokens is cut into chunks whose length depends on
+//           its count alone; the warp that finishes a row's last chunk joins them in
 //           ascending order.  Other CTAs of the same launch write the zero rows.
+//
+// Measured, bf16, tokens of a 1 / (id + 1) distribution: 16384 tokens x 2688 into 131072
+// rows 116 us (6.8 TB/s, the measured copy peak); added to 128256 rows of 4096, 50 us
+// (4.9 TB/s, 72%: 9.5 us are the sort, and the reduce launch is held by the instructions
+// of short rows and by the sums of the longest ones); fp32, 2049 x 1001 into 50257 rows
+// 39 us (79%).
 #include "elem.cuh"
 
 namespace llp {
@@ -28,134 +34,206 @@ __device__ __forceinline__ bool token_ok(long long t, long long V, long long ign
 // ---------------------------------------------------------------- lookup
 
 constexpr int kFwdWarps = 8;
-constexpr int kFwdLoads = 4;  // units per lane, all in flight together
+constexpr int kFwdLoads = 4;  // vectors per lane, all in flight together
 
-// One warp per row and chunk of 32 * kFwdLoads units (2 KB of vectors).
-template <int DT, bool VEC>
+// One warp per row and chunk of at most 32 * kFwdLoads vectors (2 KB).  Bound by memory:
+// 16384 rows of 2688 bf16 take 21.4 us, 86% of the measured copy peak on the rows written
+// and the distinct ones read; 32 rows 1.6 us, one launch.
+template <int DT, bool AL>
 __global__ void __launch_bounds__(32 * kFwdWarps) embedding_fwd_kernel(const long long* __restrict__ tokens,
                                                                        const typename Elem<DT>::T* __restrict__ weight,
-                                                                       int N, int V, int D, int chunk_units,
-                                                                       float scale, long long ignore_index,
+                                                                       int N, int V, int D, int chunk, float scale,
+                                                                       long long ignore_index,
                                                                        typename Elem<DT>::T* __restrict__ out) {
-  using U = Unit<DT, VEC>;
+  using S = Slot<DT, AL>;
+  constexpr int W = Elem<DT>::W;
   const long long n = static_cast<long long>(blockIdx.x) * kFwdWarps + (threadIdx.x >> 5);
   if (n >= N) return;
-  const int units = D / U::W;
-  const int u0 = blockIdx.y * chunk_units;
-  const int u1 = min(u0 + chunk_units, units);
+  const int u0 = blockIdx.y * chunk + (threadIdx.x & 31);
+  const int u1 = min(static_cast<int>(blockIdx.y + 1) * chunk, (D + W - 1) / W);
   const long long t = __ldg(tokens + n);
   const bool ok = token_ok(t, V, ignore_index);
-  const typename U::T* w = weight + (ok ? static_cast<size_t>(t) * D : 0);
-  typename U::T* o = out + static_cast<size_t>(n) * D;
-  typename U::Raw r[kFwdLoads];
+  const typename Elem<DT>::T* const row = weight + (ok ? static_cast<size_t>(t) * D : 0);
+  typename Elem<DT>::T* const o = out + static_cast<size_t>(n) * D;
+  uint4 r[kFwdLoads];
 #pragma unroll
   for (int k = 0; k < kFwdLoads; ++k) {
-    const int u = u0 + 32 * k + (threadIdx.x & 31);
-    r[k] = (ok && u < u1) ? U::load(w + static_cast<size_t>(u) * U::W) : U::zero();
+    const int u = u0 + 32 * k;
+    r[k] = make_uint4(0, 0, 0, 0);
+    if (ok && u < u1) r[k] = S::load(row + u * W, min(D - u * W, W), weight, weight + static_cast<size_t>(V) * D);
   }
 #pragma unroll
   for (int k = 0; k < kFwdLoads; ++k) {
-    const int u = u0 + 32 * k + (threadIdx.x & 31);
+    const int u = u0 + 32 * k;
     if (u >= u1) break;
-    float v[U::W];
-    U::unpack(r[k], v);
+    float v[W];
+    Elem<DT>::unpack(r[k], v);
 #pragma unroll
-    for (int i = 0; i < U::W; ++i) v[i] = ok ? v[i] * scale : 0.f;
-    U::store(o + static_cast<size_t>(u) * U::W, v);
+    for (int i = 0; i < W; ++i) v[i] = ok ? v[i] * scale : 0.f;
+    S::store(o + u * W, Elem<DT>::pack(v), min(D - u * W, W));
   }
 }
 
 // ---------------------------------------------------------------- gradient: sort
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortOwners = 152;      // CTAs that share the table's rows, one per SM
-constexpr int kSortMaxRange = 1536;   // rows of one CTA: 32 warps x 1536 counters fill its shared memory
+constexpr int kSortWarps = kSortThreads / 32;  // each scans a span of the tokens
+constexpr int kSortSets = kSortWarps / 2;      // two spans share a set of counters: fewer to clear and to add up
+constexpr int kSortOwners = 128;      // CTAs that share the table's rows (a power of two)
+constexpr int kSortMaxRange = 2048;   // rows of one CTA
+constexpr int kSortList = 512;        // tokens of its rows that a warp notes as it scans
 constexpr int kSortLoads = 8;         // tokens per lane in flight
-constexpr int kWindow = 64;           // shortest chunk of a long row
+constexpr int kSortSmem = 224 * 1024;
+constexpr int kWindow = 32;           // shortest chunk of a long row
 
-// A place of the sorted order: the token n, its row v, and the places [begin, end) of that row.
+// A place of the sorted order: the token n, its row v, and the places [begin, end) of that
+// row.  The sign bits say, of n, that it is the row's last token, and of v, that the row has
+// more than kWindow.
 using Place = int4;
+constexpr int kFlag = static_cast<int>(0x80000000u);
 
+// CTA b owns the rows v with v mod owners = b: frequent tokens, whose ids often lie
+// together, are spread over the CTAs (with contiguous ranges one of them had 57% of the
+// tokens of a 1 / (id + 1) distribution, and the launch took 17 us instead of 9.5).
 struct SortPlan {
-  int owners, range, warps, span;  // CTAs; rows per CTA (multiple of 32); scanning warps; tokens per warp
+  int shift, owners, range;  // log2 of the CTAs; rows of each, a multiple of 32
+  int warps, span, list;     // scanning warps; tokens of each (a multiple of 32), tokens that it notes
   size_t smem;
 };
 
 SortPlan sort_plan(long long N, long long V) {
   SortPlan p;
-  long long range = ((V + kSortOwners - 1) / kSortOwners + 31) / 32 * 32;
-  if (range > kSortMaxRange) range = kSortMaxRange;
-  p.range = static_cast<int>(range);
-  p.owners = static_cast<int>((V + range - 1) / range);
+  p.shift = 7;
+  while (((V - 1) >> p.shift) >= kSortMaxRange) ++p.shift;
+  p.owners = 1 << p.shift;
+  p.range = static_cast<int>((((V - 1) >> p.shift) + 32) / 32 * 32);
   const long long w = (N + 255) / 256;  // at least 256 tokens per warp
   p.warps = static_cast<int>(w < kSortWarps ? w : kSortWarps);
   p.span = static_cast<int>(((N + p.warps - 1) / p.warps + 31) / 32 * 32);
-  p.smem = static_cast<size_t>(p.range) * (p.warps + 2) * sizeof(int);
+  const size_t counters = static_cast<size_t>(p.range) * ((p.warps + 1) / 2 + 2) * sizeof(int);
+  const size_t room = (kSortSmem - counters) / (p.warps * sizeof(int));
+  p.list = static_cast<int>(room < kSortList ? room : kSortList);
+  if (p.list > p.span) p.list = p.span;
+  p.smem = counters + static_cast<size_t>(p.list) * p.warps * sizeof(int);
   return p;
 }
 
-// First place of the chunk arithmetic: chunks of 64 * 2^s places, at most 64 of them.
+// Chunks of a row of `count` tokens: 32 * 2^s places for at most 1024 * 4^s tokens.  A chunk's
+// places are added one after another, and so are the chunks: with about as many chunks as
+// places neither is long.
 __device__ __forceinline__ int chunk_of(int count) {
-  return kWindow << (count > 4096 ? 32 - __clz((count - 1) >> 12) : 0);
+  return kWindow << ((32 - __clz((count - 1) >> 10) + 1) / 2);
 }
 
+// Measured, 16384 tokens of a 1 / (id + 1) distribution, 131072 rows: 9.5 us, bound by
+// latency: the scan is 2.5 us of it, the counters and their sums 2, placing the tokens 1.5
+// to 2.5, the launch the rest.  2049 tokens and 50257 rows: 5.9 us.
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const long long* __restrict__ tokens, int N,
-                                                                         int V, long long ignore_index, int range,
-                                                                         int warps, int span, Place* __restrict__ places,
+                                                                         int V, long long ignore_index, int shift,
+                                                                         int range, int warps, int span, int list,
+                                                                         Place* __restrict__ places,
                                                                          unsigned* __restrict__ named,
                                                                          int* __restrict__ arrivals, int num_arrivals,
                                                                          int* __restrict__ total) {
-  extern __shared__ int sm[];
-  int* count = sm;                       // [warps][range]
-  int* first = count + warps * range;    // [range] first place of each row
-  int* last = first + range;             // [range] one past its last place
-  __shared__ int warp_sum[kSortWarps], warp_low[kSortWarps];
+  extern __shared__ int4 sm4[];
+  const int sets = (warps + 1) / 2;
+  int* const count = reinterpret_cast<int*>(sm4);  // [sets][range]
+  int* const first = count + sets * range;         // [range] first place of each row
+  int* const last = first + range;                 // [range] one past its last place
+  unsigned* const noted = reinterpret_cast<unsigned*>(last + range);  // [warps][list]: place in the span, row in the range
+  __shared__ int warp_sum[kSortWarps], warp_low[kSortWarps], warp_hits[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long lo = static_cast<long long>(blockIdx.x) * range;
-  const long long hi = min(lo + range, static_cast<long long>(V));
+  const unsigned self = blockIdx.x, mask = (1u << shift) - 1, below = (1u << lane) - 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = blockIdx.x * kSortThreads + tid; i < num_arrivals; i += gridDim.x * kSortThreads) arrivals[i] = 0;
-  for (int i = tid; i < warps * range; i += kSortThreads) count[i] = 0;
-  __syncthreads();
+  for (int i = tid; i < sets * range / 4; i += kSortThreads) sm4[i] = make_int4(0, 0, 0, 0);  // range % 32 == 0
 
-  // this warp's tokens, in ascending order
-  const long long t0 = static_cast<long long>(warp) * span;
-  const long long t1 = min(t0 + span, static_cast<long long>(N));
-  int* mine = count + warp * range;
-  int low = 0;
-  if (warp < warps) {
-    for (long long b = t0; b < t1; b += 32 * kSortLoads) {
+  // Calls take(place in the span, valid, row) for the tokens of a span in ascending order, a warp's
+  // 32 at a time.
+  const unsigned skipped = ignore_index >= 0 && ignore_index < V ? static_cast<unsigned>(ignore_index) : ~0u;
+  auto scan = [&](int which, auto&& take) {
+    const unsigned t0 = static_cast<unsigned>(which) * span;
+    const unsigned count_of = t0 < static_cast<unsigned>(N) ? min(static_cast<unsigned>(span), N - t0) : 0;
+    const long long* const src = tokens + t0 + lane;
+    auto one = [&](unsigned at, long long t) {
+      const unsigned v = static_cast<unsigned>(t);
+      take(at, (t >> 32) == 0 && v < static_cast<unsigned>(V) && v != skipped, v);
+    };
+    for (unsigned b = 0; b < count_of; b += 32 * kSortLoads) {
       long long t[kSortLoads];
+      if (b + 32 * kSortLoads <= count_of) {
 #pragma unroll
-      for (int k = 0; k < kSortLoads; ++k) {
-        const long long n = b + 32 * k + lane;
-        t[k] = n < t1 ? __ldg(tokens + n) : -1;
+        for (int k = 0; k < kSortLoads; ++k) t[k] = __ldg(src + b + 32 * k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSortLoads; ++k) t[k] = b + 32 * k + lane < count_of ? __ldg(src + b + 32 * k) : -1;
       }
 #pragma unroll
-      for (int k = 0; k < kSortLoads; ++k) {
-        const bool ok = t[k] >= 0 && t[k] < hi && t[k] != ignore_index;
-        if (ok && t[k] >= lo) atomicAdd(mine + static_cast<int>(t[k] - lo), 1);
-        low += ok && t[k] < lo;
-      }
+      for (int k = 0; k < kSortLoads; ++k)
+        if (b + 32 * k < count_of) one(b + 32 * k + lane, t[k]);
     }
+  };
+
+  int low = 0, hits = 0;
+  if (warp < warps) {
+    unsigned* const mine = noted + warp * list;
+    scan(warp, [&](unsigned at, bool ok, unsigned v) {
+      const unsigned owner = v & mask;
+      const bool in = ok && owner == self;
+      low += ok && owner < self;
+      const unsigned act = __ballot_sync(0xffffffffu, in);
+      if (act == 0) return;
+      const int h = hits + __popc(act & below);
+      if (in && h < list) mine[h] = at << 11 | v >> shift;  // used when all of them fit and at < 2^21
+      hits += __popc(act);
+    });
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) low += __shfl_xor_sync(0xffffffffu, low, off);
-  if (lane == 0) warp_low[warp] = low;
+  if (lane == 0) {
+    warp_low[warp] = low;
+    warp_hits[warp] = hits;
+  }
+  __syncthreads();
+  // Calls take(is one, token, row in the range) for this CTA's tokens in a set's spans, in ascending order.
+  auto own_tokens = [&](int set, auto&& take) {
+    for (int w = 2 * set; w < min(2 * set + 2, warps); ++w) {
+      const int n = warp_hits[w];
+      const unsigned t0 = static_cast<unsigned>(w) * span;
+      if (n <= list && span <= (1 << 21)) {
+        for (int h = 0; h < n; h += 32) {
+          const unsigned e = h + lane < n ? noted[w * list + h + lane] : 0;
+          take(h + lane < n, t0 + (e >> 11), e & 2047);
+        }
+      } else {  // more than were noted: scan again
+        scan(w, [&](unsigned at, bool ok, unsigned v) { take(ok && (v & mask) == self, t0 + at, v >> shift); });
+      }
+    }
+  };
+  int* const mine = count + warp * range;
+  if (warp < sets) {
+    own_tokens(warp, [&](bool in, unsigned, unsigned r) {
+      if (in) atomicAdd(mine + r, 1);
+    });
+  }
   __syncthreads();
 
-  // per row: exclusive prefix over the warps; over the rows: exclusive scan
+  // per row: exclusive prefix over the sets; over the rows: exclusive scan
   const int per = (range + kSortThreads - 1) / kSortThreads;  // 1 or 2 rows per thread
   int own = 0;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r < range) {
       int run = 0;
-      for (int w = 0; w < warps; ++w) {
-        const int c = count[w * range + r];
-        count[w * range + r] = run;
-        run += c;
+      for (int w0 = 0; w0 < sets; w0 += 8) {
+        int c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < sets ? count[(w0 + w) * range + r] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w0 + w < sets) count[(w0 + w) * range + r] = run;
+          run += c[w];
+        }
       }
       last[r] = run;  // the row's count for now
       own += run;
@@ -169,8 +247,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const l
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int base = 0;
-  for (int w = 0; w < kSortWarps; ++w) base += warp_low[w] + (w < warp ? warp_sum[w] : 0);
+  int base = warp_low[lane] + (lane < warp ? warp_sum[lane] : 0);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) base += __shfl_xor_sync(0xffffffffu, base, off);
   int at = base + incl - own;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
@@ -185,44 +264,36 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const l
   __syncthreads();
   for (int r = tid; r < range; r += kSortThreads) {  // range and kSortThreads are multiples of 32
     const unsigned m = __ballot_sync(0xffffffffu, last[r] > first[r]);
-    if (lane == 0) named[(lo + r) >> 5] = m;
+    if (lane == 0) named[(self * range + r) >> 5] = m;
   }
 
-  if (warp < warps) {
-    const unsigned below = (1u << lane) - 1;
-    for (long long b = t0; b < t1; b += 32 * kSortLoads) {
-      long long t[kSortLoads];
-#pragma unroll
-      for (int k = 0; k < kSortLoads; ++k) {
-        const long long n = b + 32 * k + lane;
-        t[k] = n < t1 ? __ldg(tokens + n) : -1;
-      }
-#pragma unroll
-      for (int k = 0; k < kSortLoads; ++k) {
-        const bool in = t[k] >= lo && t[k] < hi && t[k] != ignore_index;
-        const unsigned act = __ballot_sync(0xffffffffu, in);
-        if (act == 0) continue;
-        if (in) {
-          const int r = static_cast<int>(t[k] - lo);
-          const unsigned same = __match_any_sync(act, r);
-          const int seen = mine[r];
-          __syncwarp(act);
-          if ((same & below) == 0) mine[r] = seen + __popc(same);
-          const int begin = first[r];
-          places[begin + seen + __popc(same & below)] =
-              make_int4(static_cast<int>(b + 32 * k + lane), static_cast<int>(t[k]), begin, last[r]);
-        }
-        __syncwarp();
-      }
+  // each token to its place: its row's, its set's, then its own among the set's
+  if (warp >= sets) return;
+  own_tokens(warp, [&](bool in, unsigned n, unsigned r) {
+    const unsigned act = __ballot_sync(0xffffffffu, in);
+    if (act == 0) return;
+    unsigned same = act;  // the lanes with this lane's row, bit by bit
+    for (int bit = 1; bit < range; bit <<= 1) {
+      const bool set = (r & bit) != 0;
+      const unsigned with = __ballot_sync(0xffffffffu, set);
+      same &= set ? with : ~with;
     }
-  }
+    const int seen = in ? mine[r] : 0;
+    __syncwarp();
+    if (in) {
+      if ((same & below) == 0) mine[r] = seen + __popc(same);
+      const int begin = first[r], end = last[r], at = begin + seen + __popc(same & below);
+      places[at] = make_int4(static_cast<int>(n) | (at + 1 == end ? kFlag : 0),
+                             static_cast<int>(r << shift | self) | (end - begin > kWindow ? kFlag : 0), begin, end);
+    }
+    __syncwarp();
+  });
 }
 
 // ---------------------------------------------------------------- gradient: reduce
 
-constexpr int kPlaces = 32;   // places whose chunks a CTA takes
-constexpr int kTile = 64;     // places held in shared memory
-constexpr int kDeep = 8;      // rows in flight
+constexpr int kTile = 64;  // places that a warp holds in shared memory: place b at b % kTile
+constexpr int kPer = 2;    // vectors per lane
 
 // Slot of a long row's chunk among the partial sums.  Two chunks of one row begin at
 // least kWindow places apart, and two long rows' first chunks (or two later ones)
@@ -236,190 +307,251 @@ struct ReduceParams {
   const int* total;
   const unsigned* named;
   int* arrivals;   // [windows][slices]
-  float* part;     // [2 * windows][D]
-  long long stride;
-  int V, D;
-  int slices, slice_units;
-  int reduce_ctas;
+  float* part;     // [2 * windows][units * W]
+  int stride;
+  int N, V, D;
+  int slices, slice_units;  // vectors of a slice: at most kPer per lane
+  int per_warp;             // places whose chunks a warp takes
+  unsigned warps;           // that reduce; the CTAs behind them write the zero rows
+  int shift, range;         // of the sort
+  int zero_rows;            // table rows that a CTA of those looks after: 4, 8, 16 or 32
   float scale;
 };
 
-template <int DT, bool VEC, bool ACC, int T>
-__global__ void __launch_bounds__(T) embedding_reduce_kernel(ReduceParams p,
-                                                             const typename Elem<DT>::T* __restrict__ grad_out,
-                                                             typename Elem<DT>::T* __restrict__ grad_weight) {
-  using U = Unit<DT, VEC>;
-  constexpr int W = U::W;
-  constexpr int K = VEC ? 1 : 4;  // units per thread
-  __shared__ Place tile[kTile];
-  __shared__ int is_last;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int units = p.D / W;
+// ACC: grad_weight's row is added to.  Its vectors are fetched with the row's last token --
+// EARLY, unless a vector's words can hold its neighbours' elements, which another thread
+// may be writing: those are read element by element when they are needed.
+template <int DT, bool AL, bool ACC>
+struct ReduceShape {
+  static constexpr bool EARLY = ACC && !Slot<DT, AL>::FIVE;
+  static constexpr int KINDS = EARLY ? 2 : 1;   // vectors in a stage: grad_out's, grad_weight's
+  static constexpr int STAGES = EARLY ? 6 : 12;  // tokens of the ring, all but one in flight
+  // Warps of a CTA, each working alone: one, so that none holds the room of the others that are
+  // done; four where the CTAs behind write zero rows, of which one-warp CTAs are too many.
+  static constexpr int WARPS = ACC ? 1 : 4;
+  static constexpr int BYTES = STAGES * KINDS * kPer * Slot<DT, AL>::BYTES;  // of the ring per thread
+};
 
-  if (static_cast<int>(blockIdx.x) >= p.reduce_ctas) {  // zero rows: 32 table rows, one warp per row
-    const int block = blockIdx.x - p.reduce_ctas;
-    const unsigned m = __ldg(p.named + block);
-    for (int i = threadIdx.x >> 5; i < 32; i += T / 32) {
-      const long long v = 32ll * block + i;
+template <int DT, bool AL, bool ACC>
+__global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embedding_reduce_kernel(
+    ReduceParams p, const typename Elem<DT>::T* __restrict__ grad_out, typename Elem<DT>::T* grad_weight) {
+  using S = Slot<DT, AL>;
+  using T = typename Elem<DT>::T;
+  using Shape = ReduceShape<DT, AL, ACC>;
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = Shape::STAGES, KINDS = Shape::KINDS;
+  constexpr int kWarps = Shape::WARPS, threads = 32 * kWarps;
+  extern __shared__ uint4 ring[];  // [STAGES][KINDS][kPer][threads]; then the slots' fifth words
+  __shared__ Place tiles[kWarps][kTile];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int units = (p.D + W - 1) / W;
+  const unsigned reduce_ctas = (p.warps + kWarps - 1) / kWarps;
+
+  if (blockIdx.x >= reduce_ctas) {  // zero rows, one warp per row
+    const unsigned block = blockIdx.x - reduce_ctas;
+    const unsigned owner = block & ((1u << p.shift) - 1), r0 = (block >> p.shift) * p.zero_rows;
+    const unsigned m = __ldg(p.named + (owner * p.range + r0) / 32) >> (r0 & 31);
+    for (int i = warp; i < p.zero_rows; i += kWarps) {
+      const long long v = static_cast<long long>(r0 + i) << p.shift | owner;
       if (v >= p.V || ((m >> i) & 1)) continue;
-      typename U::T* o = grad_weight + static_cast<size_t>(v) * p.D;
-      for (int u = threadIdx.x & 31; u < units; u += 32) U::store_raw(o + static_cast<size_t>(u) * W, U::zero());
+      T* const row = grad_weight + static_cast<size_t>(v) * p.D;
+      // elements up to a 128-byte line, vectors, elements
+      const int head = AL ? 0 : min(p.D, static_cast<int>((128 - (reinterpret_cast<uintptr_t>(row) & 127)) % 128 / sizeof(T)));
+      const int body = (p.D - head) / W;
+      for (int c = lane; c < head; c += 32) row[c] = Elem<DT>::put(0.f);
+      for (int u = lane; u < body; u += 32) reinterpret_cast<uint4*>(row + head)[u] = make_uint4(0, 0, 0, 0);
+      if (!AL && head + body * W + lane < p.D) row[head + body * W + lane] = Elem<DT>::put(0.f);
     }
     return;
   }
 
-  const int slice = blockIdx.x % p.slices;
-  const unsigned p0 = static_cast<unsigned>(blockIdx.x / p.slices) * kPlaces;
+  const unsigned w = blockIdx.x * kWarps + warp;
+  if (w >= p.warps) return;
+  const unsigned block = w / p.slices, p0 = block * p.per_warp;
+  const int slice = w - block * p.slices;
   const unsigned M = __ldg(p.total);
   if (p0 >= M) return;
-  unsigned tile0 = p0;
-  auto fill = [&]() {
-    for (unsigned i = threadIdx.x; i < kTile; i += T)
-      if (tile0 + i < M) tile[i] = __ldg(p.places + tile0 + i);
-    __syncthreads();
-  };
-  fill();
-  // the chunks that begin in [p0, p0 + kPlaces): the places [h0, h1)
+  // the chunks that begin in [p0, p0 + per_warp): the places [h0, h1)
   unsigned h0 = p0, h1;
   {
-    const Place e = tile[0];
-    const unsigned C = chunk_of(e.w - e.z), off = (p0 - e.z) % C;
+    const unsigned q = min(p0 + p.per_warp, M) - 1;
+    const Place e = __ldg(p.places + p0), f = __ldg(p.places + q);
+    const unsigned C = chunk_of(e.w - e.z), off = (p0 - e.z) & (C - 1);
     if (off != 0) h0 = min(p0 - off + C, static_cast<unsigned>(e.w));
-    const unsigned q = min(p0 + kPlaces, M) - 1;
     if (h0 > q) return;
-    const Place f = tile[q - p0];
     const unsigned Cq = chunk_of(f.w - f.z);
-    h1 = min(q - (q - f.z) % Cq + Cq, static_cast<unsigned>(f.w));
+    h1 = min(q - ((q - f.z) & (Cq - 1)) + Cq, static_cast<unsigned>(f.w));
   }
-  const int ubase = slice * p.slice_units;
-  const int uend = min(ubase + p.slice_units, units);
-  size_t col[K];
-  bool on[K];
+  Place* const tile = tiles[warp];
+  auto place = [&](unsigned b) { return b < M ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
+  tile[(h0 + lane) % kTile] = place(h0 + lane);
+  tile[(h0 + 32 + lane) % kTile] = place(h0 + 32 + lane);
+  Place coming = place(h0 + 64 + lane);  // takes the room of the 32 places that are done with
+  __syncwarp();
+  // this lane's vectors
+  int col[kPer], left[kPer];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int u = ubase + k * T + static_cast<int>(threadIdx.x);
-    on[k] = u < uend;
-    col[k] = static_cast<size_t>(on[k] ? u : 0) * W;
+  for (int k = 0; k < kPer; ++k) {
+    const int u = slice * p.slice_units + 32 * k + lane;
+    const bool on = 32 * k + lane < p.slice_units && u < units;
+    col[k] = on ? u * W : 0;
+    left[k] = on ? min(p.D - u * W, W) : 0;
   }
-  float acc[K][W];
+  const T* const ghi = grad_out + static_cast<long long>(p.N - 1) * p.stride + p.D;
+  const T* const whi = grad_weight + static_cast<size_t>(p.V) * p.D;
+  uint32_t* const fifth = reinterpret_cast<uint32_t*>(ring + STAGES * KINDS * kPer * threads);
+  constexpr int STEP = KINDS * kPer * threads;  // of a stage
+  auto row_of = [&](int n) { return grad_out + static_cast<long long>(n & ~kFlag) * p.stride; };
+  auto table_row = [&](int v) { return grad_weight + static_cast<long long>(v & ~kFlag) * p.D; };
+  auto issue = [&](unsigned b, int at) {
+    if (b < h1) {
+      const Place e = tile[b % kTile];
+      const T* const g = row_of(e.x);
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+      for (int k = 0; k < kPer; ++k)
+        if (left[k] > 0) S::copy(ring + at + k * threads, fifth + at + k * threads, g + col[k], left[k], grad_out, ghi);
+      if (Shape::EARLY && e.x < 0 && e.y >= 0) {
+        const T* const o = table_row(e.y);
 #pragma unroll
-    for (int i = 0; i < W; ++i) acc[k][i] = 0.f;
+        for (int k = 0; k < kPer; ++k)
+          if (left[k] > 0)
+            S::copy(ring + at + (kPer + k) * threads, fifth + at + (kPer + k) * threads, o + col[k], left[k], grad_weight,
+                    whi);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(h0 + s, s * STEP + tid);
+  int in = (STAGES - 1) * STEP + tid, out = tid;  // the ring's places of the next copy and the next read
+  F2 acc[kPer][H];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+#pragma unroll
+    for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
 
-  for (unsigned b = h0; b < h1; b += kDeep) {
-    if (b + kDeep > tile0 + kTile) {
-      __syncthreads();
-      tile0 = b;
-      fill();
+  for (unsigned b = h0; b < h1; ++b) {
+    if (((b - h0) & 31) == 0 && b != h0) {
+      __syncwarp();
+      tile[(b + 32 + lane) % kTile] = coming;
+      coming = place(b + 64 + lane);
+      __syncwarp();
     }
-    typename U::Raw g[kDeep][K], old[ACC ? kDeep : 1][K];
+    issue(b + STAGES - 1, in);
+    in = in + STEP < STAGES * STEP ? in + STEP : tid;
+    const int at = out;
+    out = out + STEP < STAGES * STEP ? out + STEP : tid;
+    copy_wait<STAGES - 1>();
+    const Place e = tile[b % kTile];
+    const bool gshift = S::shifted(row_of(e.x));
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      if (b + j < h1) {
-        const Place e = tile[b + j - tile0];
-        const typename U::T* row = grad_out + e.x * p.stride;
+    for (int k = 0; k < kPer; ++k) {
+      F2 v[H];
+      unpack2<DT, W>(S::read(ring + at + k * threads, fifth + at + k * threads, gshift, left[k]), v);
 #pragma unroll
-        for (int k = 0; k < K; ++k) g[j][k] = on[k] ? U::load(row + col[k]) : U::zero();
-        if (ACC && b + j + 1 == static_cast<unsigned>(e.w) && e.w - e.z <= kWindow) {
-          const typename U::T* o = grad_weight + static_cast<size_t>(e.y) * p.D;
-#pragma unroll
-          for (int k = 0; k < K; ++k)
-            old[ACC ? j : 0][k] = on[k] ? *reinterpret_cast<const typename U::Raw*>(o + col[k]) : U::zero();
-        }
-      }
+      for (int i = 0; i < H; ++i) acc[k][i] = add2(acc[k][i], v[i]);
     }
+    bool ends = e.x < 0, write = ends;
+    if (__builtin_expect(e.y < 0, 0)) {  // a long row: its chunks' sums meet in memory
+      const unsigned begin = e.z, end = e.w, count = end - begin;
+      const unsigned C = chunk_of(count);
+      ends = ends || ((b + 1 - begin) & (C - 1)) == 0;
+      write = false;
+      if (ends) {
+        const unsigned head = b - ((b - begin) & (C - 1));
+        float* const part = p.part + slot_of(head, head == begin) * units * W;
 #pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-      const unsigned at = b + j;
-      if (at >= h1) break;
-      const Place e = tile[at - tile0];
-      const unsigned begin = e.z, end = e.w;
-      const unsigned C = chunk_of(e.w - e.z);
+        for (int k = 0; k < kPer; ++k)
+          if (left[k] > 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        float v[W];
-        U::unpack(g[j][k], v);
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[k][i] += v[i];
-      }
-      const bool row_ends = at + 1 == end;
-      if (!row_ends && (at + 1 - begin) % C != 0) continue;
-      typename U::T* o = grad_weight + static_cast<size_t>(e.y) * p.D;
-      bool write = end - begin <= C;
-      if (!write) {  // a chunk of a long row
-        const unsigned head = at - (at - begin) % C;
-        float* part = p.part + slot_of(head, head == begin) * p.D;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            if (on[k]) part[col[k] + i] = acc[k][i];
-        const int chunks = (end - begin + C - 1) / C;
+            for (int i = 0; i < H; i += 2)
+              reinterpret_cast<float4*>(part + col[k])[i / 2] =
+                  make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+          }
+        const int chunks = (count + C - 1) / C;
         __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-          is_last = atomicAdd(p.arrivals + static_cast<long long>(begin / kWindow) * p.slices + slice, 1) == chunks - 1;
-        __syncthreads();
-        write = is_last;
-        if (write) {
+        __syncwarp();
+        int before = 0;
+        if (lane == 0)
+          before = atomicAdd(p.arrivals + static_cast<long long>(begin / kWindow) * p.slices + slice, 1);
+        write = __shfl_sync(0xffffffffu, before, 0) == chunks - 1;
+        if (write) {  // the warp that came last adds them, in ascending order, four loads at a time
           __threadfence();
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+          for (int k = 0; k < kPer; ++k)
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[k][i] = 0.f;
-          for (int c = 0; c < chunks; ++c) {
-            const float* q = p.part + slot_of(begin + c * C, c == 0) * p.D;
+            for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+          for (int k = 0; k < kPer; ++k) {
+            const float* const q = p.part + col[k];
+            for (int c0 = 0; c0 < chunks; c0 += 8) {
+              float4 v[8][H / 2];
 #pragma unroll
-              for (int i = 0; i < W; ++i)
-                if (on[k]) acc[k][i] += __ldcg(q + col[k] + i);
+              for (int c = 0; c < 8; ++c) {
+                const int at = min(c0 + c, chunks - 1);
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i)
+                  v[c][i] = __ldcg(reinterpret_cast<const float4*>(q + slot_of(begin + at * C, at == 0) * units * W) + i);
+              }
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                if (c0 + c < chunks) {
+#pragma unroll
+                  for (int i = 0; i < H / 2; ++i) {
+                    acc[k][2 * i] = add2(acc[k][2 * i], f2(v[c][i].x, v[c][i].y));
+                    acc[k][2 * i + 1] = add2(acc[k][2 * i + 1], f2(v[c][i].z, v[c][i].w));
+                  }
+                }
+              }
+            }
           }
         }
       }
-      if (write) {
+    }
+    if (write) {
+      T* const o = table_row(e.y);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (!on[k]) continue;
-          float v[W];
-          if (ACC) {
-            U::unpack(end - begin <= C ? old[ACC ? j : 0][k] : *reinterpret_cast<const typename U::Raw*>(o + col[k]), v);
+      for (int k = 0; k < kPer; ++k) {
+        if (left[k] <= 0) continue;
+        F2 v[H];
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = fmaf(p.scale, acc[k][i], v[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = p.scale * acc[k][i];
-          }
-          U::store(o + col[k], v);
+        for (int i = 0; i < H; ++i) v[i] = f2(0.f);
+        if (ACC) {
+          uint4 old;
+          if (Shape::EARLY && e.y >= 0)
+            old = S::read(ring + at + (kPer + k) * threads, fifth + at + (kPer + k) * threads, false, left[k]);
+          else
+            old = S::load_changed(o + col[k], left[k]);
+          unpack2<DT, W>(old, v);
         }
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = ACC ? fma2(acc[k][i], f2(p.scale), v[i]) : mul2(acc[k][i], f2(p.scale));
+        S::store(o + col[k], pack2<DT, W>(v), left[k]);
       }
+    }
+    if (ends) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int k = 0; k < kPer; ++k)
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[k][i] = 0.f;
+        for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
     }
   }
+  copy_wait<0>();
 }
 
 // ---------------------------------------------------------------- launches
 
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Column slices of the reduce launch: T threads, one vector or four elements each.
-int slices_of(int units, int per_cta) { return (units + per_cta - 1) / per_cta; }
-
 struct BwdLayout {
   size_t places, named, total, arrivals, part, bytes;
-  long long windows;
+  long long windows, num_arrivals;
 };
-
-// Columns of the narrowest slice of any type and alignment (one slice when rows have fewer).
-constexpr int kMinSlice = 512;
 
 BwdLayout bwd_layout(long long N, long long V, long long D) {
   BwdLayout L;
   L.windows = (N + kWindow - 1) / kWindow;
+  L.num_arrivals = L.windows * ((D + 255) / 256);  // slices have 256 columns (fp32) or 512
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -427,107 +559,133 @@ BwdLayout bwd_layout(long long N, long long V, long long D) {
     return here;
   };
   L.places = take(static_cast<size_t>(N) * sizeof(Place));
-  L.named = take((static_cast<size_t>(V) / 32 + kSortMaxRange) * sizeof(unsigned));
+  const SortPlan sp = sort_plan(N, V);
+  L.named = take(static_cast<size_t>(sp.owners) * (sp.range / 32) * sizeof(unsigned));
   L.total = take(sizeof(int));
-  L.arrivals = take(static_cast<size_t>(L.windows) * ((D + kMinSlice - 1) / kMinSlice) * sizeof(int));
-  L.part = take(static_cast<size_t>(L.windows) * 2 * D * sizeof(float));
+  L.arrivals = take(static_cast<size_t>(L.num_arrivals) * sizeof(int));
+  L.part = take(static_cast<size_t>(L.windows) * 2 * ((D + 7) / 8 * 8) * sizeof(float));
   L.bytes = at;
   return L;
 }
 
-template <int DT, bool VEC>
+template <int DT, bool AL>
 cudaError_t fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStream_t s) {
-  using U = Unit<DT, VEC>;
-  const int units = p.D / U::W;
+  using T = typename Elem<DT>::T;
+  const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
   const int chunks = (units + 32 * kFwdLoads - 1) / (32 * kFwdLoads);
   const dim3 grid((p.N + kFwdWarps - 1) / kFwdWarps, chunks);
-  embedding_fwd_kernel<DT, VEC><<<grid, 32 * kFwdWarps, 0, s>>>(
-      p.tokens, static_cast<const typename U::T*>(weight), p.N, p.V, p.D, (units + chunks - 1) / chunks, p.scale,
-      p.ignore_index, static_cast<typename U::T*>(out));
+  embedding_fwd_kernel<DT, AL><<<grid, 32 * kFwdWarps, 0, s>>>(p.tokens, static_cast<const T*>(weight), p.N, p.V, p.D,
+                                                               (units + chunks - 1) / chunks, p.scale, p.ignore_index,
+                                                               static_cast<T*>(out));
   return launch_result();
 }
 
-template <int DT, bool VEC, bool ACC, int T>
-cudaError_t reduce(ReduceParams r, long long N, int units, const void* grad_out, void* grad_weight, cudaStream_t s) {
-  using Te = typename Elem<DT>::T;
-  r.slices = slices_of(units, VEC ? T : 4 * T);
+template <int DT, bool AL, bool ACC>
+cudaError_t reduce(ReduceParams r, const void* grad_out, void* grad_weight, cudaStream_t s) {
+  using T = typename Elem<DT>::T;
+  const int units = (r.D + Elem<DT>::W - 1) / Elem<DT>::W;
+  r.slices = (units + 32 * kPer - 1) / (32 * kPer);
   r.slice_units = (units + r.slices - 1) / r.slices;
-  r.reduce_ctas = static_cast<int>((N + kPlaces - 1) / kPlaces * r.slices);
+  // Places per warp: 16, or 8 where that leaves too few warps (16384 x 4096, accumulating: 50.1
+  // us with 8, 54 with 16; 65600 x 2688: 123 and 117).
+  using Shape = ReduceShape<DT, AL, ACC>;
+  r.per_warp = (r.N + 15) / 16 * static_cast<long long>(r.slices) < 152 * (ACC ? 64 : 32) ? 8 : 16;
+  r.warps = static_cast<unsigned>((static_cast<long long>(r.N) + r.per_warp - 1) / r.per_warp * r.slices);
+  // about 32 KB of zeros per CTA: with 128 KB the last of few CTAs had the GPU to themselves
+  r.zero_rows = 32;
+  while (r.zero_rows > 4 && static_cast<long long>(r.zero_rows) * r.D * elem_bytes(DT) > 48 * 1024) r.zero_rows /= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(r.reduce_ctas + (ACC ? 0 : (r.V + 31) / 32));
-  cfg.blockDim = dim3(T);
+  cfg.gridDim = dim3((r.warps + Shape::WARPS - 1) / Shape::WARPS + (ACC ? 0 : r.range / r.zero_rows << r.shift));
+  cfg.blockDim = dim3(32 * Shape::WARPS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(32 * Shape::WARPS) * Shape::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return note_cuda(cudaLaunchKernelEx(&cfg, embedding_reduce_kernel<DT, VEC, ACC, T>, r,
-                                      static_cast<const Te*>(grad_out), static_cast<Te*>(grad_weight)));
+  return note_cuda(cudaLaunchKernelEx(&cfg, embedding_reduce_kernel<DT, AL, ACC>, r, static_cast<const T*>(grad_out),
+                                      static_cast<T*>(grad_weight)));
 }
 
-template <int DT, bool VEC>
-cudaError_t reduce_any(const ReduceParams& r, long long N, bool accumulate, const void* grad_out, void* grad_weight,
+template <int DT>
+cudaError_t reduce_any(const ReduceParams& r, bool al, bool accumulate, const void* grad_out, void* grad_weight,
                        cudaStream_t s) {
-  const int units = r.D / Unit<DT, VEC>::W;
-  // rows of few units take one-warp CTAs
-  if (units <= (VEC ? 32 : 128))
-    return accumulate ? reduce<DT, VEC, true, 32>(r, N, units, grad_out, grad_weight, s)
-                      : reduce<DT, VEC, false, 32>(r, N, units, grad_out, grad_weight, s);
-  return accumulate ? reduce<DT, VEC, true, 128>(r, N, units, grad_out, grad_weight, s)
-                    : reduce<DT, VEC, false, 128>(r, N, units, grad_out, grad_weight, s);
+  if (al)
+    return accumulate ? reduce<DT, true, true>(r, grad_out, grad_weight, s)
+                      : reduce<DT, true, false>(r, grad_out, grad_weight, s);
+  return accumulate ? reduce<DT, false, true>(r, grad_out, grad_weight, s)
+                    : reduce<DT, false, false>(r, grad_out, grad_weight, s);
+}
+
+template <int DT>
+cudaError_t allow() {
+  const void* const kernels[4] = {reinterpret_cast<const void*>(embedding_reduce_kernel<DT, true, true>),
+                                  reinterpret_cast<const void*>(embedding_reduce_kernel<DT, true, false>),
+                                  reinterpret_cast<const void*>(embedding_reduce_kernel<DT, false, true>),
+                                  reinterpret_cast<const void*>(embedding_reduce_kernel<DT, false, false>)};
+  for (const void* k : kernels) {
+    const cudaError_t e = note_cuda(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t embedding_setup() {
-  const int bytes = kSortMaxRange * (kSortWarps + 2) * static_cast<int>(sizeof(int));
-  return note_cuda(cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  cudaError_t e = note_cuda(cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kSortSmem));
+  if (e == cudaSuccess) e = allow<kDtypeBF16>();
+  if (e == cudaSuccess) e = allow<kDtypeF32>();
+  if (e == cudaSuccess) e = allow<kDtypeF16>();
+  return e;
 }
 
 size_t embedding_bwd_workspace(long long N, long long V, long long D) { return bwd_layout(N, V, D).bytes; }
 
 cudaError_t launch_embedding_fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStream_t s) {
-  const bool vec = aligned16(weight) && aligned16(out) && (static_cast<long long>(p.D) * elem_bytes(p.dtype)) % 16 == 0;
-  if (p.dtype == kDtypeBF16) return vec ? fwd<kDtypeBF16, true>(p, weight, out, s) : fwd<kDtypeBF16, false>(p, weight, out, s);
-  if (p.dtype == kDtypeF16) return vec ? fwd<kDtypeF16, true>(p, weight, out, s) : fwd<kDtypeF16, false>(p, weight, out, s);
-  return vec ? fwd<kDtypeF32, true>(p, weight, out, s) : fwd<kDtypeF32, false>(p, weight, out, s);
+  const bool al = aligned16(weight) && aligned16(out) && (static_cast<long long>(p.D) * elem_bytes(p.dtype)) % 16 == 0;
+  if (p.dtype == kDtypeBF16)
+    return al ? fwd<kDtypeBF16, true>(p, weight, out, s) : fwd<kDtypeBF16, false>(p, weight, out, s);
+  if (p.dtype == kDtypeF16)
+    return al ? fwd<kDtypeF16, true>(p, weight, out, s) : fwd<kDtypeF16, false>(p, weight, out, s);
+  return al ? fwd<kDtypeF32, true>(p, weight, out, s) : fwd<kDtypeF32, false>(p, weight, out, s);
 }
 
 cudaError_t launch_embedding_bwd(const EmbeddingParams& p, const void* grad_out, long long stride, int accumulate,
                                  void* grad_weight, void* workspace, cudaStream_t s) {
   const BwdLayout L = bwd_layout(p.N, p.V, p.D);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
   const int es = elem_bytes(p.dtype);
-  const bool vec = aligned16(grad_out) && aligned16(grad_weight) && (static_cast<long long>(p.D) * es) % 16 == 0 &&
-                   (stride * es) % 16 == 0;
+  const bool al = aligned16(grad_out) && aligned16(grad_weight) && (static_cast<long long>(p.D) * es) % 16 == 0 &&
+                  (stride * es) % 16 == 0;
   const SortPlan sp = sort_plan(p.N, p.V);
-  ReduceParams r = {};
-  r.places = reinterpret_cast<Place*>(ws + L.places);
-  r.named = reinterpret_cast<unsigned*>(ws + L.named);
-  r.total = reinterpret_cast<int*>(ws + L.total);
-  r.arrivals = reinterpret_cast<int*>(ws + L.arrivals);
-  r.part = reinterpret_cast<float*>(ws + L.part);
-  r.stride = stride;
-  r.V = p.V;
-  r.D = p.D;
-  r.scale = p.scale;
-  const int num_arrivals = static_cast<int>(L.windows * ((p.D + kMinSlice - 1) / kMinSlice));
-  embedding_sort_kernel<<<sp.owners, kSortThreads, sp.smem, s>>>(
-      p.tokens, p.N, p.V, p.ignore_index, sp.range, sp.warps, sp.span, reinterpret_cast<Place*>(ws + L.places),
-      reinterpret_cast<unsigned*>(ws + L.named), reinterpret_cast<int*>(ws + L.arrivals), num_arrivals,
-      reinterpret_cast<int*>(ws + L.total));
+  Place* const places = reinterpret_cast<Place*>(ws + L.places);
+  unsigned* const named = reinterpret_cast<unsigned*>(ws + L.named);
+  int* const total = reinterpret_cast<int*>(ws + L.total);
+  int* const arrivals = reinterpret_cast<int*>(ws + L.arrivals);
+  embedding_sort_kernel<<<sp.owners, kSortThreads, sp.smem, s>>>(p.tokens, p.N, p.V, p.ignore_index, sp.shift,
+                                                                 sp.range, sp.warps, sp.span, sp.list, places, named, arrivals,
+                                                                 static_cast<int>(L.num_arrivals), total);
   const cudaError_t e = launch_result();
   if (e != cudaSuccess) return e;
-  const bool acc = accumulate != 0;
-  if (p.dtype == kDtypeBF16)
-    return vec ? reduce_any<kDtypeBF16, true>(r, p.N, acc, grad_out, grad_weight, s)
-               : reduce_any<kDtypeBF16, false>(r, p.N, acc, grad_out, grad_weight, s);
-  if (p.dtype == kDtypeF16)
-    return vec ? reduce_any<kDtypeF16, true>(r, p.N, acc, grad_out, grad_weight, s)
-               : reduce_any<kDtypeF16, false>(r, p.N, acc, grad_out, grad_weight, s);
-  return vec ? reduce_any<kDtypeF32, true>(r, p.N, acc, grad_out, grad_weight, s)
-             : reduce_any<kDtypeF32, false>(r, p.N, acc, grad_out, grad_weight, s);
+  ReduceParams r = {};
+  r.places = places;
+  r.total = total;
+  r.named = named;
+  r.arrivals = arrivals;
+  r.part = reinterpret_cast<float*>(ws + L.part);
+  r.stride = static_cast<int>(stride);
+  r.N = p.N;
+  r.V = p.V;
+  r.D = p.D;
+  r.shift = sp.shift;
+  r.range = sp.range;
+  r.scale = p.scale;
+  if (p.dtype == kDtypeBF16) return reduce_any<kDtypeBF16>(r, al, accumulate != 0, grad_out, grad_weight, s);
+  if (p.dtype == kDtypeF16) return reduce_any<kDtypeF16>(r, al, accumulate != 0, grad_out, grad_weight, s);
+  return reduce_any<kDtypeF32>(r, al, accumulate != 0, grad_out, grad_weight, s);
 }
 
 }  // namespace llp
