@@ -185,17 +185,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < 2 * D) {
-#pragma unroll 8
-    for (int i = warp; i < parts; i += kJoinWarps) s += __ldcg(part + static_cast<size_t>(i) * 2 * D + c);
-  }
+  // the loads go out together: a part past the end is read again and not added
+  constexpr int MOST = (kPipeSMs + kJoinWarps - 1) / kJoinWarps;
+  float v[MOST], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    v[i] = __ldcg(part + static_cast<size_t>(min(warp + i * kJoinWarps, parts - 1)) * 2 * D + min(c, 2 * D - 1));
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    if (warp + i * kJoinWarps < parts) s += v[i];
   sm[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= 2 * D) return;
-  s = sm[0][lane];
+  s = 0.f;
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) s += sm[w][lane];
+  for (int w = 0; w < kJoinWarps; ++w) s += sm[w][lane];
   if (c < D) {
     if (gw != nullptr) gw[c] = Elem<PT>::put(s);
   } else {
