@@ -7,6 +7,10 @@
 // element halve the generator's work: 32 would cost 40 wide multiplies per eight
 // elements, about what the multiplier pipe can do in the time their 32 bytes
 // take through HBM.
+//
+// Bound by memory.  Measured, bf16: 16384 x 2688 with a residual 38.4 us (6.9 TB/s, the
+// measured copy peak), without one 30.0 (5.9 TB/s, 87%); 65600 x 2688 without one 112.5
+// (6.3 TB/s, 93%).
 #include "elem.cuh"
 
 namespace llp {

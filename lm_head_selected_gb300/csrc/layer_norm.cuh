@@ -6,7 +6,6 @@
 namespace llp {
 
 // A row is D elements in `units` 16-byte vectors of W; the last one may be ragged.
-
 // AL: rows are whole vectors, 16-byte aligned, and so are the parameters (a template
 // parameter: as a run-time flag it cost the aligned kernels the predicated-off
 // instructions of the other form, 1.5 times the time).

@@ -18,8 +18,8 @@
 // (contiguous ranges instead: 190 us).  A second launch joins the CTAs' column sums in
 // ascending order.  Rows beyond 1024 vectors take three plain kernels.
 //
-// Measured, bf16, three tensors of traffic: 16384 x 4096 68 us (5.9 TB/s, 87% of the
-// measured copy peak), 65600 x 2688 171 us (91%), 16384 x 2688 51 us (76%: 5 us are the
+// Measured, bf16, three tensors of traffic: 16384 x 4096 67.4 us (6.0 TB/s, 88% of the
+// measured copy peak), 65600 x 2688 170 us (92%), 16384 x 2688 50.4 us (77%: 5 us are the
 // join and the two launches' ends).
 #include "layer_norm.cuh"
 
@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
 constexpr int kJoinWarps = 32;
 
 template <int PT>
-__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ part, int parts, int D,
-                                                              typename Elem<PT>::T* __restrict__ gw,
-                                                              typename Elem<PT>::T* __restrict__ gb) {
+__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ part, int parts,
+                                                                          int D, typename Elem<PT>::T* __restrict__ gw,
+                                                                          typename Elem<PT>::T* __restrict__ gb) {
   __shared__ float sm[kJoinWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -9,9 +9,9 @@
 // Rows beyond 1024 vectors are read three times by one CTA each (from L2 after the
 // first).
 //
-// Bound by memory, both ways.  Measured, bf16: 16384 x 2688 30.2 us (5.8 TB/s, 86% of
+// Bound by memory, both ways.  Measured, bf16: 16384 x 2688 29.9 us (5.9 TB/s, 87% of
 // the measured copy peak; an elementwise kernel of the same traffic takes 30.0), 65600 x
-// 2688 112 us (93%).  One vector per thread, with six warps to a row, took 36.4 us, one
+// 2688 111 us (94%).  One vector per thread, with six warps to a row, took 36.4 us, one
 // warp to a row with eleven 32.6, contiguous ranges of rows 31.1 and 121.
 #include "layer_norm.cuh"
 
