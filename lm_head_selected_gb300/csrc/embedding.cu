@@ -325,7 +325,8 @@ template <int DT, bool AL, bool ACC>
 struct ReduceShape {
   static constexpr bool EARLY = ACC && !Slot<DT, AL>::FIVE;
   static constexpr int KINDS = EARLY ? 2 : 1;   // vectors in a stage: grad_out's, grad_weight's
-  static constexpr int STAGES = EARLY ? 6 : 12;  // tokens of the ring, all but one in flight
+  static constexpr int STAGES = EARLY ? 6 : 12;  // tokens of the ring
+  static constexpr int BATCH = STAGES / 3;       // of a long run added together, the others in flight
   // Warps of a CTA, each working alone: one, so that none holds the room of the others that are
   // done; four where the CTAs behind write zero rows, of which one-warp CTAs are too many.
   static constexpr int WARPS = ACC ? 1 : 4;
@@ -390,10 +391,11 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
   __syncwarp();
   // this lane's vectors
   int col[kPer], left[kPer];
+  const int here = min(p.slice_units, units - slice * p.slice_units);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int u = slice * p.slice_units + 32 * k + lane;
-    const bool on = 32 * k + lane < p.slice_units && u < units;
+    const bool on = 32 * k + lane < here;
     col[k] = on ? u * W : 0;
     left[k] = on ? min(p.D - u * W, W) : 0;
   }
@@ -422,28 +424,22 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
     copy_commit();
   };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(h0 + s, s * STEP + tid);
-  int in = (STAGES - 1) * STEP + tid, out = tid;  // the ring's places of the next copy and the next read
-  F2 acc[kPer][H];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-#pragma unroll
-    for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
-
-  for (unsigned b = h0; b < h1; ++b) {
-    if (((b - h0) & 31) == 0 && b != h0) {
+  for (int s = 0; s < STAGES; ++s) issue(h0 + s, s * STEP + tid);
+  int out = tid;       // the ring's place of b
+  unsigned base = h0;  // places [base, base + kTile) are in the tile
+  auto step = [&](int at) { return at + STEP < STAGES * STEP ? at + STEP : at + STEP - STAGES * STEP; };
+  auto refill = [&](unsigned b) {
+    if (b - base >= 32) {
       __syncwarp();
-      tile[(b + 32 + lane) % kTile] = coming;
-      coming = place(b + 64 + lane);
+      tile[(base + kTile + lane) % kTile] = coming;
+      base += 32;
+      coming = place(base + kTile + lane);
       __syncwarp();
     }
-    issue(b + STAGES - 1, in);
-    in = in + STEP < STAGES * STEP ? in + STEP : tid;
-    const int at = out;
-    out = out + STEP < STAGES * STEP ? out + STEP : tid;
-    copy_wait<STAGES - 1>();
-    const Place e = tile[b % kTile];
-    const bool gshift = S::shifted(row_of(e.x));
+  };
+  F2 acc[kPer][H];
+  auto add = [&](unsigned b, int at) {
+    const bool gshift = S::FIVE && S::shifted(row_of(tile[b % kTile].x));
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       F2 v[H];
@@ -451,89 +447,113 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
 #pragma unroll
       for (int i = 0; i < H; ++i) acc[k][i] = add2(acc[k][i], v[i]);
     }
-    bool ends = e.x < 0, write = ends;
-    if (__builtin_expect(e.y < 0, 0)) {  // a long row: its chunks' sums meet in memory
-      const unsigned begin = e.z, end = e.w, count = end - begin;
-      const unsigned C = chunk_of(count);
-      ends = ends || ((b + 1 - begin) & (C - 1)) == 0;
-      write = false;
-      if (ends) {
-        const unsigned head = b - ((b - begin) & (C - 1));
-        float* const part = p.part + slot_of(head, head == begin) * units * W;
+  };
+
+  // One run of places, a row's or a long row's chunk, at a time; h1 is the end of one.
+  for (unsigned b = h0; b < h1;) {
+    const Place e = tile[b % kTile];
+    const unsigned head = b, begin = e.z, end = e.w;
+    const bool cut = e.y < 0;
+    const unsigned C = cut ? chunk_of(end - begin) : 0;
+    const unsigned stop = cut ? min(end, b + C) : end;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+#pragma unroll
+      for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
+    // several places together while there are: one after another, the instructions of a place
+    // wait for one another
+    while (b + Shape::BATCH < stop) {
+      copy_wait<STAGES - Shape::BATCH>();
+      int at = out;
+#pragma unroll
+      for (int j = 0; j < Shape::BATCH; ++j) {
+        add(b + j, at);
+        at = step(at);
+      }
+      at = out;
+#pragma unroll
+      for (int j = 0; j < Shape::BATCH; ++j) {
+        issue(b + STAGES + j, at);
+        at = step(at);
+      }
+      out = at;
+      b += Shape::BATCH;
+      refill(b);
+    }
+    uint4 old[kPer];
+    for (; b < stop; ++b) {
+      copy_wait<STAGES - 1>();
+      add(b, out);
+      if (Shape::EARLY && b + 1 == stop) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
-          if (left[k] > 0) {
+          old[k] = S::read(ring + out + (kPer + k) * threads, fifth + out + (kPer + k) * threads, false, left[k]);
+      }
+      issue(b + STAGES, out);
+      out = step(out);
+      refill(b + 1);
+    }
+    if (__builtin_expect(cut, 0)) {  // the chunks' sums meet in memory
+      float* const part = p.part + slot_of(head, head == begin) * units * W;
 #pragma unroll
-            for (int i = 0; i < H; i += 2)
-              reinterpret_cast<float4*>(part + col[k])[i / 2] =
-                  make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+      for (int k = 0; k < kPer; ++k)
+        if (left[k] > 0) {
+#pragma unroll
+          for (int i = 0; i < H; i += 2)
+            reinterpret_cast<float4*>(part + col[k])[i / 2] =
+                make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+        }
+      const int chunks = (end - begin + C - 1) / C;
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0)
+        before = atomicAdd(p.arrivals + static_cast<long long>(begin / kWindow) * p.slices + slice, 1);
+      if (__shfl_sync(0xffffffffu, before, 0) != chunks - 1) continue;
+      // the warp that came last adds them, in ascending order, eight loads at a time
+      __threadfence();
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
+        if (32 * k >= here) continue;
+        const float* const q = p.part + col[k];
+        for (int c0 = 0; c0 < chunks; c0 += 8) {
+          float4 v[8][H / 2];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int at = min(c0 + c, chunks - 1);
+#pragma unroll
+            for (int i = 0; i < H / 2; ++i)
+              v[c][i] = __ldcg(reinterpret_cast<const float4*>(q + slot_of(begin + at * C, at == 0) * units * W) + i);
           }
-        const int chunks = (count + C - 1) / C;
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0)
-          before = atomicAdd(p.arrivals + static_cast<long long>(begin / kWindow) * p.slices + slice, 1);
-        write = __shfl_sync(0xffffffffu, before, 0) == chunks - 1;
-        if (write) {  // the warp that came last adds them, in ascending order, four loads at a time
-          __threadfence();
 #pragma unroll
-          for (int k = 0; k < kPer; ++k)
+          for (int c = 0; c < 8; ++c) {
+            if (c0 + c < chunks) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const float* const q = p.part + col[k];
-            for (int c0 = 0; c0 < chunks; c0 += 8) {
-              float4 v[8][H / 2];
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const int at = min(c0 + c, chunks - 1);
-#pragma unroll
-                for (int i = 0; i < H / 2; ++i)
-                  v[c][i] = __ldcg(reinterpret_cast<const float4*>(q + slot_of(begin + at * C, at == 0) * units * W) + i);
-              }
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                if (c0 + c < chunks) {
-#pragma unroll
-                  for (int i = 0; i < H / 2; ++i) {
-                    acc[k][2 * i] = add2(acc[k][2 * i], f2(v[c][i].x, v[c][i].y));
-                    acc[k][2 * i + 1] = add2(acc[k][2 * i + 1], f2(v[c][i].z, v[c][i].w));
-                  }
-                }
+              for (int i = 0; i < H / 2; ++i) {
+                acc[k][2 * i] = add2(acc[k][2 * i], f2(v[c][i].x, v[c][i].y));
+                acc[k][2 * i + 1] = add2(acc[k][2 * i + 1], f2(v[c][i].z, v[c][i].w));
               }
             }
           }
         }
       }
     }
-    if (write) {
-      T* const o = table_row(e.y);
+    T* const o = table_row(e.y);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (left[k] <= 0) continue;
-        F2 v[H];
+    for (int k = 0; k < kPer; ++k) {
+      if (left[k] <= 0) continue;
+      F2 v[H];
 #pragma unroll
-        for (int i = 0; i < H; ++i) v[i] = f2(0.f);
-        if (ACC) {
-          uint4 old;
-          if (Shape::EARLY && e.y >= 0)
-            old = S::read(ring + at + (kPer + k) * threads, fifth + at + (kPer + k) * threads, false, left[k]);
-          else
-            old = S::load_changed(o + col[k], left[k]);
-          unpack2<DT, W>(old, v);
-        }
-#pragma unroll
-        for (int i = 0; i < H; ++i) v[i] = ACC ? fma2(acc[k][i], f2(p.scale), v[i]) : mul2(acc[k][i], f2(p.scale));
-        S::store(o + col[k], pack2<DT, W>(v), left[k]);
+      for (int i = 0; i < H; ++i) v[i] = f2(0.f);
+      if (ACC) {
+        if (!Shape::EARLY || cut) old[k] = S::load_changed(o + col[k], left[k]);
+        unpack2<DT, W>(old[k], v);
       }
-    }
-    if (ends) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-#pragma unroll
-        for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
+      for (int i = 0; i < H; ++i) v[i] = ACC ? fma2(acc[k][i], f2(p.scale), v[i]) : mul2(acc[k][i], f2(p.scale));
+      S::store(o + col[k], pack2<DT, W>(v), left[k]);
     }
   }
   copy_wait<0>();
