@@ -326,7 +326,7 @@ struct ReduceShape {
   static constexpr bool EARLY = ACC && !Slot<DT, AL>::FIVE;
   static constexpr int KINDS = EARLY ? 2 : 1;   // vectors in a stage: grad_out's, grad_weight's
   static constexpr int STAGES = EARLY ? 6 : 12;  // tokens of the ring
-  static constexpr int BATCH = STAGES / 3;       // of a long run added together, the others in flight
+  static constexpr int BATCH = EARLY ? 3 : 4;    // of a long run added together, the others in flight
   // Warps of a CTA, each working alone: one, so that none holds the room of the others that are
   // done; four where the CTAs behind write zero rows, of which one-warp CTAs are too many.
   static constexpr int WARPS = ACC ? 1 : 4;
@@ -370,24 +370,28 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
   if (w >= p.warps) return;
   const unsigned block = w / p.slices, p0 = block * p.per_warp;
   const int slice = w - block * p.slices;
+  // The first places, read without waiting for their number: those past it hold nothing yet.
   const unsigned M = __ldg(p.total);
+  auto raw_place = [&](unsigned b) { return b < static_cast<unsigned>(p.N) ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
+  auto place = [&](unsigned b) { return b < M ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
+  const Place first = raw_place(p0 + lane), second = raw_place(p0 + 32 + lane);
+  Place coming = raw_place(p0 + kTile + lane);  // takes the room of the 32 places that are done with
   if (p0 >= M) return;
+  Place* const tile = tiles[warp];
+  tile[(p0 + lane) % kTile] = first;
+  tile[(p0 + 32 + lane) % kTile] = second;
   // the chunks that begin in [p0, p0 + per_warp): the places [h0, h1)
   unsigned h0 = p0, h1;
   {
     const unsigned q = min(p0 + p.per_warp, M) - 1;
-    const Place e = __ldg(p.places + p0), f = __ldg(p.places + q);
-    const unsigned C = chunk_of(e.w - e.z), off = (p0 - e.z) & (C - 1);
-    if (off != 0) h0 = min(p0 - off + C, static_cast<unsigned>(e.w));
+    const unsigned e_begin = __shfl_sync(0xffffffffu, first.z, 0), e_end = __shfl_sync(0xffffffffu, first.w, 0);
+    const unsigned f_begin = __shfl_sync(0xffffffffu, first.z, q - p0), f_end = __shfl_sync(0xffffffffu, first.w, q - p0);
+    const unsigned C = chunk_of(e_end - e_begin), off = (p0 - e_begin) & (C - 1);
+    if (off != 0) h0 = min(p0 - off + C, e_end);
     if (h0 > q) return;
-    const unsigned Cq = chunk_of(f.w - f.z);
-    h1 = min(q - ((q - f.z) & (Cq - 1)) + Cq, static_cast<unsigned>(f.w));
+    const unsigned Cq = chunk_of(f_end - f_begin);
+    h1 = min(q - ((q - f_begin) & (Cq - 1)) + Cq, f_end);
   }
-  Place* const tile = tiles[warp];
-  auto place = [&](unsigned b) { return b < M ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
-  tile[(h0 + lane) % kTile] = place(h0 + lane);
-  tile[(h0 + 32 + lane) % kTile] = place(h0 + 32 + lane);
-  Place coming = place(h0 + 64 + lane);  // takes the room of the 32 places that are done with
   __syncwarp();
   // this lane's vectors
   int col[kPer], left[kPer];
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) issue(h0 + s, s * STEP + tid);
   int out = tid;       // the ring's place of b
-  unsigned base = h0;  // places [base, base + kTile) are in the tile
+  unsigned base = p0;  // places [base, base + kTile) are in the tile
   auto step = [&](int at) { return at + STEP < STAGES * STEP ? at + STEP : at + STEP - STAGES * STEP; };
   auto refill = [&](unsigned b) {
     if (b - base >= 32) {
