@@ -11,8 +11,8 @@
  *
  * The gradient sorts the tokens and sums each table row's tokens in ascending
  * token order in fp32, with one rounding to the table's type.  A row named
- * more than 32 times is summed in pieces whose length depends on that count
- * alone, joined in ascending order.  A row of the gradient therefore depends
+ * more than 32 times is summed in pieces, and groups of pieces, whose lengths
+ * depend on that count alone, joined in ascending order.  A row of the gradient therefore depends
  * on its own tokens only, and is bitwise the same in every run.
  *
  * Conventions as in linear_logp.h: device pointers, caller-owned buffers, work

@@ -11,16 +11,18 @@
 //           place: sorted by row, ascending within a row.
 //   reduce  a warp takes 8 or 16 places of the sorted order and 64 vectors of the columns.
 //           It streams those rows of grad_out through its own ring in shared memory
-//           (cp.async, 5 or 11 rows in flight), and writes a table row whenever its tokens
-//           end.  A row of more than 32 tokens is cut into chunks whose length depends on
-//           its count alone; the warp that finishes a row's last chunk joins them in
-//           ascending order.  Other CTAs of the same launch write the zero rows.
+//           (cp.async, 6 or 12 rows), and writes a table row whenever its tokens end.  A row
+//           of more than 32 tokens is cut into chunks, and where it has more than 16, those
+//           into groups, whose lengths depend on its count alone; the warp that finishes a
+//           group's last chunk joins them in ascending order, and the one that finishes the
+//           last group the groups.  Other CTAs of the same launch write the zero rows.
 //
 // Measured, bf16, tokens of a 1 / (id + 1) distribution: 16384 tokens x 2688 into 131072
-// rows 116 us (6.8 TB/s, the measured copy peak); added to 128256 rows of 4096, 50 us
-// (4.9 TB/s, 72%: 9.5 us are the sort, and the reduce launch is held by the instructions
-// of short rows and by the sums of the longest ones); fp32, 2049 x 1001 into 50257 rows
-// 39 us (79%).
+// rows 115 us (6.9 TB/s, the measured copy peak); added to 128256 rows of 4096, 49 us
+// (5.0 TB/s, 74%: 9.5 us are the sort, and the reduce launch is held by the instructions
+// of short rows); fp32, 2049 x 1001 into 50257 rows 38 us (82%).  Where the longest row
+// decides, 65600 x 512 into 101 rows 48 us, of which 21 are the sort (checks at every place
+// and chunks of the square root of the count, without groups: 75).
 #include "elem.cuh"
 
 namespace llp {
@@ -84,7 +86,8 @@ constexpr int kSortMaxRange = 2048;   // rows of one CTA
 constexpr int kSortList = 512;        // tokens of its rows that a warp notes as it scans
 constexpr int kSortLoads = 8;         // tokens per lane in flight
 constexpr int kSortSmem = 224 * 1024;
-constexpr int kWindow = 32;           // shortest chunk of a long row
+constexpr int kWindowShift = 5;
+constexpr int kWindow = 1 << kWindowShift;  // shortest chunk of a long row
 
 // A place of the sorted order: the token n, its row v, and the places [begin, end) of that
 // row.  The sign bits say, of n, that it is the row's last token, and of v, that the row has
@@ -118,11 +121,15 @@ SortPlan sort_plan(long long N, long long V) {
   return p;
 }
 
-// Chunks of a row of `count` tokens: 32 * 2^s places for at most 1024 * 4^s tokens.  A chunk's
-// places are added one after another, and so are the chunks: with about as many chunks as
-// places neither is long.
-__device__ __forceinline__ int chunk_of(int count) {
-  return kWindow << ((32 - __clz((count - 1) >> 10) + 1) / 2);
+// Chunks of a row of `count` tokens: 32 * 2^s places for at most 2^14 * 8^s tokens.  A chunk's
+// places are added one after another, so are the chunks of a group, and so are the groups:
+// with about as many of each none is long.
+__device__ __forceinline__ int chunk_shift(int count) {  // log2 of the places
+  return kWindowShift + (32 - __clz((count - 1) >> 14) + 2) / 3;
+}
+// log2 of the chunks of a group: all of them, where they are few.
+__device__ __forceinline__ int group_shift(int chunks) {
+  return chunks <= 16 ? 4 : (32 - __clz(chunks - 1)) / 2;
 }
 
 // Measured, 16384 tokens of a 1 / (id + 1) distribution, 131072 rows: 9.5 us, bound by
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const l
 
 constexpr int kTile = 64;  // places that a warp holds in shared memory: place b at b % kTile
 constexpr int kPer = 2;    // vectors per lane
+constexpr int kJoin = 3;   // partial sums loaded together: two cost the join more, four the others registers
 
 // Slot of a long row's chunk among the partial sums.  Two chunks of one row begin at
 // least kWindow places apart, and two long rows' first chunks (or two later ones)
@@ -306,8 +314,9 @@ struct ReduceParams {
   const Place* places;
   const int* total;
   const unsigned* named;
-  int* arrivals;   // [windows][slices]
+  int* arrivals;   // [2 * windows][slices] of a long row's groups of chunks, [windows][slices] of its groups
   float* part;     // [2 * windows][units * W]
+  long long windows;
   int stride;
   int N, V, D;
   int slices, slice_units;  // vectors of a slice: at most kPer per lane
@@ -334,7 +343,7 @@ struct ReduceShape {
 };
 
 template <int DT, bool AL, bool ACC>
-__global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embedding_reduce_kernel(
+__global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS, 1) embedding_reduce_kernel(
     ReduceParams p, const typename Elem<DT>::T* __restrict__ grad_out, typename Elem<DT>::T* grad_weight) {
   using S = Slot<DT, AL>;
   using T = typename Elem<DT>::T;
@@ -386,10 +395,10 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
     const unsigned q = min(p0 + p.per_warp, M) - 1;
     const unsigned e_begin = __shfl_sync(0xffffffffu, first.z, 0), e_end = __shfl_sync(0xffffffffu, first.w, 0);
     const unsigned f_begin = __shfl_sync(0xffffffffu, first.z, q - p0), f_end = __shfl_sync(0xffffffffu, first.w, q - p0);
-    const unsigned C = chunk_of(e_end - e_begin), off = (p0 - e_begin) & (C - 1);
+    const unsigned C = 1u << chunk_shift(e_end - e_begin), off = (p0 - e_begin) & (C - 1);
     if (off != 0) h0 = min(p0 - off + C, e_end);
     if (h0 > q) return;
-    const unsigned Cq = chunk_of(f_end - f_begin);
+    const unsigned Cq = 1u << chunk_shift(f_end - f_begin);
     h1 = min(q - ((q - f_begin) & (Cq - 1)) + Cq, f_end);
   }
   __syncwarp();
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
     }
     copy_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue(h0 + s, s * STEP + tid);
   int out = tid;       // the ring's place of b
   unsigned base = p0;  // places [base, base + kTile) are in the tile
@@ -458,8 +467,8 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
     const Place e = tile[b % kTile];
     const unsigned head = b, begin = e.z, end = e.w;
     const bool cut = e.y < 0;
-    const unsigned C = cut ? chunk_of(end - begin) : 0;
-    const unsigned stop = cut ? min(end, b + C) : end;
+    const int cs = cut ? chunk_shift(end - begin) : 0;
+    const unsigned stop = cut ? min(end, b + (1u << cs)) : end;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
 #pragma unroll
@@ -497,52 +506,70 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS) embeddin
       out = step(out);
       refill(b + 1);
     }
-    if (__builtin_expect(cut, 0)) {  // the chunks' sums meet in memory
-      float* const part = p.part + slot_of(head, head == begin) * units * W;
+    if (__builtin_expect(cut, 0)) {
+      // The chunks' sums meet in memory: the warp that comes last of a group adds its chunks, and
+      // the last of those the groups, each in ascending order.
+      const int chunks = ((end - begin - 1) >> cs) + 1, shift = group_shift(chunks);
+      const int group = (head - begin) >> (cs + shift);
+      const bool more = chunks > 1 << shift;
+      unsigned from = begin + (group << (cs + shift)), own = head;
+      int members = min(1 << shift, chunks - (group << shift)), apart = cs;
+      int* arrivals = p.arrivals + slot_of(from, group == 0) * p.slices;
+      bool joined;
+      while (true) {
+        float* const part = p.part + slot_of(own, own == begin) * units * W;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (left[k] > 0) {
+        for (int k = 0; k < kPer; ++k)
+          if (left[k] > 0) {
 #pragma unroll
-          for (int i = 0; i < H; i += 2)
-            reinterpret_cast<float4*>(part + col[k])[i / 2] =
-                make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
-        }
-      const int chunks = (end - begin + C - 1) / C;
-      __threadfence();
-      __syncwarp();
-      int before = 0;
-      if (lane == 0)
-        before = atomicAdd(p.arrivals + static_cast<long long>(begin / kWindow) * p.slices + slice, 1);
-      if (__shfl_sync(0xffffffffu, before, 0) != chunks - 1) continue;
-      // the warp that came last adds them, in ascending order, eight loads at a time
-      __threadfence();
+            for (int i = 0; i < H; i += 2)
+              reinterpret_cast<float4*>(part + col[k])[i / 2] =
+                  make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+          }
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(arrivals + slice, 1);
+        joined = __shfl_sync(0xffffffffu, before, 0) == members - 1;
+        if (!joined) break;
+        __threadfence();
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
+        for (int k = 0; k < kPer; ++k)
 #pragma unroll
-        for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
-        if (32 * k >= here) continue;
-        const float* const q = p.part + col[k];
-        for (int c0 = 0; c0 < chunks; c0 += 8) {
-          float4 v[8][H / 2];
+          for (int i = 0; i < H; ++i) acc[k][i] = f2(0.f);
+        for (int c0 = 0; c0 < members; c0 += kJoin) {
+          float4 v[kJoin][kPer][H / 2];  // loaded together
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int at = min(c0 + c, chunks - 1);
+          for (int c = 0; c < kJoin; ++c) {
+            const unsigned at = from + (min(c0 + c, members - 1) << apart);
+            const float* const q = p.part + slot_of(at, at == begin) * units * W;
 #pragma unroll
-            for (int i = 0; i < H / 2; ++i)
-              v[c][i] = __ldcg(reinterpret_cast<const float4*>(q + slot_of(begin + at * C, at == 0) * units * W) + i);
+            for (int k = 0; k < kPer; ++k)
+#pragma unroll
+              for (int i = 0; i < H / 2; ++i) v[c][k][i] = __ldcg(reinterpret_cast<const float4*>(q + col[k]) + i);
           }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c0 + c < chunks) {
+          for (int c = 0; c < kJoin; ++c) {
+            if (c0 + c < members) {
 #pragma unroll
-              for (int i = 0; i < H / 2; ++i) {
-                acc[k][2 * i] = add2(acc[k][2 * i], f2(v[c][i].x, v[c][i].y));
-                acc[k][2 * i + 1] = add2(acc[k][2 * i + 1], f2(v[c][i].z, v[c][i].w));
-              }
+              for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) {
+                  acc[k][2 * i] = add2(acc[k][2 * i], f2(v[c][k][i].x, v[c][k][i].y));
+                  acc[k][2 * i + 1] = add2(acc[k][2 * i + 1], f2(v[c][k][i].z, v[c][k][i].w));
+                }
             }
           }
         }
+        if (!more || apart != cs) break;
+        // the groups of the row
+        own = from;
+        from = begin;
+        apart = cs + shift;
+        members = ((chunks - 1) >> shift) + 1;
+        arrivals = p.arrivals + (p.windows * 2 + begin / kWindow) * p.slices;
       }
+      if (!joined) continue;
     }
     T* const o = table_row(e.y);
 #pragma unroll
@@ -575,7 +602,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(long long N, long long V, long long D) {
   BwdLayout L;
   L.windows = (N + kWindow - 1) / kWindow;
-  L.num_arrivals = L.windows * ((D + 255) / 256);  // slices have 256 columns (fp32) or 512
+  L.num_arrivals = L.windows * 3 * ((D + 255) / 256);  // slices have 256 columns (fp32) or 512
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -700,6 +727,7 @@ cudaError_t launch_embedding_bwd(const EmbeddingParams& p, const void* grad_out,
   r.named = named;
   r.arrivals = arrivals;
   r.part = reinterpret_cast<float*>(ws + L.part);
+  r.windows = L.windows;
   r.stride = static_cast<int>(stride);
   r.N = p.N;
   r.V = p.V;

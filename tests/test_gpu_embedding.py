@@ -109,6 +109,20 @@ def test_backward_counts_around_the_piece_lengths(N):
     _check_bwd(torch.randn(len(t), D, generator=g), t, V, torch.float32)
 
 
+@pytest.mark.parametrize("N", [511, 512, 513, 544, 545, 16383, 16384, 16385, 131073])
+def test_backward_counts_around_the_group_lengths(N):
+    """Rows whose pieces are joined at once, in groups, and with the next length of a piece;
+    a second long row begins where the first one ends."""
+    g = torch.Generator().manual_seed(N)
+    V, D = 3, 24
+    t = torch.cat([torch.full((N,), 1), torch.full((33,), 2), torch.tensor([0, -100])])
+    t = t[torch.randperm(len(t), generator=g)]
+    base = torch.randn(V, D, generator=g)
+    go = torch.randn(len(t), D, generator=g)
+    _check_bwd(go, t, V, torch.float32)
+    _check_bwd(go, t, V, torch.float32, scale=0.5, base=base)
+
+
 @pytest.mark.parametrize("V", [1, 2, 255, 256, 257, 1023, 4097, 131072])
 @pytest.mark.parametrize("N", [3, 700, 5000])
 def test_backward_table_sizes(N, V):
