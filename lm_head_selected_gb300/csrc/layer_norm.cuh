@@ -65,7 +65,11 @@ __device__ __forceinline__ void keep_params(float4* kept, const typename Elem<PT
 }
 
 constexpr int kPipeSMs = 152;     // SMs that the persistent grids are made for
-constexpr int kPipeUnits = 1024;  // vectors of the widest row of the one-pass kernels
+constexpr int kPipeUnits = 1024;  // vectors of the widest row that takes up to three per thread; twice as many take four
+
+// Vectors of a thread that lie within the row for sure.
+template <int K>
+constexpr int kFull = K == 4 ? 2 : K - 1;
 
 // Fixed-order sum over a CTA of THREADS threads: butterflies, then the warps in ascending order.
 template <int THREADS>

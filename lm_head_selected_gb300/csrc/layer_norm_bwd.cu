@@ -16,11 +16,14 @@
 // another and the rows to come are in flight whatever the registers hold.  Group q of
 // G takes the rows q, q + G, ...: the rows under way at one time are neighbours
 // (contiguous ranges instead: 190 us).  A second launch joins the CTAs' column sums in
-// ascending order.  Rows beyond 1024 vectors take three plain kernels.
+// ascending order.  Rows of 1025 to 2048 vectors take four per thread, read from the
+// ring once more for grad_x because the registers hold no more than the column sums;
+// wider ones take three plain kernels.
 //
 // Measured, bf16, three tensors of traffic: 16384 x 4096 67.4 us (6.0 TB/s, 88% of the
-// measured copy peak), 65600 x 2688 170 us (92%), 16384 x 2688 50.4 us (77%: 5 us are the
-// join and the two launches' ends).
+// measured copy peak), 65600 x 2688 170 us (92%), 16384 x 2688 50 us (78%: 5 us are the
+// join and the two launches' ends), 4096 x 16384 70 us (85%), 4096 x 8448 53 us (58%; three
+// plain kernels: 142).
 #include "layer_norm.cuh"
 
 namespace llp {
@@ -28,19 +31,22 @@ namespace llp {
 namespace {
 
 constexpr int kBwdThreads = 512;  // of a CTA, one per SM: 128 registers per thread
-template <bool AL>
+template <int K, bool AL>
 struct BwdRing {
-  static constexpr int STAGES = AL ? 4 : 3;  // rows
+  static constexpr int STAGES = K == 4 ? 2 : AL ? 4 : 3;  // rows
 };
 
 // part: [gridDim.x][2][D], the CTA's column sums of grad_y * h and of grad_y; null to skip them.
-// K = ceil(units / (32 * warps)): only a thread's last vector may lie past the row's end.
+// Vectors per thread: K = ceil(units / (32 * warps)), or 4 for more than kPipeUnits vectors and 16
+// warps; those from kFull<K> on may lie past the row's end.  Four are too many to hold beside their
+// columns' sums: they are read from the ring once more for grad_x.
 template <int DT, int PT, int K, bool AL>
 __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
     LayerNormParams p, int warps, const float* __restrict__ mean, const float* __restrict__ rstd,
     typename Elem<DT>::T* __restrict__ gx, float* __restrict__ part) {
   using T = typename Elem<DT>::T;
-  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = BwdRing<AL>::STAGES;
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = BwdRing<K, AL>::STAGES;
+  constexpr bool HOLD = K < 4;
   using S = Slot<DT, AL>;
   extern __shared__ uint4 ring[];  // [STAGES][2][K][threads]: grad_y and x; then the weight; then the slots' fifth words
   __shared__ float red[2][kBwdThreads / 32][32];
@@ -54,6 +60,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
   const int last = first + (K - 1) * width;
   const bool tail = last < units;
   const int tail_n = min(p.D - last * W, W);  // elements of the last vector
+  auto on = [&](int k) { return k < kFull<K> || (k == K - 1 ? tail : first + k * width < units); };
+  auto left = [&](int k) { return k < kFull<K> ? W : k == K - 1 ? tail_n : min(p.D - (first + k * width) * W, W); };
   // this group's rows: r0, r0 + step, ...
   const unsigned step = gridDim.x * groups, r0 = blockIdx.x * groups + group, r1 = p.N;
   const T* gsrc = static_cast<const T*>(p.gy) + static_cast<long long>(r0) * p.gy_stride + first * W;
@@ -67,14 +75,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
   float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
   uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + W / 4 * units) + threadIdx.x;
   // what no copy writes stays 0: grad_y past the row's end adds nothing to any sum
-  if (!AL || !tail)
-    for (int i = 0; i < 2 * STAGES; ++i) mine[(i * K + K - 1) * threads] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = kFull<K>; k < K; ++k)
+    if (!AL || !on(k))
+      for (int i = 0; i < 2 * STAGES; ++i) mine[(i * K + k) * threads] = make_uint4(0, 0, 0, 0);
   auto issue = [&](unsigned n, int stage) {  // row n, the next one, if there is one
     if (n < r1) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (k < K - 1 || tail) {
-          const int g = stage * pitch + k * threads, x = g + K * threads, n = k < K - 1 ? W : tail_n;
+        if (on(k)) {
+          const int g = stage * pitch + k * threads, x = g + K * threads, n = left(k);
           S::copy(mine + g, fifth + g, gsrc + k * width * W, n, glo, ghi);
           S::copy(mine + x, fifth + x, xsrc + k * width * W, n, xlo, xhi);
         }
@@ -109,30 +119,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
     const float sc = __shfl_sync(0xffffffffu, s_lane, i0);
     // h = x * rstd - mean * rstd in one step: its error stays below that of a rounding of mean
     const float ms = -__shfl_sync(0xffffffffu, m_lane, i0) * sc;
-    copy_wait<STAGES - 2>();
+    const int now = stage;
+    if (!HOLD) issue(n + step, stage ^ 1);
+    copy_wait<HOLD ? STAGES - 2 : 1>();
     const bool gshift = S::shifted(glo + static_cast<long long>(n) * p.gy_stride);
     const bool xshift = S::shifted(xlo + static_cast<long long>(n) * p.x_stride);
-    F2 a[K][H], h[K][H], t0 = f2(0.f), t1 = f2(0.f);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int g = stage * pitch + k * threads, x = g + K * threads, left = k < K - 1 ? W : tail_n;
-      unpack2<DT, W>(S::read(mine + g, fifth + g, gshift, left), a[k]);
-      unpack2<DT, W>(S::read(mine + x, fifth + x, xshift, left), h[k]);
+    F2 a[HOLD ? K : 1][H], h[HOLD ? K : 1][H], t0 = f2(0.f), t1 = f2(0.f);
+    // grad_y * weight and h of a vector, and on the first pass its share of the sums
+    auto vector = [&](int k, F2 (&a)[H], F2 (&h)[H], bool sums) {
+      const int g = now * pitch + k * threads, x = g + K * threads;
+      unpack2<DT, W>(S::read(mine + g, fifth + g, gshift, left(k)), a);
+      unpack2<DT, W>(S::read(mine + x, fifth + x, xshift, left(k)), h);
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
-        const float4 w = k < K - 1 || tail ? kept[q * units + first + k * width] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 w = on(k) ? kept[q * units + first + k * width] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 2 * q; i < 2 * q + 2; ++i) {
-          h[k][i] = fma2(h[k][i], f2(sc), f2(ms));
-          ab[k][i] = add2(ab[k][i], a[k][i]);
-          aw[k][i] = fma2(a[k][i], h[k][i], aw[k][i]);
-          a[k][i] = mul2(a[k][i], i == 2 * q ? f2(w.x, w.y) : f2(w.z, w.w));
-          t0 = add2(t0, a[k][i]);
-          t1 = fma2(a[k][i], h[k][i], t1);
+          h[i] = fma2(h[i], f2(sc), f2(ms));
+          if (sums) {
+            ab[k][i] = add2(ab[k][i], a[i]);
+            aw[k][i] = fma2(a[i], h[i], aw[k][i]);
+          }
+          a[i] = mul2(a[i], i == 2 * q ? f2(w.x, w.y) : f2(w.z, w.w));
+          if (sums) {
+            t0 = add2(t0, a[i]);
+            t1 = fma2(a[i], h[i], t1);
+          }
         }
       }
-    }
-    issue(n + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) vector(k, a[HOLD ? k : 0], h[HOLD ? k : 0], true);
+    if (HOLD) issue(n + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     float s0 = sum2(t0), s1 = sum2(t1);
     group_sums(s0, s1, red[i & 1][group], warp, warps, 1 + group);
@@ -141,10 +159,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
       const float c0 = -s0 * inv * sc, c1 = -s1 * inv * sc;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (k < K - 1 || tail) {
+        if (on(k)) {
+          F2(&av)[H] = a[HOLD ? k : 0], (&hv)[H] = h[HOLD ? k : 0];
+          if (!HOLD) vector(k, av, hv, false);
 #pragma unroll
-          for (int i = 0; i < H; ++i) a[k][i] = fma2(a[k][i], f2(sc), fma2(h[k][i], f2(c1), f2(c0)));
-          S::store(out + k * width * W, pack2<DT, W>(a[k]), k < K - 1 ? W : tail_n);
+          for (int i = 0; i < H; ++i) av[i] = fma2(av[i], f2(sc), fma2(hv[i], f2(c1), f2(c0)));
+          S::store(out + k * width * W, pack2<DT, W>(av), left(k));
         }
       }
       out += static_cast<size_t>(step) * p.D;
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
   float* const join = reinterpret_cast<float*>(ring);  // [groups][2][units * W]
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (k < K - 1 || tail) {
+    if (on(k)) {
       F2* const o = reinterpret_cast<F2*>(join + (group * 2 * units + first + k * width) * W);
 #pragma unroll
       for (int i = 0; i < H; ++i) o[i] = aw[k][i], o[units * H + i] = ab[k][i];
@@ -292,16 +312,25 @@ cudaError_t join(const LayerNormParams& p, const Grads& o, int parts, cudaStream
                                       static_cast<T*>(o.gw), static_cast<T*>(o.gb)));
 }
 
+// Whether rows that are not whole aligned vectors come here: the five-word slots of odd 16-bit rows
+// leave the weight no room beside four vectors per thread.
+template <int DT, int K>
+constexpr bool odd_rows() {
+  return K < 4 || DT == kDtypeF32;
+}
+
 template <int DT, int PT, int K>
 cudaError_t rows(const LayerNormParams& p, int warps, bool al, const Grads& o, cudaStream_t s) {
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
   const int groups = kBwdThreads / 32 / warps;  // warps is 1, 2, 4, 8 or 16
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
-  const size_t slots = static_cast<size_t>(al ? BwdRing<true>::STAGES : BwdRing<false>::STAGES) * 2 * K * kBwdThreads;
+  const size_t slots = static_cast<size_t>(al ? BwdRing<K, true>::STAGES : BwdRing<K, false>::STAGES) * 2 * K * kBwdThreads;
   const size_t smem = slots * (al ? 16 : Slot<DT, false>::BYTES) + static_cast<size_t>(units) * (Elem<DT>::W / 4) * 16;
   const bool params = o.gw != nullptr || o.gb != nullptr;
-  const auto kernel = al ? layer_norm_bwd_kernel<DT, PT, K, true> : layer_norm_bwd_kernel<DT, PT, K, false>;
+  auto kernel = layer_norm_bwd_kernel<DT, PT, K, true>;
+  if constexpr (odd_rows<DT, K>())
+    if (!al) kernel = layer_norm_bwd_kernel<DT, PT, K, false>;
   kernel<<<grid, kBwdThreads, smem, s>>>(p, warps, o.mean, o.rstd, static_cast<typename Elem<DT>::T*>(o.gx),
                                          params ? o.part : nullptr);
   const cudaError_t e = launch_result();
@@ -339,17 +368,20 @@ cudaError_t run(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
     if (K == 2) return rows<DT, PT, 2>(p, warps, al, o, s);
     return rows<DT, PT, 3>(p, warps, al, o, s);
   }
+  if (units <= 2 * kPipeUnits && (al || odd_rows<DT, 4>())) return rows<DT, PT, 4>(p, 16, al, o, s);
   return wide<DT, PT>(p, o, s);
 }
 
 template <int DT, int PT, int K>
 cudaError_t allow() {
   const int bytes = 222 * 1024;  // K = 3: 192 KB of the ring, 24 KB of the weight
-  const cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  return e != cudaSuccess ? e
-                          : note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if constexpr (odd_rows<DT, K>())
+    if (e == cudaSuccess)
+      e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  return e;
 }
 
 template <int DT, int PT>
@@ -357,6 +389,7 @@ cudaError_t setup() {
   cudaError_t e = allow<DT, PT, 1>();
   if (e == cudaSuccess) e = allow<DT, PT, 2>();
   if (e == cudaSuccess) e = allow<DT, PT, 3>();
+  if (e == cudaSuccess) e = allow<DT, PT, 4>();
   return e;
 }
 

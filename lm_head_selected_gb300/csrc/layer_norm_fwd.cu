@@ -6,13 +6,15 @@
 // meanwhile: each thread copies the vectors it will use itself, with cp.async into its
 // own slots of a ring of rows; the parameters lie in shared memory too, in fp32.  Group
 // q of G takes the rows q, q + G, ...: the rows under way at one time are neighbours.
-// Rows beyond 1024 vectors are read three times by one CTA each (from L2 after the
-// first).
+// Rows of 1025 to 2048 vectors have a CTA each and four per thread; wider ones are read
+// three times by one CTA each (from L2 after the first).
 //
 // Bound by memory, both ways.  Measured, bf16: 16384 x 2688 29.9 us (5.9 TB/s, 87% of
 // the measured copy peak; an elementwise kernel of the same traffic takes 30.0), 65600 x
 // 2688 111 us (94%).  One vector per thread, with six warps to a row, took 36.4 us, one
-// warp to a row with eleven 32.6, contiguous ranges of rows 31.1 and 121.
+// warp to a row with eleven 32.6, contiguous ranges of rows 31.1 and 121.  4096 x 16384
+// 51.6 us (77%), 4096 x 8448 40.8 (50%: a CTA has one row at a time, and its sums' latency
+// shows; read three times 86 and 49).
 #include "layer_norm.cuh"
 
 namespace llp {
@@ -21,18 +23,19 @@ namespace {
 
 template <int K>
 struct FwdShape {
-  static constexpr int THREADS = K <= 2 ? 1024 : 768;  // of a CTA, one per SM: 64 or 80 registers
+  static constexpr int THREADS = K <= 2 ? 1024 : K == 3 ? 768 : 512;  // of a CTA, one per SM: 64, 80 or 128 registers
+  static constexpr int STAGES = K <= 3 ? 3 : 2;                       // rows of the ring
 };
-constexpr int kFwdStages = 3;  // rows of the ring
 
-// K = ceil(units / (32 * warps)): only a lane's last vector may lie past the row's end.
+// Vectors per lane: K = ceil(units / (32 * warps)), or 4 for more than kPipeUnits vectors and 16
+// warps.  Those from kFull<K> on may lie past the row's end.
 template <int DT, int PT, int K, bool AL>
 __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel(
     LayerNormParams p, int warps, int groups, typename Elem<DT>::T* __restrict__ y,
     float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   using T = typename Elem<DT>::T;
   using P = typename Elem<PT>::T;
-  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = kFwdStages;
+  constexpr int W = Elem<DT>::W, H = W / 2, STAGES = FwdShape<K>::STAGES;
   using S = Slot<DT, AL>;
   extern __shared__ uint4 ring[];  // [STAGES][K][threads]; then weight and bias; then the slots' fifth words
   __shared__ float red[2][FwdShape<K>::THREADS / 32];
@@ -44,6 +47,8 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
   const int last = first + (K - 1) * width;
   const bool tail = last < units;
   const int tail_n = min(p.D - last * W, W);  // elements of the last vector
+  auto on = [&](int k) { return k < kFull<K> || (k == K - 1 ? tail : first + k * width < units); };
+  auto left = [&](int k) { return k < kFull<K> ? W : k == K - 1 ? tail_n : min(p.D - (first + k * width) * W, W); };
   // this group's rows: r0, r0 + step, ...; none when there are more groups than named barriers
   const unsigned step = gridDim.x * groups, r0 = blockIdx.x * groups + group, r1 = group < groups ? p.N : 0;
   const T* src = static_cast<const T*>(p.x) + static_cast<long long>(r0) * p.x_stride + first * W;
@@ -53,15 +58,17 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
   constexpr int pitch = K * threads;  // of a stage
   float4* const kept = reinterpret_cast<float4*>(ring + STAGES * pitch);
   uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + W / 2 * units) + threadIdx.x;
-  if (!AL || !tail)  // what no copy writes stays 0
-    for (int i = 0; i < STAGES; ++i) mine[(i * K + K - 1) * threads] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = kFull<K>; k < K; ++k)
+    if (!AL || !on(k))  // what no copy writes stays 0
+      for (int i = 0; i < STAGES; ++i) mine[(i * K + k) * threads] = make_uint4(0, 0, 0, 0);
   auto issue = [&](unsigned n, int stage) {  // row n, the next one, if there is one
     if (n < r1) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (k < K - 1 || tail)
-          S::copy(mine + stage * pitch + k * threads, fifth + stage * pitch + k * threads, src + k * width * W,
-                  k < K - 1 ? W : tail_n, lo, hi);
+        if (on(k))
+          S::copy(mine + stage * pitch + k * threads, fifth + stage * pitch + k * threads, src + k * width * W, left(k),
+                  lo, hi);
       src += step * p.x_stride;
     }
     copy_commit();
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
     F2 x[K][H], t[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack2<DT, W>(S::read(mine + at + k * threads, fifth + at + k * threads, shift, k < K - 1 ? W : tail_n), x[k]);
+      unpack2<DT, W>(S::read(mine + at + k * threads, fifth + at + k * threads, shift, left(k)), x[k]);
 #pragma unroll
       for (int i = 0; i < H; ++i) t[i & 1] = add2(t[i & 1], x[k][i]);
     }
@@ -103,12 +110,12 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
     t[0] = t[1] = f2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float m = k < K - 1 || tail ? -mean : 0.f;  // past the row's end x is and stays 0
+      const float m = on(k) ? -mean : 0.f;  // past the row's end x is and stays 0
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         x[k][i] = add2(x[k][i], f2(m));
         if constexpr (!AL) {  // a ragged last vector
-          if (k == K - 1) x[k][i] = f2(2 * i < tail_n ? x[k][i].x : 0.f, 2 * i + 1 < tail_n ? x[k][i].y : 0.f);
+          if (k >= kFull<K>) x[k][i] = f2(2 * i < left(k) ? x[k][i].x : 0.f, 2 * i + 1 < left(k) ? x[k][i].y : 0.f);
         }
         t[i & 1] = fma2(x[k][i], x[k][i], t[i & 1]);
       }
@@ -117,7 +124,7 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
     const float rstd = rsqrtf(fmaf(row_sum(sum2(add2(t[0], t[1])), red[1]), inv, p.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (k < K - 1 || tail) {
+      if (on(k)) {
         const int u = first + k * width;
 #pragma unroll
         for (int q = 0; q < W / 4; ++q) {
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
           x[k][2 * q] = fma2(mul2(x[k][2 * q], f2(rstd)), f2(w.x, w.y), f2(c.x, c.y));
           x[k][2 * q + 1] = fma2(mul2(x[k][2 * q + 1], f2(rstd)), f2(w.z, w.w), f2(c.z, c.w));
         }
-        S::store(out + k * width * W, pack2<DT, W>(x[k]), k < K - 1 ? W : tail_n);
+        S::store(out + k * width * W, pack2<DT, W>(x[k]), left(k));
       }
     }
     out += static_cast<size_t>(step) * p.D;
@@ -180,7 +187,7 @@ cudaError_t rows(const LayerNormParams& p, int warps, bool al, void* y, float* m
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
   int groups = Shape::THREADS / 32 / warps;
   if (warps > 1 && groups > 15) groups = 15;  // named barriers 1 .. 15
-  const size_t smem = static_cast<size_t>(kFwdStages) * K * Shape::THREADS * (al ? 16 : Slot<DT, false>::BYTES) +
+  const size_t smem = static_cast<size_t>(Shape::STAGES) * K * Shape::THREADS * (al ? 16 : Slot<DT, false>::BYTES) +
                       static_cast<size_t>(Elem<DT>::W / 2) * units * 16;
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
@@ -202,6 +209,7 @@ cudaError_t run(const LayerNormParams& p, void* y, float* mean, float* rstd, cud
     if (K == 2) return rows<DT, PT, 2>(p, warps, al, y, mean, rstd, s);
     return rows<DT, PT, 3>(p, warps, al, y, mean, rstd, s);
   }
+  if (units <= 2 * kPipeUnits) return rows<DT, PT, 4>(p, 16, al, y, mean, rstd, s);
   layer_norm_fwd_wide_kernel<DT, PT><<<p.N, kWideThreads, 0, s>>>(p, static_cast<typename Elem<DT>::T*>(y), mean, rstd);
   return launch_result();
 }
@@ -221,6 +229,7 @@ cudaError_t setup() {
   cudaError_t e = allow<DT, PT, 1>();
   if (e == cudaSuccess) e = allow<DT, PT, 2>();
   if (e == cudaSuccess) e = allow<DT, PT, 3>();
+  if (e == cudaSuccess) e = allow<DT, PT, 4>();
   return e;
 }
 

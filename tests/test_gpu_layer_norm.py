@@ -101,6 +101,14 @@ def test_many_rows(N):
     _check(*_problem(N, 72, torch.bfloat16, torch.float32, seed=N))
 
 
+@pytest.mark.parametrize("dtype,pdt", TYPES)
+@pytest.mark.parametrize("N,D", [(5, 8200), (155, 9001), (309, 12288), (3, 16376), (160, 16384), (2, 16392), (7, 4100),
+                                 (200, 8191)])
+def test_wide_rows(dtype, pdt, N, D):
+    """Rows of more vectors than up to three per thread take, of twice as many, and of more."""
+    _check(*_problem(N, D, dtype, pdt, seed=N + D))
+
+
 @pytest.mark.parametrize("weight,bias", [(True, False), (False, True), (False, False)])
 @pytest.mark.parametrize("D", [24, 513])
 def test_optional_parameters(weight, bias, D):
