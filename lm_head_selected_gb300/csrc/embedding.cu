@@ -161,20 +161,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const l
   auto scan = [&](int which, auto&& take) {
     const unsigned t0 = static_cast<unsigned>(which) * span;
     const unsigned count_of = t0 < static_cast<unsigned>(N) ? min(static_cast<unsigned>(span), N - t0) : 0;
-    const long long* const src = tokens + t0 + lane;
-    auto one = [&](unsigned at, long long t) {
-      const unsigned v = static_cast<unsigned>(t);
-      take(at, (t >> 32) == 0 && v < static_cast<unsigned>(V) && v != skipped, v);
+    const uint2* const src = reinterpret_cast<const uint2*>(tokens) + t0 + lane;  // low and high word
+    auto one = [&](unsigned at, const uint2& t) {
+      take(at, t.y == 0 && t.x < static_cast<unsigned>(V) && t.x != skipped, t.x);
     };
-    for (unsigned b = 0; b < count_of; b += 32 * kSortLoads) {
-      long long t[kSortLoads];
-      if (b + 32 * kSortLoads <= count_of) {
+    unsigned b = 0;
+    for (; b + 32 * kSortLoads <= count_of; b += 32 * kSortLoads) {
+      uint2 t[kSortLoads];
 #pragma unroll
-        for (int k = 0; k < kSortLoads; ++k) t[k] = __ldg(src + b + 32 * k);
-      } else {
+      for (int k = 0; k < kSortLoads; ++k) t[k] = __ldg(src + b + 32 * k);
 #pragma unroll
-        for (int k = 0; k < kSortLoads; ++k) t[k] = b + 32 * k + lane < count_of ? __ldg(src + b + 32 * k) : -1;
-      }
+      for (int k = 0; k < kSortLoads; ++k) one(b + 32 * k + lane, t[k]);
+    }
+    if (b < count_of) {
+      uint2 t[kSortLoads];
+#pragma unroll
+      for (int k = 0; k < kSortLoads; ++k)
+        t[k] = b + 32 * k + lane < count_of ? __ldg(src + b + 32 * k) : make_uint2(~0u, ~0u);
 #pragma unroll
       for (int k = 0; k < kSortLoads; ++k)
         if (b + 32 * k < count_of) one(b + 32 * k + lane, t[k]);
