@@ -19,10 +19,10 @@
 //
 // Measured, bf16, tokens of a 1 / (id + 1) distribution: 16384 tokens x 2688 into 131072
 // rows 115 us (6.9 TB/s, the measured copy peak); added to 128256 rows of 4096, 49 us
-// (5.0 TB/s, 74%: 9.5 us are the sort, and the reduce launch is held by the instructions
-// of short rows); fp32, 2049 x 1001 into 50257 rows 38 us (82%).  Where the longest row
-// decides, 65600 x 512 into 101 rows 48 us, of which 21 are the sort (checks at every place
-// and chunks of the square root of the count, without groups: 75).
+// (5.0 TB/s, 75%: 9.2 us are the sort, and the reduce launch runs at 94%); fp32, 2049 x
+// 1001 into 50257 rows 38 us (82%; the sort 5.9).  Where the longest row decides, 65600 x
+// 512 into 101 rows 45 us, of which 21 are the sort (checks at every place and chunks of
+// the square root of the count, without groups: 75).
 #include "elem.cuh"
 
 namespace llp {
@@ -39,8 +39,9 @@ constexpr int kFwdWarps = 8;
 constexpr int kFwdLoads = 4;  // vectors per lane, all in flight together
 
 // One warp per row and chunk of at most 32 * kFwdLoads vectors (2 KB).  Bound by memory:
-// 16384 rows of 2688 bf16 take 21.4 us, 86% of the measured copy peak on the rows written
-// and the distinct ones read; 32 rows 1.6 us, one launch.
+// 16384 rows of 2688 bf16 take 21.3 us, 87% of the measured copy peak on the rows written
+// and the distinct ones read, 65600 rows 72.4 (94%); 32 rows 1.6 us, one launch.  Two vectors
+// per lane 23.3 and 84.5; six, or a row's chunks side by side in the grid, 21.1 and 74.7.
 template <int DT, bool AL>
 __global__ void __launch_bounds__(32 * kFwdWarps) embedding_fwd_kernel(const long long* __restrict__ tokens,
                                                                        const typename Elem<DT>::T* __restrict__ weight,
@@ -97,7 +98,7 @@ constexpr int kFlag = static_cast<int>(0x80000000u);
 
 // CTA b owns the rows v with v mod owners = b: frequent tokens, whose ids often lie
 // together, are spread over the CTAs (with contiguous ranges one of them had 57% of the
-// tokens of a 1 / (id + 1) distribution, and the launch took 17 us instead of 9.5).
+// tokens of a 1 / (id + 1) distribution, and the launch took 17 us where it then took 9.5).
 struct SortPlan {
   int shift, owners, range;  // log2 of the CTAs; rows of each, a multiple of 32
   int warps, span, list;     // scanning warps; tokens of each (a multiple of 32), tokens that it notes
@@ -132,9 +133,11 @@ __device__ __forceinline__ int group_shift(int chunks) {
   return chunks <= 16 ? 4 : (32 - __clz(chunks - 1)) / 2;
 }
 
-// Measured, 16384 tokens of a 1 / (id + 1) distribution, 131072 rows: 9.5 us, bound by
-// latency: the scan is 2.5 us of it, the counters and their sums 2, placing the tokens 1.5
-// to 2.5, the launch the rest.  2049 tokens and 50257 rows: 5.9 us.
+// Measured, tokens of a 1 / (id + 1) distribution, 131072 rows: 16384 tokens 9.2 us, bound by
+// latency: the scan is about 2 us of it, the counters and their sums 2, placing the tokens 1.5
+// to 2.5, the launch the rest.  2049 tokens and 50257 rows: 5.9 us.  65600 tokens: 19 us, most
+// of it the scan's instructions, every CTA's over all tokens.  Zeroing a part of the table, or
+// fetching a part of grad_out into L2, while it waits: both measured, neither pays.
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const long long* __restrict__ tokens, int N,
                                                                          int V, long long ignore_index, int shift,
                                                                          int range, int warps, int span, int list,
