@@ -22,7 +22,7 @@
 //
 // Measured, bf16, three tensors of traffic: 16384 x 4096 67.4 us (6.0 TB/s, 88% of the
 // measured copy peak), 65600 x 2688 170 us (92%), 16384 x 2688 50 us (78%: 5 us are the
-// join and the two launches' ends), 4096 x 16384 70 us (85%), 4096 x 8448 53 us (58%; three
+// join and the two launches' ends), 4096 x 16384 70 us (85%), 4096 x 8448 54 us (57%; three
 // plain kernels: 142).
 #include "layer_norm.cuh"
 
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
   constexpr bool HOLD = K < 4;
   using S = Slot<DT, AL>;
   extern __shared__ uint4 ring[];  // [STAGES][2][K][threads]: grad_y and x; then the weight; then the slots' fifth words
-  __shared__ float red[2][kBwdThreads / 32][32];
+  __shared__ float red[2][K == 4 ? 1 : kBwdThreads / 32][32];  // [groups]: one of 16 warps when K is 4
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int threads = kBwdThreads;
   const int lane = threadIdx.x & 31;
@@ -312,13 +312,6 @@ cudaError_t join(const LayerNormParams& p, const Grads& o, int parts, cudaStream
                                       static_cast<T*>(o.gw), static_cast<T*>(o.gb)));
 }
 
-// Whether rows that are not whole aligned vectors come here: the five-word slots of odd 16-bit rows
-// leave the weight no room beside four vectors per thread.
-template <int DT, int K>
-constexpr bool odd_rows() {
-  return K < 4 || DT == kDtypeF32;
-}
-
 template <int DT, int PT, int K>
 cudaError_t rows(const LayerNormParams& p, int warps, bool al, const Grads& o, cudaStream_t s) {
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
@@ -328,9 +321,7 @@ cudaError_t rows(const LayerNormParams& p, int warps, bool al, const Grads& o, c
   const size_t slots = static_cast<size_t>(al ? BwdRing<K, true>::STAGES : BwdRing<K, false>::STAGES) * 2 * K * kBwdThreads;
   const size_t smem = slots * (al ? 16 : Slot<DT, false>::BYTES) + static_cast<size_t>(units) * (Elem<DT>::W / 4) * 16;
   const bool params = o.gw != nullptr || o.gb != nullptr;
-  auto kernel = layer_norm_bwd_kernel<DT, PT, K, true>;
-  if constexpr (odd_rows<DT, K>())
-    if (!al) kernel = layer_norm_bwd_kernel<DT, PT, K, false>;
+  const auto kernel = al ? layer_norm_bwd_kernel<DT, PT, K, true> : layer_norm_bwd_kernel<DT, PT, K, false>;
   kernel<<<grid, kBwdThreads, smem, s>>>(p, warps, o.mean, o.rstd, static_cast<typename Elem<DT>::T*>(o.gx),
                                          params ? o.part : nullptr);
   const cudaError_t e = launch_result();
@@ -368,19 +359,19 @@ cudaError_t run(const LayerNormParams& p, const Grads& o, cudaStream_t s) {
     if (K == 2) return rows<DT, PT, 2>(p, warps, al, o, s);
     return rows<DT, PT, 3>(p, warps, al, o, s);
   }
-  if (units <= 2 * kPipeUnits && (al || odd_rows<DT, 4>())) return rows<DT, PT, 4>(p, 16, al, o, s);
+  if (units <= 2 * kPipeUnits) return rows<DT, PT, 4>(p, 16, al, o, s);
   return wide<DT, PT>(p, o, s);
 }
 
 template <int DT, int PT, int K>
 cudaError_t allow() {
-  const int bytes = 222 * 1024;  // K = 3: 192 KB of the ring, 24 KB of the weight
+  // K = 3: 192 KB of the ring, 24 KB of the weight; K = 4: 128 (odd 16-bit rows 160) and 64
+  const int bytes = (K == 4 ? 224 : 222) * 1024;
   cudaError_t e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, true>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  if constexpr (odd_rows<DT, K>())
-    if (e == cudaSuccess)
-      e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (e == cudaSuccess)
+    e = note_cuda(cudaFuncSetAttribute(layer_norm_bwd_kernel<DT, PT, K, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   return e;
 }
 

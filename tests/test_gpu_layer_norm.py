@@ -144,6 +144,28 @@ def test_strides_and_alignment(dtype, D):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [4104, 8200, 9001, 16384, 16392])
+def test_layouts_of_wide_rows(dtype, D):
+    """Odd strides and starts give the bits of contiguous rows, whichever kernel takes them."""
+    import lm_head_selected_gb300 as llp
+    x, gy, w, b = (t.cuda() for t in _problem(160, D, dtype, dtype, seed=D))
+    y, m, r = llp.layer_norm_fwd(x, w, b)
+    grads = llp.layer_norm_bwd(gy, x, m, r, w)
+
+    def odd(t, pad):
+        wide = torch.full((t.shape[0], D + pad), float("nan"), dtype=dtype, device="cuda")
+        wide[:, 1:1 + D] = t
+        return wide[:, 1:1 + D]
+
+    for pad in (3, 8):
+        xo, go = odd(x, pad), odd(gy, pad + 2)
+        for got, want in zip(llp.layer_norm_fwd(xo, w, b), (y, m, r)):
+            assert torch.equal(got, want)
+        for got, want in zip(llp.layer_norm_bwd(go, xo, m, r, w), grads):
+            assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_degenerate_rows(dtype):
     """Constant rows, huge and tiny values, zeros; eps decides where the variance vanishes."""
     x = torch.randn(6, 128, generator=torch.Generator().manual_seed(1))
