@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS, 1) embed
   if (blockIdx.x >= reduce_ctas) {  // zero rows, one warp per row
     const unsigned block = blockIdx.x - reduce_ctas;
     const unsigned owner = block & ((1u << p.shift) - 1), r0 = (block >> p.shift) * p.zero_rows;
-    const unsigned m = __ldg(p.named + (owner * p.range + r0) / 32) >> (r0 & 31);
+    const unsigned m = load_written(p.named + (owner * p.range + r0) / 32) >> (r0 & 31);
     for (int i = warp; i < p.zero_rows; i += kWarps) {
       const long long v = static_cast<long long>(r0 + i) << p.shift | owner;
       if (v >= p.V || ((m >> i) & 1)) continue;
@@ -386,9 +386,11 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS, 1) embed
   const unsigned block = w / p.slices, p0 = block * p.per_warp;
   const int slice = w - block * p.slices;
   // The first places, read without waiting for their number: those past it hold nothing yet.
-  const unsigned M = __ldg(p.total);
-  auto raw_place = [&](unsigned b) { return b < static_cast<unsigned>(p.N) ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
-  auto place = [&](unsigned b) { return b < M ? __ldg(p.places + b) : make_int4(0, 0, 0, 0); };
+  const unsigned M = load_written(p.total);
+  auto raw_place = [&](unsigned b) {
+    return b < static_cast<unsigned>(p.N) ? load_written(p.places + b) : make_int4(0, 0, 0, 0);
+  };
+  auto place = [&](unsigned b) { return b < M ? load_written(p.places + b) : make_int4(0, 0, 0, 0); };
   const Place first = raw_place(p0 + lane), second = raw_place(p0 + 32 + lane);
   Place coming = raw_place(p0 + kTile + lane);  // takes the room of the 32 places that are done with
   if (p0 >= M) return;
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(32 * ReduceShape<DT, AL, ACC>::WARPS, 1) embed
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
 #pragma unroll
-              for (int i = 0; i < H / 2; ++i) v[c][k][i] = __ldcg(reinterpret_cast<const float4*>(q + col[k]) + i);
+              for (int i = 0; i < H / 2; ++i) v[c][k][i] = load_written(reinterpret_cast<const float4*>(q + col[k]) + i);
           }
 #pragma unroll
           for (int c = 0; c < kJoin; ++c) {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
 constexpr int kJoinWarps = 32;
 
 template <int PT>
-__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ part, int parts,
+__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* part, int parts,
                                                                           int D, typename Elem<PT>::T* __restrict__ gw,
                                                                           typename Elem<PT>::T* __restrict__ gb) {
   __shared__ float sm[kJoinWarps][32];
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const 
   float v[MOST], s = 0.f;
 #pragma unroll
   for (int i = 0; i < MOST; ++i)
-    v[i] = __ldcg(part + static_cast<size_t>(min(warp + i * kJoinWarps, parts - 1)) * 2 * D + min(c, 2 * D - 1));
+    v[i] = load_written(part + static_cast<size_t>(min(warp + i * kJoinWarps, parts - 1)) * 2 * D + min(c, 2 * D - 1));
 #pragma unroll
   for (int i = 0; i < MOST; ++i)
     if (warp + i * kJoinWarps < parts) s += v[i];
