@@ -20,9 +20,9 @@
 // ring once more for grad_x because the registers hold no more than the column sums;
 // wider ones take three plain kernels.
 //
-// Measured, bf16, three tensors of traffic: 16384 x 4096 67.4 us (6.0 TB/s, 88% of the
-// measured copy peak), 65600 x 2688 170 us (92%), 16384 x 2688 50 us (78%: 5 us are the
-// join and the two launches' ends), 4096 x 16384 70 us (85%), 4096 x 8448 54 us (57%; three
+// Measured, bf16, three tensors of traffic: 16384 x 4096 67.1 us (6.0 TB/s, 89% of the
+// measured copy peak), 65600 x 2688 171 us (91%), 16384 x 2688 44.8 us (87%: 5 us are the
+// join and the two launches' ends), 4096 x 16384 71 us (84%), 4096 x 8448 55 us (56%; three
 // plain kernels: 142).
 #include "layer_norm.cuh"
 
@@ -116,9 +116,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
       m_lane = m_next, s_lane = s_next;
       m_next = stats(mean, n + 32 * step), s_next = stats(rstd, n + 32 * step);
     }
-    const float sc = __shfl_sync(0xffffffffu, s_lane, i0);
-    // h = x * rstd - mean * rstd in one step: its error stays below that of a rounding of mean
-    const float ms = -__shfl_sync(0xffffffffu, m_lane, i0) * sc;
+    const float sc = __shfl_sync(0xffffffffu, s_lane, i0), minus = -__shfl_sync(0xffffffffu, m_lane, i0);
     const int now = stage;
     if (!HOLD) issue(n + step, stage ^ 1);
     copy_wait<HOLD ? STAGES - 2 : 1>();
@@ -130,12 +128,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
       const int g = now * pitch + k * threads, x = g + K * threads;
       unpack2<DT, W>(S::read(mine + g, fifth + g, gshift, left(k)), a);
       unpack2<DT, W>(S::read(mine + x, fifth + x, xshift, left(k)), h);
+      const float m = on(k) ? minus : 0.f;  // past the row's end x is and stays 0
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
         const float4 w = on(k) ? kept[q * units + first + k * width] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 2 * q; i < 2 * q + 2; ++i) {
-          h[i] = fma2(h[i], f2(sc), f2(ms));
+          // The mean is subtracted first, as in the forward: x - mean is exact where they are close.
+          // x * rstd - mean * rstd in one step saves an instruction and adds half a unit of mean *
+          // rstd to every h: 2.7e-3 in place of 0 for a row of 1000s.
+          h[i] = add2(h[i], f2(m));
+          if constexpr (!AL) {  // a ragged last vector; the second pass stores none of what is past the end
+            if (sums && k >= kFull<K>)
+              h[i] = f2(2 * i < left(k) ? h[i].x : 0.f, 2 * i + 1 < left(k) ? h[i].y : 0.f);
+          }
+          h[i] = mul2(h[i], f2(sc));
           if (sums) {
             ab[k][i] = add2(ab[k][i], a[i]);
             aw[k][i] = fma2(a[i], h[i], aw[k][i]);
