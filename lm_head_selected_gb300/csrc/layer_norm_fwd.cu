@@ -9,11 +9,11 @@
 // Rows of 1025 to 2048 vectors have a CTA each and four per thread; wider ones are read
 // three times by one CTA each (from L2 after the first).
 //
-// Bound by memory, both ways.  Measured, bf16: 16384 x 2688 29.9 us (5.9 TB/s, 87% of
+// Bound by memory, both ways.  Measured, bf16: 16384 x 2688 31.0 us (5.7 TB/s, 84% of
 // the measured copy peak; an elementwise kernel of the same traffic takes 30.0), 65600 x
-// 2688 111 us (94%).  One vector per thread, with six warps to a row, took 36.4 us, one
+// 2688 108.6 us (96%).  One vector per thread, with six warps to a row, took 36.4 us, one
 // warp to a row with eleven 32.6, contiguous ranges of rows 31.1 and 121.  4096 x 16384
-// 51.6 us (77%), 4096 x 8448 40.8 (50%: a CTA has one row at a time, and its sums' latency
+// 52.0 us (76%), 4096 x 8448 41.7 (49%: a CTA has one row at a time, and its sums' latency
 // shows; read three times 86 and 49).
 #include "layer_norm.cuh"
 
@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(FwdShape<K>::THREADS, 1) layer_norm_fwd_kernel
     }
     issue(n + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float mean = row_sum(sum2(add2(t[0], t[1])), red[0]) * inv;
+    // a quotient, not a product with 1 / D: the mean of equal values has to be that value (0.08 in
+    // place of 0 came out of 1000 columns of 3000)
+    const float mean = row_sum(sum2(add2(t[0], t[1])), red[0]) / static_cast<float>(p.D);
     t[0] = t[1] = f2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_fwd_wide_kernel(Layer
   float s = 0.f;
 #pragma unroll 8
   for (int c = threadIdx.x; c < p.D; c += kWideThreads) s += E::get(__ldg(x + c));
-  const float mean = cta_sum<kWideThreads>(s, sm) * inv;
+  const float mean = cta_sum<kWideThreads>(s, sm) / static_cast<float>(p.D);
   s = 0.f;
 #pragma unroll 8
   for (int c = threadIdx.x; c < p.D; c += kWideThreads) {

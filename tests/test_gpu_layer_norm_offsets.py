@@ -74,3 +74,20 @@ def test_gradients_of_a_constant_row_whose_mean_times_rstd_is_past_the_largest_f
     x = torch.full((2, D), 2.0 ** 123)
     x[1] = torch.randn(D, generator=g)
     _check_gradients(x.to(dtype), torch.randn(2, D, generator=g).to(dtype), 1 + 0.3 * torch.randn(D, generator=g))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", WIDTHS + [7, 49, 383, 769])
+def test_forward_of_constant_rows(dtype, D):
+    """Values of at most nine bits: sums of up to 2^15 of them are exact in fp32, so the mean, a
+    quotient that fits, has to be exact too, and y is the bias."""
+    import lm_head_selected_gb300 as llp
+    g = torch.Generator().manual_seed(D)
+    values = torch.tensor([3000.0, 1000.0, -0.375, 7.0, 0.0, -491.0]).to(dtype)
+    x = values[:, None].expand(-1, D).contiguous().cuda()
+    w, b = (1 + 0.3 * torch.randn(D, generator=g)).to(dtype).cuda(), torch.randn(D, generator=g).to(dtype).cuda()
+    y, mean, rstd = llp.layer_norm_fwd(x, w, b)
+    assert torch.equal(mean.cpu(), values.float())
+    assert torch.equal(y, b.expand_as(y)) and not llp.layer_norm_fwd(x)[0].any()
+    r = 1 / np.sqrt(float(np.float32(1e-5)))
+    within("rstd", rstd, np.full(len(values), r), 4 * U32 * r)  # two units in the last place
