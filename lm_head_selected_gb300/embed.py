@@ -15,7 +15,17 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import IGNORE_INDEX, _dtype_code, _need, _need_rows, _out, _raw_stream, _workspace, on_tensor_device
+from .ops import (
+    IGNORE_INDEX,
+    _dtype_code,
+    _need,
+    _need_rows,
+    _out,
+    _raw_stream,
+    _readable_rows,
+    _workspace,
+    on_tensor_device,
+)
 
 
 @on_tensor_device
@@ -84,8 +94,7 @@ class _Embedding(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_out):
         tokens, = ctx.saved_tensors
-        g = grad_out if grad_out.stride(1) == 1 else grad_out.contiguous()
-        return None, embedding_bwd(g, tokens, ctx.rows, ctx.scale, ctx.ignore_index), None, None
+        return None, embedding_bwd(_readable_rows(grad_out), tokens, ctx.rows, ctx.scale, ctx.ignore_index), None, None
 
 
 def embedding(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,

@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import _dtype_code, _need, _need_rows, _out, _raw_stream, _workspace, on_tensor_device
+from .ops import _dtype_code, _need, _need_rows, _out, _raw_stream, _readable_rows, _workspace, on_tensor_device
 
 EPS = 1e-5
 
@@ -110,8 +110,7 @@ class _LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y):
         x, weight, mean, rstd = ctx.saved_tensors
-        g = grad_y if grad_y.stride(1) == 1 else grad_y.contiguous()
-        gx, gw, gb = layer_norm_bwd(g, x, mean, rstd, weight, *ctx.needs_input_grad[:3], ctx.param_dtype)
+        gx, gw, gb = layer_norm_bwd(_readable_rows(grad_y), x, mean, rstd, weight, *ctx.needs_input_grad[:3], ctx.param_dtype)
         return gx, gw, gb, None
 
 
@@ -119,6 +118,4 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                eps: float = EPS) -> torch.Tensor:
     """(x - mean) * rstd * weight + bias over the last dimension, with autograd: x [..., D]."""
     x2 = x.reshape(-1, x.shape[-1])
-    if x2.stride(1) != 1:
-        x2 = x2.contiguous()
-    return _LayerNorm.apply(x2, weight, bias, float(eps)).reshape(x.shape)
+    return _LayerNorm.apply(_readable_rows(x2), weight, bias, float(eps)).reshape(x.shape)

@@ -94,6 +94,15 @@ def _need_rows(t: torch.Tensor, name: str, device: torch.device) -> int:
     return stride if N > 1 else D
 
 
+def _readable_rows(t: torch.Tensor) -> torch.Tensor:
+    """The 2-D tensor itself where the kernels read its rows in place, otherwise a copy: rows
+    that overlap (windows of a signal) or whose elements lie apart, and strides past 32 bits."""
+    N, D = t.shape
+    if (D <= 1 or t.stride(1) == 1) and (N <= 1 or t.stride(0) == 0 or D <= t.stride(0) < 2 ** 31):
+        return t
+    return t.contiguous()
+
+
 def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
