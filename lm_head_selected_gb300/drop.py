@@ -13,15 +13,14 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import _dtype_code, _out, _raw_stream, on_tensor_device
+from .ops import _dtype_code, _need_cuda, _out, _raw_stream, on_tensor_device
 
 _MASK64 = (1 << 64) - 1
 Offset = Union[int, torch.Tensor]
 
 
 def _check(x: torch.Tensor, name: str):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
+    _need_cuda(x, name)
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return _dtype_code(x, name)
@@ -103,5 +102,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Offset = 0,
             residual: Optional[torch.Tensor] = None) -> torch.Tensor:
     """residual + dropout(x, p), with autograd.  x and residual may have any shape (one
     and the same); elements are numbered row-major."""
+    _need_cuda(x, "x")
+    if residual is not None:
+        _need_cuda(residual, "residual")
     r = None if residual is None else residual.contiguous()
     return _Dropout.apply(x.contiguous(), r, _probability(p), int(seed), offset)

@@ -19,6 +19,7 @@ from .ops import (
     IGNORE_INDEX,
     _dtype_code,
     _need,
+    _need_cuda,
     _need_rows,
     _out,
     _raw_stream,
@@ -32,8 +33,7 @@ from .ops import (
 def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, ignore_index: int = IGNORE_INDEX,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * weight[tokens], [N, D] in the table's dtype (the product in fp32, rounded once)."""
-    if not isinstance(weight, torch.Tensor) or not weight.is_cuda:
-        raise ValueError("weight must be a CUDA tensor; this op has no CPU path")
+    _need_cuda(weight, "weight")
     dev = weight.device
     code = _dtype_code(weight, "weight")
     _need(weight, "weight", weight.dtype, dev, 2)
@@ -60,8 +60,7 @@ def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, s
     token names are neither read nor written: the form for a table tied to the LM head,
     after ``linear_logp_bwd`` has written the head's gradient.  grad_out's rows may have
     any stride."""
-    if not isinstance(grad_out, torch.Tensor) or not grad_out.is_cuda:
-        raise ValueError("grad_out must be a CUDA tensor; this op has no CPU path")
+    _need_cuda(grad_out, "grad_out")
     dev = grad_out.device
     code = _dtype_code(grad_out, "grad_out")
     stride = _need_rows(grad_out, "grad_out", dev)
@@ -86,9 +85,10 @@ def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, s
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale, ignore_index):
+        out = embedding_fwd(tokens, weight, scale, ignore_index)
         ctx.save_for_backward(tokens)
         ctx.rows, ctx.scale, ctx.ignore_index = weight.shape[0], scale, ignore_index
-        return embedding_fwd(tokens, weight, scale, ignore_index)
+        return out
 
     @staticmethod
     @once_differentiable
@@ -100,5 +100,8 @@ class _Embedding(torch.autograd.Function):
 def embedding(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
               ignore_index: int = IGNORE_INDEX) -> torch.Tensor:
     """scale * weight[tokens] with autograd: tokens [...] int64, weight [V, D] -> [..., D]."""
+    _need_cuda(weight, "weight")
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
     out = _Embedding.apply(tokens.reshape(-1).contiguous(), weight, float(scale), int(ignore_index))
     return out.reshape(*tokens.shape, weight.shape[1])

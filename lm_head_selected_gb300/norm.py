@@ -12,14 +12,13 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import _dtype_code, _need, _need_rows, _out, _raw_stream, _readable_rows, _workspace, on_tensor_device
+from .ops import _dtype_code, _need, _need_cuda, _need_rows, _out, _raw_stream, _readable_rows, _workspace, on_tensor_device
 
 EPS = 1e-5
 
 
 def _check_x(x: torch.Tensor):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor; this op has no CPU path")
+    _need_cuda(x, "x")
     code = _dtype_code(x, "x")
     stride = _need_rows(x, "x", x.device)
     if x.shape[1] < 1:
@@ -117,5 +116,8 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                eps: float = EPS) -> torch.Tensor:
     """(x - mean) * rstd * weight + bias over the last dimension, with autograd: x [..., D]."""
+    _need_cuda(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have at least one column")
     x2 = x.reshape(-1, x.shape[-1])
     return _LayerNorm.apply(_readable_rows(x2), weight, bias, float(eps)).reshape(x.shape)

@@ -65,6 +65,11 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, 
         raise ValueError(f"{name} must be contiguous")
 
 
+def _need_cuda(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor; this op has no CPU path")
+
+
 _DTYPE_CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 

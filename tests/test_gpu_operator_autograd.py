@@ -63,3 +63,17 @@ def test_rows_that_can_be_read_in_place_are_not_copied():
         assert _readable_rows(t) is t
     for t in (buf.t(), buf[:, ::2], buf.as_strided((5, 10), (4, 1)), buf.expand(2, 20, 100)[:, :, 0]):
         assert _readable_rows(t) is not t and torch.equal(_readable_rows(t), t)
+
+
+def test_refusals():
+    import lm_head_selected_gb300 as llp
+    x, t = torch.zeros(4, 8, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    for bad in (lambda: llp.layer_norm(x[0, 0]), lambda: llp.layer_norm(x[:, :0]), lambda: llp.layer_norm(x[:0, :0]),
+                lambda: llp.dropout(x, 0.1, 1, residual=3.0), lambda: llp.dropout(x, 0.1, 1, residual=x.cpu()),
+                lambda: llp.embedding(t, x[0, 0]), lambda: llp.embedding(t, x[0]), lambda: llp.embedding(t.cpu(), x)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: llp.embedding(None, x), lambda: llp.embedding([1, 2], x), lambda: llp.embedding(t.int(), x),
+                lambda: llp.layer_norm(x.double()), lambda: llp.dropout(x.double(), 0.1, 1)):
+        with pytest.raises(TypeError):
+            bad()
