@@ -632,7 +632,7 @@ cudaError_t fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStr
   using T = typename Elem<DT>::T;
   const int units = (p.D + Elem<DT>::W - 1) / Elem<DT>::W;
   const int chunks = (units + 32 * kFwdLoads - 1) / (32 * kFwdLoads);
-  const dim3 grid((p.N + kFwdWarps - 1) / kFwdWarps, chunks);
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.N) + kFwdWarps - 1) / kFwdWarps), chunks);
   embedding_fwd_kernel<DT, AL><<<grid, 32 * kFwdWarps, 0, s>>>(p.tokens, static_cast<const T*>(weight), p.N, p.V, p.D,
                                                                (units + chunks - 1) / chunks, p.scale, p.ignore_index,
                                                                static_cast<T*>(out));
@@ -648,7 +648,7 @@ cudaError_t reduce(ReduceParams r, const void* grad_out, void* grad_weight, cuda
   // Places per warp: 16, or 8 where that leaves too few warps (16384 x 4096, accumulating: 50.1
   // us with 8, 54 with 16; 65600 x 2688: 123 and 117).
   using Shape = ReduceShape<DT, AL, ACC>;
-  r.per_warp = (r.N + 15) / 16 * static_cast<long long>(r.slices) < 152 * (ACC ? 64 : 32) ? 8 : 16;
+  r.per_warp = (static_cast<long long>(r.N) + 15) / 16 * r.slices < 152 * (ACC ? 64 : 32) ? 8 : 16;
   r.warps = static_cast<unsigned>((static_cast<long long>(r.N) + r.per_warp - 1) / r.per_warp * r.slices);
   // about 32 KB of zeros per CTA: with 128 KB the last of few CTAs had the GPU to themselves
   r.zero_rows = 32;
