@@ -21,7 +21,8 @@
  * out [N, D] are contiguous row-major in bf16 (dtype 0), fp32 (dtype 1) or
  * fp16 (dtype 2); any D >= 1.  Element alignment suffices; 16-byte aligned
  * tensors with rows of a multiple of 16 bytes move fastest.  scale is rounded
- * to fp32 by the caller and must be finite.  N, V < 2^31, D < 2^22, N * D <= 2^42.
+ * to fp32 by the caller; one that is not finite is refused (LLP_ERR_BAD_SHAPE).
+ * N, V < 2^31, D < 2^22, N * D <= 2^42.
  */
 #ifndef EMBEDDING_H_
 #define EMBEDDING_H_

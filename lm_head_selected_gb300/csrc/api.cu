@@ -3,6 +3,7 @@
 // Declarations and the contract are in include/linear_logp.h.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -1235,7 +1236,8 @@ static bool row_stride_ok(int64_t N, int64_t D, int64_t stride) {
   return (N <= 1 && stride >= 0) || stride == 0 || (stride >= D && product_ok(N, stride));
 }
 
-static int embedding_shapes(int dtype, int64_t N, int64_t V, int64_t D) {
+static int embedding_shapes(int dtype, int64_t N, int64_t V, int64_t D, float scale) {
+  if (!std::isfinite(scale)) return LLP_ERR_BAD_SHAPE;
   if (!dtype_ok(dtype) || N < 0 || V < 1 || D < 1 || N > kLim31 || V > kLim31 || D >= kMaxOpD)
     return LLP_ERR_BAD_SHAPE;
   return LLP_OK;
@@ -1243,7 +1245,7 @@ static int embedding_shapes(int dtype, int64_t N, int64_t V, int64_t D) {
 
 int embedding_fwd(const int64_t* tokens, const void* weight, int dtype, int64_t N, int64_t V, int64_t D, float scale,
                   int64_t ignore_index, void* out, void* stream) {
-  int st = embedding_shapes(dtype, N, V, D);
+  int st = embedding_shapes(dtype, N, V, D, scale);
   if (st != LLP_OK) return st;
   if (N == 0) return LLP_OK;
   if (tokens == nullptr || weight == nullptr || out == nullptr) return LLP_ERR_NULL_POINTER;
@@ -1258,14 +1260,14 @@ int embedding_fwd(const int64_t* tokens, const void* weight, int dtype, int64_t 
 }
 
 size_t embedding_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D) {
-  if (N <= 0 || embedding_shapes(llp::kDtypeF32, N, V, D) != LLP_OK) return 0;
+  if (N <= 0 || embedding_shapes(llp::kDtypeF32, N, V, D, 1.f) != LLP_OK) return 0;
   return llp::embedding_bwd_workspace(N, V, D);
 }
 
 int embedding_bwd(const int64_t* tokens, const void* grad_out, int64_t grad_out_row_stride, int dtype, int64_t N,
                   int64_t V, int64_t D, float scale, int64_t ignore_index, int accumulate, void* grad_weight,
                   void* workspace, size_t workspace_bytes, void* stream) {
-  int st = embedding_shapes(dtype, N, V, D);
+  int st = embedding_shapes(dtype, N, V, D, scale);
   if (st != LLP_OK) return st;
   if (!row_stride_ok(N, D, grad_out_row_stride) || grad_out_row_stride > kLim31 || N * D > (int64_t(1) << 42))
     return LLP_ERR_BAD_SHAPE;

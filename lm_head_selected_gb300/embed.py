@@ -29,6 +29,14 @@ from .ops import (
 )
 
 
+_FP32_MAX = torch.finfo(torch.float32).max
+
+
+def _check_scale(scale: float):
+    if not abs(scale) <= _FP32_MAX:
+        raise ValueError(f"scale must be finite in fp32, got {scale}")
+
+
 @on_tensor_device
 def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, ignore_index: int = IGNORE_INDEX,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -41,6 +49,7 @@ def embedding_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0
     V, D = weight.shape
     if V < 1 or D < 1:
         raise ValueError(f"weight must have at least one row and one column, got {(V, D)}")
+    _check_scale(scale)
     N = tokens.shape[0]
     out = _out(out, (N, D), weight.dtype, dev)
     st = _lib.load().embedding_fwd(tokens.data_ptr(), weight.data_ptr(), code, N, V, D, scale, ignore_index,
@@ -71,6 +80,7 @@ def embedding_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_rows: int, s
         raise ValueError("tokens must have one entry per row of grad_out")
     if V < 1 or D < 1:
         raise ValueError("the table must have at least one row and one column")
+    _check_scale(scale)
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: pass it")
     out = _out(out, (V, D), grad_out.dtype, dev)

@@ -77,3 +77,15 @@ def test_refusals():
                 lambda: llp.layer_norm(x.double()), lambda: llp.dropout(x.double(), 0.1, 1)):
         with pytest.raises(TypeError):
             bad()
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf"), 1e39])
+def test_scales_that_are_not_finite(scale):
+    import lm_head_selected_gb300 as llp
+    w, t = torch.zeros(4, 8, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    for bad in (lambda: llp.embedding(t, w, scale), lambda: llp.embedding_fwd(t, w, scale),
+                lambda: llp.embedding_bwd(w[:3], t, 4, scale),
+                lambda: llp.embedding_bwd(w[:3], t, 4, scale, out=w, accumulate=True)):
+        with pytest.raises(ValueError, match="scale"):
+            bad()
+    assert not w.any()
