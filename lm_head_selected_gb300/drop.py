@@ -26,13 +26,21 @@ def _check(x: torch.Tensor, name: str):
     return _dtype_code(x, name)
 
 
-def _counter(seed: int, offset: Offset, device):
+def _counter(seed: int, offset: Offset, device_offset: Optional[torch.Tensor], device):
     """(seed, host offset, device pointer or None)."""
+    host = 0
     if not isinstance(offset, torch.Tensor):
-        return int(seed) & _MASK64, int(offset) & _MASK64, None
-    if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
-        raise ValueError("offset must be an int, or one int64 on the inputs' device")
-    return int(seed) & _MASK64, 0, offset.data_ptr()
+        host = int(offset) & _MASK64
+    elif device_offset is not None:
+        raise ValueError("offset must be an int beside device_offset")
+    else:
+        device_offset = offset
+    if device_offset is None:
+        return int(seed) & _MASK64, host, None
+    t = device_offset
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.numel() != 1 or t.device != device:
+        raise ValueError("an offset must be an int, or one int64 on the inputs' device")
+    return int(seed) & _MASK64, host, t.data_ptr()
 
 
 def _probability(p: float) -> float:
@@ -44,11 +52,13 @@ def _probability(p: float) -> float:
 
 @on_tensor_device
 def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residual: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None, device_offset: Optional[torch.Tensor] = None) -> torch.Tensor:
     """residual + (kept ? x / (1 - p) : 0), p rounded to a multiple of 2^-16.  ``offset`` numbers
     the mask under one seed; as an int64 tensor on the device it is read when the kernel
-    runs, so that a captured graph can advance it between replays.  ``out`` may be x or
-    residual itself."""
+    runs, so that a captured graph can advance it between replays.  With ``device_offset``
+    the mask's number is offset + device_offset: the layers of a captured step share one
+    counter on the device (advanced by the number of layers) and each adds its own offset;
+    under one number they would draw one mask.  ``out`` may be x or residual itself."""
     code = _check(x, "x")
     dev = x.device
     if residual is not None:
@@ -56,7 +66,7 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residu
             raise ValueError("residual must have x's shape and dtype")
         if residual.device != dev or not residual.is_contiguous():
             raise ValueError("residual must be contiguous, on x's device")
-    seed, off, off_ptr = _counter(seed, offset, dev)
+    seed, off, off_ptr = _counter(seed, offset, device_offset, dev)
     p = _probability(p)
     y = _out(out, x.shape, x.dtype, dev)
     st = _lib.load().dropout_fwd(x.data_ptr(), None if residual is None else residual.data_ptr(), code, x.numel(), p,
@@ -67,11 +77,11 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residu
 
 @on_tensor_device
 def dropout_bwd(grad_y: torch.Tensor, p: float, seed: int, offset: Offset = 0,
-                out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """grad_x = kept ? grad_y / (1 - p) : 0 under the forward's p, seed and offset."""
+                out: Optional[torch.Tensor] = None, device_offset: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grad_x = kept ? grad_y / (1 - p) : 0 under the forward's p, seed and offsets."""
     code = _check(grad_y, "grad_y")
     dev = grad_y.device
-    seed, off, off_ptr = _counter(seed, offset, dev)
+    seed, off, off_ptr = _counter(seed, offset, device_offset, dev)
     p = _probability(p)
     gx = _out(out, grad_y.shape, grad_y.dtype, dev)
     st = _lib.load().dropout_bwd(grad_y.data_ptr(), code, grad_y.numel(), p, seed, off, off_ptr, gx.data_ptr(),
@@ -82,28 +92,30 @@ def dropout_bwd(grad_y: torch.Tensor, p: float, seed: int, offset: Offset = 0,
 
 class _Dropout(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, p, seed, offset):
-        ctx.p, ctx.seed = p, seed
-        if isinstance(offset, torch.Tensor):
-            ctx.save_for_backward(offset)
-        else:
-            ctx.offset = offset
-        return dropout_fwd(x, p, seed, offset, residual)
+    def forward(ctx, x, residual, p, seed, offset, device_offset):
+        ctx.p, ctx.seed, ctx.offset = p, seed, offset
+        if device_offset is not None:
+            ctx.save_for_backward(device_offset)
+        return dropout_fwd(x, p, seed, offset, residual, device_offset=device_offset)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_y):
-        offset = ctx.saved_tensors[0] if ctx.saved_tensors else ctx.offset
-        gx = dropout_bwd(grad_y.contiguous(), ctx.p, ctx.seed, offset) if ctx.needs_input_grad[0] else None
-        return gx, grad_y if ctx.needs_input_grad[1] else None, None, None, None
+        device_offset = ctx.saved_tensors[0] if ctx.saved_tensors else None
+        gx = None
+        if ctx.needs_input_grad[0]:
+            gx = dropout_bwd(grad_y.contiguous(), ctx.p, ctx.seed, ctx.offset, device_offset=device_offset)
+        return gx, grad_y if ctx.needs_input_grad[1] else None, None, None, None, None
 
 
-def dropout(x: torch.Tensor, p: float, seed: int, offset: Offset = 0,
-            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+def dropout(x: torch.Tensor, p: float, seed: int, offset: Offset = 0, residual: Optional[torch.Tensor] = None,
+            device_offset: Optional[torch.Tensor] = None) -> torch.Tensor:
     """residual + dropout(x, p), with autograd.  x and residual may have any shape (one
-    and the same); elements are numbered row-major."""
+    and the same); elements are numbered row-major.  The offsets are ``dropout_fwd``'s."""
     _need_cuda(x, "x")
     if residual is not None:
         _need_cuda(residual, "residual")
     r = None if residual is None else residual.contiguous()
-    return _Dropout.apply(x.contiguous(), r, _probability(p), int(seed), offset)
+    if isinstance(offset, torch.Tensor) and device_offset is None:
+        offset, device_offset = 0, offset
+    return _Dropout.apply(x.contiguous(), r, _probability(p), int(seed), offset, device_offset)
