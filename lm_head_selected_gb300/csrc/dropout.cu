@@ -112,7 +112,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const typename Elem<D
   }
 }
 
-// Tensors that do not start on a 16-byte boundary: element by element.
+// Tensors that do not start on a 16-byte boundary: element by element, one thread per block of
+// eight.  One element late, bf16: 16384 x 2688 with a residual 110 us, without one 78, 65600 x
+// 2688 305: 2.6 to 2.9 times the vectors' time.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) dropout_unaligned_kernel(const typename Elem<DT>::T* x,
                                                                      const typename Elem<DT>::T* residual,

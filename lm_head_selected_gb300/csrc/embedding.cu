@@ -21,8 +21,9 @@
 // rows 115 us (6.9 TB/s, the measured copy peak); added to 128256 rows of 4096, 49 us
 // (5.0 TB/s, 75%: 9.2 us are the sort, and the reduce launch runs at 94%); fp32, 2049 x
 // 1001 into 50257 rows 38 us (82%; the sort 5.9).  Where the longest row decides, 65600 x
-// 512 into 101 rows 45 us, of which 21 are the sort (checks at every place and chunks of
-// the square root of the count, without groups: 75).
+// 512 into 101 rows 46 us, of which 19 are the sort (checks at every place and chunks of
+// the square root of the count, without groups: 75).  Rows of an odd number of 16-bit elements:
+// 16384 x 1001 into 50257 rows 39.4 us, added 41.3 (x 1000: 30.1, 26).
 #include "elem.cuh"
 
 namespace llp {
@@ -42,6 +43,7 @@ constexpr int kFwdLoads = 4;  // vectors per lane, all in flight together
 // 16384 rows of 2688 bf16 take 21.3 us, 87% of the measured copy peak on the rows written
 // and the distinct ones read, 65600 rows 72.4 (94%); 32 rows 1.6 us, one launch.  Two vectors
 // per lane 23.3 and 84.5; six, or a row's chunks side by side in the grid, 21.1 and 74.7.
+// Odd rows of 16 bits: 16384 x 1001 19.0 us, x 1000 9.7.
 template <int DT, bool AL>
 __global__ void __launch_bounds__(32 * kFwdWarps) embedding_fwd_kernel(const long long* __restrict__ tokens,
                                                                        const typename Elem<DT>::T* __restrict__ weight,
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps) embedding_fwd_kernel(const lon
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;  // each scans a span of the tokens
 constexpr int kSortSets = kSortWarps / 2;      // two spans share a set of counters: fewer to clear and to add up
-constexpr int kSortOwners = 128;      // CTAs that share the table's rows (a power of two)
+constexpr int kSortShift = 7;         // log2 of the CTAs that share the table's rows: 128, more for large tables
 constexpr int kSortMaxRange = 2048;   // rows of one CTA
 constexpr int kSortList = 512;        // tokens of its rows that a warp notes as it scans
 constexpr int kSortLoads = 8;         // tokens per lane in flight
@@ -99,6 +101,8 @@ constexpr int kFlag = static_cast<int>(0x80000000u);
 // CTA b owns the rows v with v mod owners = b: frequent tokens, whose ids often lie
 // together, are spread over the CTAs (with contiguous ranges one of them had 57% of the
 // tokens of a 1 / (id + 1) distribution, and the launch took 17 us where it then took 9.5).
+// Above 262144 rows there are 256 CTAs, 512 above 524288, and one SM has room for one: 16384 x
+// 2688 added takes 38.2 us at 131072 rows, 40.6 at 262144, 43.1 at 262145, 55.0 at 524289.
 struct SortPlan {
   int shift, owners, range;  // log2 of the CTAs; rows of each, a multiple of 32
   int warps, span, list;     // scanning warps; tokens of each (a multiple of 32), tokens that it notes
@@ -107,7 +111,7 @@ struct SortPlan {
 
 SortPlan sort_plan(long long N, long long V) {
   SortPlan p;
-  p.shift = 7;
+  p.shift = kSortShift;
   while (((V - 1) >> p.shift) >= kSortMaxRange) ++p.shift;
   p.owners = 1 << p.shift;
   p.range = static_cast<int>((((V - 1) >> p.shift) + 32) / 32 * 32);

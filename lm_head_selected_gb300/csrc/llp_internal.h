@@ -269,7 +269,7 @@ cudaError_t launch_segment_sum(const float* part, int nseg, long long count, __n
 cudaError_t launch_bias_sum(const float* gb_part, int nblocks, int V, float* out, cudaStream_t s);
 
 // Token embedding (embedding.cu): lookup, and the table's gradient by sorted
-// tokens.  `stride`: elements between rows of grad_out.
+// tokens.
 struct EmbeddingParams {
   const long long* tokens;
   int N, V, D;
@@ -280,10 +280,11 @@ struct EmbeddingParams {
 cudaError_t embedding_setup();
 cudaError_t launch_embedding_fwd(const EmbeddingParams& p, const void* weight, void* out, cudaStream_t s);
 size_t embedding_bwd_workspace(long long N, long long V, long long D);
+// `stride`: elements between rows of grad_out.
 cudaError_t launch_embedding_bwd(const EmbeddingParams& p, const void* grad_out, long long stride, int accumulate,
                                  void* grad_weight, void* workspace, cudaStream_t s);
 
-// Layer norm (layer_norm.cu).  gy is the backward's upstream gradient; weight
+// Layer norm (layer_norm_fwd.cu, layer_norm_bwd.cu).  gy is the backward's upstream gradient; weight
 // and bias may be null.  gx, gw, gb may each be null.
 struct LayerNormParams {
   const void* x;
