@@ -28,19 +28,16 @@ def _check(x: torch.Tensor, name: str):
 
 def _counter(seed: int, offset: Offset, device_offset: Optional[torch.Tensor], device):
     """(seed, host offset, device pointer or None)."""
-    host = 0
-    if not isinstance(offset, torch.Tensor):
-        host = int(offset) & _MASK64
-    elif device_offset is not None:
-        raise ValueError("offset must be an int beside device_offset")
-    else:
-        device_offset = offset
     if device_offset is None:
-        return int(seed) & _MASK64, host, None
+        if not isinstance(offset, torch.Tensor):
+            return int(seed) & _MASK64, int(offset) & _MASK64, None
+        offset, device_offset = 0, offset
+    if isinstance(offset, torch.Tensor):
+        raise ValueError("offset must be an int beside device_offset")
     t = device_offset
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.numel() != 1 or t.device != device:
         raise ValueError("an offset must be an int, or one int64 on the inputs' device")
-    return int(seed) & _MASK64, host, t.data_ptr()
+    return int(seed) & _MASK64, int(offset) & _MASK64, t.data_ptr()
 
 
 def _probability(p: float) -> float:
