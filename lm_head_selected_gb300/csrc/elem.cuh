@@ -166,9 +166,10 @@ __device__ __forceinline__ void copy_wait() {
 // elements may start in the middle of one, so that its vectors take five words; they keep
 // that shift until they are read.  `lo`, `hi`: the tensor's first and one past its last
 // element; a word that sticks out of it is put together from elements instead.  Neighbouring
-// lanes' words lie 16 bytes apart, so that a warp's access takes four lines for 128 bytes, and
-// five copies and as many stores of a vector bound these rows by L1: layer norm of 16384 x
-// 1001 bf16 28.0 us, its gradient 35.8, where x 1000 takes 15.8 and 21.9.
+// lanes' words lie 16 bytes apart, so that a warp's access takes four lines for 128 bytes, five
+// times per vector each way, and L1 is the busiest unit (75 to 77% of its peak, HBM at 15 to
+// 26%): layer norm of 16384 x 1001 bf16 28.0 us, its gradient 35.8, where x 1000 takes 15.8
+// and 21.9.
 template <int DT, bool AL>
 struct Slot {
   using T = typename Elem<DT>::T;

@@ -23,7 +23,7 @@
 // 1001 into 50257 rows 38 us (82%; the sort 5.9).  Where the longest row decides, 65600 x
 // 512 into 101 rows 46 us, of which 19 are the sort (checks at every place and chunks of
 // the square root of the count, without groups: 75).  Rows of an odd number of 16-bit elements:
-// 16384 x 1001 into 50257 rows 39.4 us, added 41.3 (x 1000: 30.1, 26).
+// 16384 x 1001 into 50257 rows 39.4 us, added 41.0 (x 1000: 30.1, 24.9).
 #include "elem.cuh"
 
 namespace llp {
