@@ -20,8 +20,8 @@
 // ring once more for grad_x because the registers hold no more than the column sums;
 // wider ones take three plain kernels.
 //
-// Measured, bf16, three tensors of traffic: 16384 x 4096 67.1 us (6.0 TB/s, 89% of the
-// measured copy peak), 65600 x 2688 171 us (91%), 16384 x 2688 44.8 us (87%: 5 us are the
+// Measured, bf16, three tensors of traffic: 16384 x 4096 66.4 us (6.1 TB/s, 90% of the
+// measured copy peak), 65600 x 2688 166.5 us (94%), 16384 x 2688 45.1 us (87%: 5 us are the
 // join and the two launches' ends), 4096 x 16384 71 us (84%), 4096 x 8448 55 us (56%; three
 // plain kernels: 142).
 #include "layer_norm.cuh"
@@ -162,15 +162,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(
     float s0 = sum2(t0), s1 = sum2(t1);
     group_sums(s0, s1, red[i & 1][group], warp, warps, 1 + group);
     if (out != nullptr) {
-      // rstd * (a - s0 / D - h * s1 / D)
-      const float c0 = -s0 * inv * sc, c1 = -s1 * inv * sc;
+      // rstd * (a - s0 / D - h * s1 / D), rstd last: where grad_y * weight is one value in all of a
+      // row, nothing of it is left.  For that s0 / D has to be a quotient.  Its remainder under the
+      // product with 1 / D is exact in one fma, and the remainder's share corrects the product
+      // (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+      // 1990); the division took registers that 2688 columns do not have (44.8 -> 52.1 us).
+      const float q = s0 * inv;
+      const float c0 = -fmaf(fmaf(-q, static_cast<float>(p.D), s0), inv, q), c1 = -s1 * inv;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (on(k)) {
           F2(&av)[H] = a[HOLD ? k : 0], (&hv)[H] = h[HOLD ? k : 0];
           if (!HOLD) vector(k, av, hv, false);
 #pragma unroll
-          for (int i = 0; i < H; ++i) av[i] = fma2(av[i], f2(sc), fma2(hv[i], f2(c1), f2(c0)));
+          for (int i = 0; i < H; ++i) av[i] = mul2(fma2(hv[i], f2(c1), add2(av[i], f2(c0))), f2(sc));
           S::store(out + k * width * W, pack2<DT, W>(av), left(k));
         }
       }
@@ -258,13 +263,13 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_bwd_wide_x_kernel(Lay
     s0 += a;
     s1 = fmaf(a, (E::get(__ldg(x + c)) - m) * r, s1);
   }
-  s0 = cta_sum<kWideThreads>(s0, sm) * inv;
+  s0 = cta_sum<kWideThreads>(s0, sm) / static_cast<float>(p.D);
   s1 = cta_sum<kWideThreads>(s1, sm) * inv;
 #pragma unroll 4
   for (int c = threadIdx.x; c < p.D; c += kWideThreads) {
     const float a = E::get(__ldg(g + c)) * (w != nullptr ? P::get(__ldg(w + c)) : 1.f);
     const float h = (E::get(__ldg(x + c)) - m) * r;
-    gx[static_cast<size_t>(n) * p.D + c] = E::put((fmaf(-h, s1, a) - s0) * r);
+    gx[static_cast<size_t>(n) * p.D + c] = E::put(fmaf(-h, s1, a - s0) * r);
   }
 }
 

@@ -91,3 +91,29 @@ def test_forward_of_constant_rows(dtype, D):
     assert torch.equal(y, b.expand_as(y)) and not llp.layer_norm_fwd(x)[0].any()
     r = 1 / np.sqrt(float(np.float32(1e-5)))
     within("rstd", rstd, np.full(len(values), r), 4 * U32 * r)  # two units in the last place
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", WIDTHS + [7, 49, 383, 769])
+def test_gradients_of_one_upstream_value_per_row(dtype, D):
+    """grad_x without a weight: a - mean(a) is 0, and so is all of grad_x for a constant row of x;
+    for another one -h * mean(a h) * rstd is left, of the size of the rounding of a sum of h."""
+    import lm_head_selected_gb300 as llp
+    g = torch.Generator().manual_seed(D)
+    a = torch.tensor([1.0, 491.0, -0.375, 3.0, 7.0]).to(dtype)
+    x = torch.full((5, D), 5.0)
+    x[3:] = torch.randn(2, D, generator=g)
+    x = x.to(dtype)
+    xn, an = np64(x), np64(a)[:, None]
+    mean = torch.from_numpy(xn.mean(1)).float()
+    rstd = torch.from_numpy(1.0 / np.sqrt(((xn - np64(mean)[:, None]) ** 2).mean(1) + 1e-5)).float()
+    gx = llp.layer_norm_bwd(a[:, None].expand(-1, D).contiguous().cuda(), x.cuda(), mean.cuda(), rstd.cuda(),
+                            need_weight=False, need_bias=False)[0]
+    assert not gx[:3].any()
+    m, r = np64(mean)[:, None], np64(rstd)[:, None]
+    h = (xn - m) * r
+    ref = -h * (an * h).mean(1, keepdims=True) * r
+    # the sum of a h, the roundings of h and of the terms, one of the result
+    s2 = np.abs(an * h).mean(1, keepdims=True)
+    err = r * np.abs(h) * (sum_depth(D) + 8) * U32 * s2
+    within("grad_x", gx, ref, (1 + 1e-2) * (rounded(ref, dtype) + err))
