@@ -168,7 +168,7 @@ __device__ __forceinline__ void copy_wait() {
 // element; a word that sticks out of it is put together from elements instead.  Neighbouring
 // lanes' words lie 16 bytes apart, so that a warp's access takes four lines for 128 bytes, five
 // times per vector each way, and L1 is the busiest unit (75 to 77% of its peak, HBM at 15 to
-// 26%): layer norm of 16384 x 1001 bf16 28.0 us, its gradient 35.8, where x 1000 takes 15.8
+// 26%): layer norm of 16384 x 1001 bf16 28.0 us, its gradient 36.0, where x 1000 takes 15.8
 // and 21.9.
 template <int DT, bool AL>
 struct Slot {

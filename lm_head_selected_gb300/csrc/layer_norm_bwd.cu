@@ -20,8 +20,8 @@
 // ring once more for grad_x because the registers hold no more than the column sums;
 // wider ones take three plain kernels.
 //
-// Measured, bf16, three tensors of traffic: 16384 x 4096 66.4 us (6.1 TB/s, 90% of the
-// measured copy peak), 65600 x 2688 166.5 us (94%), 16384 x 2688 45.1 us (87%: 5 us are the
+// Measured, bf16, three tensors of traffic: 16384 x 4096 66.2 us (6.1 TB/s, 90% of the
+// measured copy peak), 65600 x 2688 164 to 166 us (94%), 16384 x 2688 45.1 us (87%: 5 us are the
 // join and the two launches' ends), 4096 x 16384 71 us (84%), 4096 x 8448 55 us (56%; three
 // plain kernels: 142).
 #include "layer_norm.cuh"
