@@ -1,5 +1,6 @@
 """GB300-native fused linear selected-token log-probability, and the operators
-around it: token embedding, layer norm, dropout.
+around it: token embedding, layer norm, dropout, the gated linear layer and the RMS
+norms of a model's blocks, and the AdamW step over its parameters.
 
 The computation lives in ``liblinear_logp.so`` (sm_103a CUDA kernels behind the
 C ABI of the headers in ``include/``); this package only marshals PyTorch tensors
@@ -14,6 +15,7 @@ from .fused import (  # noqa: F401
     fused_logp_fwd,
     fused_logp_fwd_indexed,
 )
+from .gated import gated_linear, gated_linear_bwd, gated_linear_fwd  # noqa: F401
 from .norm import layer_norm, layer_norm_bwd, layer_norm_fwd  # noqa: F401
 from .ops import (  # noqa: F401
     IGNORE_INDEX,
@@ -26,3 +28,5 @@ from .ops import (  # noqa: F401
     linear_logp_fwd,
     linear_logp_fwd_indexed,
 )
+from .optim import adamw_state, adamw_step  # noqa: F401
+from .residual import residual_rms_norm, residual_rms_norm_bwd, residual_rms_norm_fwd  # noqa: F401

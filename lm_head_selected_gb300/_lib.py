@@ -72,6 +72,16 @@ EXPORTED_OPERATORS = (
     "dropout_fwd",
     "dropout_bwd",
 )
+# include/gated_linear.h, include/residual_rms_norm.h, include/adamw.h (a model's blocks and their optimizer)
+EXPORTED_BLOCKS = (
+    "gated_linear_fwd",
+    "gated_linear_bwd_workspace_bytes",
+    "gated_linear_bwd",
+    "residual_rms_norm_fwd",
+    "residual_rms_norm_bwd_workspace_bytes",
+    "residual_rms_norm_bwd",
+    "adamw_step",
+)
 DEVICE_SELFTEST_CODE = 6
 LLP_ERR_SCRATCH_LIMIT = -8
 
@@ -202,6 +212,22 @@ def load() -> ctypes.CDLL:
         lib.dropout_fwd.restype = _i
         lib.dropout_bwd.argtypes = [_p, _i, _i64, _f64, _u64, _u64, _p, _p, _p]
         lib.dropout_bwd.restype = _i
+        lib.gated_linear_fwd.argtypes = [_p, _p, _p, _i, _i, _i64, _i64, _i64, _p, _p, _p]
+        lib.gated_linear_fwd.restype = _i
+        lib.gated_linear_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        lib.gated_linear_bwd_workspace_bytes.restype = _size
+        lib.gated_linear_bwd.argtypes = [_p, _p, _p, _p, _p, _i, _i, _i64, _i64, _i64, _p, _p, _p, _p, _size, _p]
+        lib.gated_linear_bwd.restype = _i
+        lib.residual_rms_norm_fwd.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i, _p, _p, _i, _i, _i64, _i64, _f32, _f32,
+                                              _p, _p, _p, _p, _p]
+        lib.residual_rms_norm_fwd.restype = _i
+        lib.residual_rms_norm_bwd_workspace_bytes.argtypes = [_i64, _i64]
+        lib.residual_rms_norm_bwd_workspace_bytes.restype = _size
+        lib.residual_rms_norm_bwd.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p, _p, _p, _i,
+                                              _i, _i64, _i64, _f32, _p, _p, _p, _p, _p, _p, _size, _p]
+        lib.residual_rms_norm_bwd.restype = _i
+        lib.adamw_step.argtypes = [_i64] + [_p] * 11 + [_i] + [_f64] * 4 + [_i64] + [_p] * 4
+        lib.adamw_step.restype = _i
         _lib = lib
         return lib
 

@@ -7,14 +7,21 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
+#include "adamw.h"
+#include "adamw_internal.h"
 #include "dropout.h"
 #include "embedding.h"
 #include "fused_logp.h"
+#include "gated.h"
+#include "gated_linear.h"
 #include "layer_norm.h"
 #include "linear_logp.h"
 #include "llp_internal.h"
+#include "residual_norm.h"
+#include "residual_rms_norm.h"
 #include "sm103_ptx.cuh"
 
 // Code of the last failed CUDA call made by this library on the calling thread,
@@ -49,6 +56,7 @@ struct DeviceInit {
   int num_sms = 0;
   unsigned int* status_ptr = nullptr;
   llp::LaunchCaps caps = {};
+  llp::GatedCaps gated = {};
 };
 
 std::mutex g_mu;
@@ -116,6 +124,7 @@ int init_device(DeviceInit** out) {
     } else if (llp::fwd_setup(&d.caps) != cudaSuccess || llp::bwd_setup(&d.caps) != cudaSuccess ||
                llp::small_grad_hidden_setup() != cudaSuccess || llp::embedding_setup() != cudaSuccess ||
                llp::layer_norm_fwd_setup() != cudaSuccess || llp::layer_norm_bwd_setup() != cudaSuccess ||
+               llp::gated_setup(&d.gated) != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status_ptr), g_status_word) != cudaSuccess) {
       d.status = fail_cuda(__LINE__);
     } else {
@@ -255,6 +264,21 @@ int make_map_part(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, es,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) g_last_driver_result = static_cast<int>(r);
+  return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
+}
+
+// Output map of a stack of `planes` 16-bit matrices [rows][cols], box {64, 32, 1}: a store clips at
+// `rows` inside each.
+int make_map_planes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, bool f16) {
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  cuuint32_t box[3] = {64, 32, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) g_last_driver_result = static_cast<int>(r);
   return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
 }
@@ -1390,6 +1414,454 @@ int dropout_fwd(const void* x, const void* residual, int dtype, int64_t count, d
 int dropout_bwd(const void* grad_y, int dtype, int64_t count, double p, uint64_t seed, uint64_t offset,
                 const int64_t* device_offset, void* grad_x, void* stream) {
   return dropout_call(grad_y, nullptr, dtype, count, p, seed, offset, device_offset, grad_x, stream);
+}
+
+// ----------------------------------------------------------------------------
+// Gated linear layer (gated_linear.h)
+// ----------------------------------------------------------------------------
+static int64_t gated_pad(int64_t F) { return static_cast<int64_t>(round_up(static_cast<size_t>(F), 128)); }
+
+static int gated_shapes(int dtype, int act, int64_t N, int64_t D, int64_t F) {
+  if ((dtype != llp::kDtypeBF16 && dtype != llp::kDtypeF16) || act < 0 || act > GATED_LINEAR_GELU_TANH)
+    return LLP_ERR_BAD_SHAPE;
+  if (N < 0 || D < 8 || F < 8 || (D % 8) != 0 || (F % 8) != 0) return LLP_ERR_BAD_SHAPE;
+  if (N > kLim31 || D >= (int64_t(1) << 30) || F >= (int64_t(1) << 30) - 128) return LLP_ERR_BAD_SHAPE;
+  if (!product_ok(N, D) || !product_ok(N, 4 * gated_pad(F)) || !product_ok(F, D)) return LLP_ERR_BAD_SHAPE;
+  // every work-unit count and tile index must fit a 32-bit int
+  const int64_t num_m = cdiv(N, llp::kUnitM), num_d = cdiv(D, llp::kTileN);
+  if (num_m * cdiv(F, llp::kTileN / 2) > kLim31 || num_m * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
+  if (2 * cdiv(F, llp::kUnitM) * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
+  return LLP_OK;
+}
+
+int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dtype, int act, int64_t N, int64_t D,
+                     int64_t F, void* y, void* pre, void* stream) {
+  int st = gated_shapes(dtype, act, N, D, F);
+  if (st != LLP_OK) return st;
+  if (N == 0) return LLP_OK;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || y == nullptr) return LLP_ERR_NULL_POINTER;
+  if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(y, 16) || !aligned(pre, 16))
+    return LLP_ERR_MISALIGNED;
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  if ((st = load_encode_fn()) != LLP_OK) return st;
+  const bool f16 = dtype == llp::kDtypeF16;
+  const int kps = k_blocks_per_stage(D, false);
+  CUtensorMap tm_x, tm_wg, tm_wu, tm_y, tm_pre;
+  if (make_kmajor_maps(&tm_x, &tm_wg, x, w_gate, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
+      make_kmajor_maps(&tm_x, &tm_wu, x, w_up, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
+      make_map(&tm_y, y, F, N, F * 2, 64, 32, f16) != LLP_OK)
+    return fail_cuda(__LINE__);
+  if (pre == nullptr)
+    tm_pre = tm_y;  // not stored through
+  else if (make_map_planes(&tm_pre, pre, F, N, 2, f16) != LLP_OK)
+    return fail_cuda(__LINE__);
+  llp::GatedFwdParams p = {};
+  p.N = static_cast<int>(N);
+  p.D = static_cast<int>(D);
+  p.F = static_cast<int>(F);
+  p.num_m = static_cast<int>(cdiv(N, llp::kUnitM));
+  p.num_ft = static_cast<int>(cdiv(F, llp::kTileN / 2));
+  p.group_m = llp::kGroupM;
+  p.keep = pre != nullptr;
+  p.act = act;
+  p.f16 = f16 ? 1 : 0;
+  p.kps = kps;
+  p.err = dev->status_ptr;
+  const cudaError_t e =
+      llp::launch_gated_fwd(tm_x, tm_wg, tm_wu, tm_y, tm_pre, p, dev->gated, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+namespace {
+struct GatedLayout {
+  size_t sched, dpre, total;
+};
+GatedLayout gated_layout(int64_t N, int64_t F) {
+  Carver c;
+  GatedLayout L;
+  L.sched = c.take(llp::kNumSchedCounters * sizeof(int));
+  L.dpre = c.take(static_cast<size_t>(N) * 2 * gated_pad(F) * 2);
+  L.total = c.off;
+  return L;
+}
+}  // namespace
+
+size_t gated_linear_bwd_workspace_bytes(int64_t N, int64_t D, int64_t F) {
+  if (N <= 0 || gated_shapes(llp::kDtypeBF16, 0, N, D, F) != LLP_OK) return 0;
+  return gated_layout(N, F).total;
+}
+
+int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const void* w_gate, const void* w_up,
+                     int dtype, int act, int64_t N, int64_t D, int64_t F, void* grad_x, void* grad_w_gate,
+                     void* grad_w_up, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = gated_shapes(dtype, act, N, D, F);
+  if (st != LLP_OK) return st;
+  const bool want_w = grad_w_gate != nullptr || grad_w_up != nullptr;
+  if (grad_x == nullptr && !want_w) return LLP_OK;
+  if (N == 0 && !want_w) return LLP_OK;
+  if (!aligned(grad_x, 16) || !aligned(grad_w_gate, 16) || !aligned(grad_w_up, 16)) return LLP_ERR_MISALIGNED;
+  if (N > 0) {
+    if (grad_y == nullptr || pre == nullptr || workspace == nullptr) return LLP_ERR_NULL_POINTER;
+    if ((want_w && x == nullptr) || (grad_x != nullptr && (w_gate == nullptr || w_up == nullptr)))
+      return LLP_ERR_NULL_POINTER;
+    if (!aligned(grad_y, 16) || !aligned(pre, 16) || !aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) ||
+        !aligned(workspace, 16))
+      return LLP_ERR_MISALIGNED;
+    if (workspace_bytes < gated_linear_bwd_workspace_bytes(N, D, F)) return LLP_ERR_WORKSPACE_TOO_SMALL;
+  }
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    void* const outs[2] = {grad_w_gate, grad_w_up};
+    for (void* o : outs) {
+      if (o != nullptr && llp::note_cuda(cudaMemsetAsync(o, 0, static_cast<size_t>(F) * D * 2, s)) != cudaSuccess)
+        return fail_cuda(__LINE__);
+    }
+    return LLP_OK;
+  }
+  if ((st = load_encode_fn()) != LLP_OK) return st;
+  const bool f16 = dtype == llp::kDtypeF16;
+  const int64_t P = gated_pad(F);
+  const GatedLayout L = gated_layout(N, F);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  int* const sched = reinterpret_cast<int*>(ws + L.sched);  // zeroed by the elementwise kernel
+  uint8_t* const dpre = ws + L.dpre;
+  const llp::GatedBwdParams b = {grad_y, pre, dpre, sched, static_cast<int>(N), static_cast<int>(F),
+                                 static_cast<int>(P), dtype, act};
+  if (llp::launch_gated_dpre(b, dev->num_sms, s) != cudaSuccess) return fail_cuda(__LINE__);
+  const bool d_chunked = LLP_CHUNKED_MN && !LLP_HALF_TILE && (D % 64) == 0;  // half tiles load one chunk
+  if (grad_x != nullptr) {
+    // one K block per stage, as in the linear log-prob's grad_hidden
+    CUtensorMap tm_d, tm_wg, tm_wu, tm_gx;
+    if (make_map(&tm_d, dpre, 2 * P, N, 4 * P, llp::kTileK, llp::kTileM, f16) != LLP_OK) return fail_cuda(__LINE__);
+    const void* const w[2] = {w_gate, w_up};
+    CUtensorMap* const tm_w[2] = {&tm_wg, &tm_wu};
+    for (int k = 0; k < 2; ++k) {
+      const int r = d_chunked ? make_map_chunked(tm_w[k], w[k], D, F, D * 2, llp::kTileK, llp::kBRows / 64, f16)
+                              : make_map(tm_w[k], w[k], D, F, D * 2, 64, llp::kTileK, f16);
+      if (r != LLP_OK) return fail_cuda(__LINE__);
+    }
+    llp::GatedGradXParams p = {};
+    p.b_chunked = d_chunked ? 1 : 0;
+    p.kps = 1;
+    p.rows = static_cast<int>(N);
+    p.D = static_cast<int>(D);
+    p.K = static_cast<int>(2 * P);
+    p.num_m = static_cast<int>(cdiv(N, llp::kUnitM));
+    p.num_d = static_cast<int>(cdiv(D, llp::kTileN));
+    p.nseg = 1;
+    p.kseg_blocks = static_cast<int>(2 * P / llp::kTileK);
+    p.half_blocks = static_cast<int>(P / llp::kTileK);
+    p.out = static_cast<__nv_bfloat16*>(grad_x);
+    p.err = dev->status_ptr;
+    p.f16 = f16 ? 1 : 0;
+    p.sched = !force_static_schedule() && max_unit_kblocks(p) >= llp::kDynMinKBlocks ? sched + 0 : nullptr;
+    if (make_map_grad_out(&tm_gx, p) != LLP_OK) return fail_cuda(__LINE__);
+    if (llp::launch_gated_grad_x(tm_d, tm_wg, tm_wu, tm_gx, p, dev->gated, s) != cudaSuccess)
+      return fail_cuda(__LINE__);
+  }
+  if (want_w) {
+    CUtensorMap tm_d, tm_x, tm_g, tm_u;
+    const int kps = ((LLP_KPS2 & 4) && LLP_CHUNKED_MN && d_chunked && N >= 1024) ? 2 : 1;
+    if ((LLP_CHUNKED_MN ? make_map_chunked(&tm_d, dpre, 2 * P, N, 4 * P, llp::kTileK * kps, llp::kTileM / 64, f16)
+                        : make_map(&tm_d, dpre, 2 * P, N, 4 * P, 64, llp::kTileK, f16)) != LLP_OK ||
+        (d_chunked ? make_map_chunked(&tm_x, x, D, N, D * 2, llp::kTileK * kps, llp::kBRows / 64, f16)
+                   : make_map(&tm_x, x, D, N, D * 2, 64, llp::kTileK, f16)) != LLP_OK)
+      return fail_cuda(__LINE__);
+    llp::GatedGradWParams p = {};
+    p.a_chunked = LLP_CHUNKED_MN ? 1 : 0;
+    p.b_chunked = d_chunked ? 1 : 0;
+    p.kps = kps;
+    p.rows = static_cast<int>(F);
+    p.D = static_cast<int>(D);
+    p.K = static_cast<int>(N);
+    p.tiles = static_cast<int>(cdiv(F, llp::kUnitM));
+    p.first_tile = grad_w_gate == nullptr ? p.tiles : 0;
+    p.num_m = grad_w_gate != nullptr && grad_w_up != nullptr ? 2 * p.tiles : p.tiles;
+    p.F_pad = static_cast<int>(P);
+    p.num_d = static_cast<int>(cdiv(D, llp::kTileN));
+    p.nseg = 1;
+    p.kseg_blocks = static_cast<int>(cdiv(N, llp::kTileK));
+    p.err = dev->status_ptr;
+    p.f16 = f16 ? 1 : 0;
+    p.sched = !force_static_schedule() && max_unit_kblocks(p) >= llp::kDynMinKBlocks ? sched + 1 : nullptr;
+    p.out = static_cast<__nv_bfloat16*>(grad_w_gate != nullptr ? grad_w_gate : grad_w_up);
+    if (make_map_grad_out(&tm_g, p) != LLP_OK) return fail_cuda(__LINE__);
+    p.out = static_cast<__nv_bfloat16*>(grad_w_up != nullptr ? grad_w_up : grad_w_gate);
+    if (make_map_grad_out(&tm_u, p) != LLP_OK) return fail_cuda(__LINE__);
+    if (llp::launch_gated_grad_w(tm_d, tm_x, tm_g, tm_u, p, dev->gated, s) != cudaSuccess) return fail_cuda(__LINE__);
+  }
+  return LLP_OK;
+}
+
+// ----------------------------------------------------------------------------
+// RMS norms around a block (residual_rms_norm.h)
+// ----------------------------------------------------------------------------
+static int residual_norm_shapes(int dtype, int param_dtype, int64_t N, int64_t D, int gate_kind, const void* gate,
+                                const void* branch, const void* post_weight, const void* weight, float scale) {
+  if (!dtype_ok(dtype) || (param_dtype != dtype && param_dtype != llp::kDtypeF32)) return LLP_ERR_BAD_SHAPE;
+  if (N < 0 || D < 1 || N > kLim31 || D >= kMaxOpD || !std::isfinite(scale)) return LLP_ERR_BAD_SHAPE;
+  if (gate_kind < llp::kGateNone || gate_kind > llp::kGateRows) return LLP_ERR_BAD_SHAPE;
+  // a gate and a norm after the block need the block's output; without it there is the other norm
+  if (branch == nullptr && N > 0 && (gate_kind != llp::kGateNone || post_weight != nullptr || weight == nullptr))
+    return LLP_ERR_NULL_POINTER;
+  if (N > 0 && gate_kind != llp::kGateNone && gate == nullptr) return LLP_ERR_NULL_POINTER;
+  return gate_kind == llp::kGateNone && gate != nullptr ? LLP_ERR_BAD_SHAPE : LLP_OK;
+}
+
+int residual_rms_norm_fwd(const void* x, int64_t x_row_stride, const void* branch, int64_t branch_row_stride,
+                          const void* gate, int64_t gate_row_stride, int gate_kind, const void* post_weight,
+                          const void* weight, int dtype, int param_dtype, int64_t N, int64_t D, float scale, float eps,
+                          void* s, void* h, float* post_rstd, float* rstd, void* stream) {
+  int st = residual_norm_shapes(dtype, param_dtype, N, D, gate_kind, gate, branch, post_weight, weight, scale);
+  if (st != LLP_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return LLP_ERR_BAD_SHAPE;
+  if (!row_stride_ok(N, D, x_row_stride) || (branch != nullptr && !row_stride_ok(N, D, branch_row_stride)) ||
+      (gate_kind == llp::kGateRows && !row_stride_ok(N, D, gate_row_stride)))
+    return LLP_ERR_BAD_SHAPE;
+  if (N == 0) return LLP_OK;
+  if (x == nullptr || (branch != nullptr) != (s != nullptr) || (weight != nullptr) != (h != nullptr) ||
+      (weight != nullptr) != (rstd != nullptr) || (post_weight != nullptr) != (post_rstd != nullptr))
+    return LLP_ERR_NULL_POINTER;
+  const uintptr_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  if (!aligned(x, es) || !aligned(branch, es) || !aligned(gate, gate_kind == llp::kGateRows ? es : ps) ||
+      !aligned(post_weight, ps) || !aligned(weight, ps) || !aligned(s, es) || !aligned(h, es) ||
+      !aligned(post_rstd, 4) || !aligned(rstd, 4))
+    return LLP_ERR_MISALIGNED;
+  DeviceInit* dev = nullptr;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  llp::ResidualNormParams p = {};
+  p.x = x;
+  p.branch = branch;
+  p.gate = gate;
+  p.x_stride = x_row_stride;
+  p.b_stride = branch_row_stride;
+  p.gate_stride = gate_row_stride;
+  p.post_weight = post_weight;
+  p.weight = weight;
+  p.gate_kind = gate_kind;
+  p.N = static_cast<int>(N);
+  p.D = static_cast<int>(D);
+  p.dtype = dtype;
+  p.param_dtype = param_dtype;
+  p.scale = scale;
+  p.eps = eps;
+  const cudaError_t e = llp::launch_residual_norm_fwd(p, {s, h, post_rstd, rstd}, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+size_t residual_rms_norm_bwd_workspace_bytes(int64_t N, int64_t D) {
+  if (N <= 0 || N > kLim31 || D < 1 || D >= kMaxOpD) return 0;
+  return llp::residual_norm_bwd_workspace(N, D);
+}
+
+int residual_rms_norm_bwd(const void* grad_s, int64_t grad_s_row_stride, const void* grad_h, int64_t grad_h_row_stride,
+                          const void* s, int64_t s_row_stride, const void* branch, int64_t branch_row_stride,
+                          const void* gate, int64_t gate_row_stride, int gate_kind, const void* post_weight,
+                          const void* weight, const float* post_rstd, const float* rstd, int dtype, int param_dtype,
+                          int64_t N, int64_t D, float scale, void* grad_x, void* grad_b, void* grad_gate,
+                          void* grad_post_weight, void* grad_weight, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st = residual_norm_shapes(dtype, param_dtype, N, D, gate_kind, gate, branch, post_weight, weight, scale);
+  if (st != LLP_OK) return st;
+  if ((grad_s != nullptr && !row_stride_ok(N, D, grad_s_row_stride)) ||
+      (weight != nullptr && (!row_stride_ok(N, D, grad_h_row_stride) || !row_stride_ok(N, D, s_row_stride))) ||
+      (branch != nullptr && !row_stride_ok(N, D, branch_row_stride)) ||
+      (gate_kind == llp::kGateRows && !row_stride_ok(N, D, gate_row_stride)))
+    return LLP_ERR_BAD_SHAPE;
+  // gradients of what the forward was not given
+  if ((grad_b != nullptr && branch == nullptr && N > 0) || (grad_gate != nullptr && gate_kind == llp::kGateNone) ||
+      (grad_post_weight != nullptr && post_weight == nullptr && N > 0) ||
+      (grad_weight != nullptr && weight == nullptr && N > 0))
+    return LLP_ERR_NULL_POINTER;
+  const uintptr_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  const uintptr_t gs = gate_kind == llp::kGateRows ? es : ps;
+  if (!aligned(grad_gate, gs) || !aligned(grad_post_weight, ps) || !aligned(grad_weight, ps)) return LLP_ERR_MISALIGNED;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  DeviceInit* dev = nullptr;
+  if (N == 0) {
+    void* const outs[3] = {gate_kind == llp::kGateColumns ? grad_gate : nullptr, grad_post_weight, grad_weight};
+    if (outs[0] == nullptr && outs[1] == nullptr && outs[2] == nullptr) return LLP_OK;
+    if ((st = init_device(&dev)) != LLP_OK) return st;
+    for (void* o : outs) {
+      if (o != nullptr && llp::note_cuda(cudaMemsetAsync(o, 0, static_cast<size_t>(D) * ps, cs)) != cudaSuccess)
+        return fail_cuda(__LINE__);
+    }
+    return LLP_OK;
+  }
+  if (grad_x == nullptr && grad_b == nullptr && grad_gate == nullptr && grad_post_weight == nullptr &&
+      grad_weight == nullptr)
+    return LLP_OK;
+  if (grad_s == nullptr && weight == nullptr) return LLP_ERR_NULL_POINTER;  // no gradient comes in
+  if (weight != nullptr && (grad_h == nullptr || s == nullptr || rstd == nullptr)) return LLP_ERR_NULL_POINTER;
+  if ((post_weight != nullptr && post_rstd == nullptr) || workspace == nullptr) return LLP_ERR_NULL_POINTER;
+  if (!aligned(grad_s, es) || !aligned(grad_h, es) || !aligned(s, es) || !aligned(branch, es) || !aligned(gate, gs) ||
+      !aligned(post_weight, ps) || !aligned(weight, ps) || !aligned(post_rstd, 4) || !aligned(rstd, 4) ||
+      !aligned(grad_x, es) || !aligned(grad_b, es) || !aligned(workspace, 16))
+    return LLP_ERR_MISALIGNED;
+  if (workspace_bytes < residual_rms_norm_bwd_workspace_bytes(N, D)) return LLP_ERR_WORKSPACE_TOO_SMALL;
+  if ((st = init_device(&dev)) != LLP_OK) return st;
+  llp::ResidualNormParams p = {};
+  p.x = s;
+  p.branch = branch;
+  p.gate = gate;
+  p.gs = grad_s;
+  p.gh = grad_h;
+  p.x_stride = s_row_stride;
+  p.b_stride = branch_row_stride;
+  p.gate_stride = gate_row_stride;
+  p.gs_stride = grad_s_row_stride;
+  p.gh_stride = grad_h_row_stride;
+  p.post_weight = post_weight;
+  p.weight = weight;
+  p.gate_kind = gate_kind;
+  p.N = static_cast<int>(N);
+  p.D = static_cast<int>(D);
+  p.dtype = dtype;
+  p.param_dtype = param_dtype;
+  p.scale = scale;
+  const cudaError_t e = llp::launch_residual_norm_bwd(
+      p, {post_rstd, rstd, grad_x, grad_b, grad_gate, grad_post_weight, grad_weight, workspace}, cs);
+  return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+// ----------------------------------------------------------------------------
+// AdamW (adamw.h)
+// ----------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+// Elements before all arrays of a tensor with 32-bit states reach a 16-byte boundary, or -1.
+int adamw_head(const llp::AdamTensor& t) {
+  const uintptr_t ps = dtype_bytes(t.param_dtype), gs = dtype_bytes(t.grad_dtype);
+  for (int e = 0; e < 8 && e <= t.n; ++e) {
+    auto at = [&](const void* p, uintptr_t size) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) + e * size) % 16 == 0; };
+    if (at(t.p, ps) && at(t.g, gs) && at(t.m, 4) && at(t.v, 4) && at(t.master, 4)) return e;
+  }
+  return -1;
+}
+
+template <int MOST>
+int adamw_launch(const llp::AdamScalars& k, const std::vector<llp::AdamTensor>& all, size_t first, size_t last,
+                 int chunks, int bits, const DeviceInit* dev, cudaStream_t s) {
+  llp::AdamTable<MOST> table;
+  table.k = k;
+  table.count = static_cast<int>(last - first);
+  table.chunks = chunks;
+  std::memcpy(table.t, all.data() + first, (last - first) * sizeof(llp::AdamTensor));
+  return llp::launch_adamw<MOST>(table, bits, dev->num_sms, s) == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+}
+
+int adamw_checked(int64_t count, void* const* params, const void* const* grads, void* const* exp_avg,
+                  void* const* exp_avg_sq, float* const* m_scale, float* const* v_scale, float* const* masters,
+                  const int64_t* sizes, const int32_t* param_dtypes, const int32_t* grad_dtypes, const double* decay,
+                  int bits, std::vector<llp::AdamTensor>* all) {
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t n = sizes[i];
+    if (n < 0 || n > (int64_t(1) << 40) || !dtype_ok(param_dtypes[i]) || !std::isfinite(decay[i]) ||
+        (grad_dtypes[i] != param_dtypes[i] && grad_dtypes[i] != llp::kDtypeF32))
+      return LLP_ERR_BAD_SHAPE;
+    if (n == 0) continue;
+    llp::AdamTensor t = {};
+    t.p = params[i];
+    t.g = grads[i];
+    t.m = exp_avg[i];
+    t.v = exp_avg_sq[i];
+    t.m_scale = bits == 8 ? m_scale[i] : nullptr;
+    t.v_scale = bits == 8 ? v_scale[i] : nullptr;
+    t.master = masters != nullptr ? masters[i] : nullptr;
+    t.n = n;
+    t.decay = static_cast<float>(decay[i]);
+    t.param_dtype = static_cast<unsigned char>(param_dtypes[i]);
+    t.grad_dtype = static_cast<unsigned char>(grad_dtypes[i]);
+    if (t.p == nullptr || t.g == nullptr || t.m == nullptr || t.v == nullptr ||
+        (bits == 8 && (t.m_scale == nullptr || t.v_scale == nullptr)))
+      return LLP_ERR_NULL_POINTER;
+    const uintptr_t ss = bits == 8 ? 1 : 4;
+    if (!aligned(t.p, dtype_bytes(t.param_dtype)) || !aligned(t.g, dtype_bytes(t.grad_dtype)) || !aligned(t.m, ss) ||
+        !aligned(t.v, ss) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4) || !aligned(t.master, 4))
+      return LLP_ERR_MISALIGNED;
+    if (bits == 8)
+      t.head = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.master, 16) && aligned(t.m, 8) && aligned(t.v, 8) ? 0 : -1;
+    else
+      t.head = static_cast<short>(adamw_head(t));
+    all->push_back(t);
+  }
+  return LLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int adamw_step(int64_t count, void* const* params, const void* const* grads, void* const* exp_avg,
+               void* const* exp_avg_sq, float* const* exp_avg_scale, float* const* exp_avg_sq_scale,
+               float* const* masters, const int64_t* sizes, const int32_t* param_dtypes, const int32_t* grad_dtypes,
+               const double* weight_decay, int state_bits, double lr, double beta1, double beta2, double eps,
+               int64_t step, const int64_t* device_step, const float* device_lr, const float* grad_scale,
+               void* stream) {
+  if (count < 0 || count > kLim31 || (state_bits != 32 && state_bits != 8)) return LLP_ERR_BAD_SHAPE;
+  if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
+      !std::isfinite(eps) || step < (device_step != nullptr ? 0 : 1))
+    return LLP_ERR_BAD_SHAPE;
+  if (!aligned(device_step, 8) || !aligned(device_lr, 4) || !aligned(grad_scale, 4)) return LLP_ERR_MISALIGNED;
+  if (count == 0) return LLP_OK;
+  if (params == nullptr || grads == nullptr || exp_avg == nullptr || exp_avg_sq == nullptr || sizes == nullptr ||
+      param_dtypes == nullptr || grad_dtypes == nullptr || weight_decay == nullptr ||
+      (state_bits == 8) != (exp_avg_scale != nullptr) || (state_bits == 8) != (exp_avg_sq_scale != nullptr))
+    return LLP_ERR_NULL_POINTER;
+  try {
+    std::vector<llp::AdamTensor> all;
+    all.reserve(static_cast<size_t>(count));
+    int st = adamw_checked(count, params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, masters, sizes,
+                           param_dtypes, grad_dtypes, weight_decay, state_bits, &all);
+    if (st != LLP_OK || all.empty()) return st;
+    DeviceInit* dev = nullptr;
+    if ((st = init_device(&dev)) != LLP_OK) return st;
+    llp::AdamScalars k = {};
+    k.beta1 = beta1;
+    k.beta2 = beta2;
+    k.b1 = static_cast<float>(beta1);
+    k.c1 = static_cast<float>(1.0 - beta1);
+    k.b2 = static_cast<float>(beta2);
+    k.c2 = static_cast<float>(1.0 - beta2);
+    k.eps = static_cast<float>(eps);
+    k.rate = static_cast<float>(lr);
+    k.step = step;
+    if (device_step == nullptr) {
+      k.rate_m = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+      k.root_v = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+    }
+    k.device_step = reinterpret_cast<const long long*>(device_step);
+    k.device_lr = device_lr;
+    k.grad_scale = grad_scale;
+    // as many tensors to a launch as its parameters hold
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    size_t first = 0;
+    while (first < all.size()) {
+      size_t last = first;
+      int64_t chunks = 0;
+      while (last < all.size() && last - first < static_cast<size_t>(llp::kAdamMany)) {
+        const int64_t head = all[last].head > 0 ? all[last].head : 0;
+        const int64_t own = all[last].n > head ? cdiv(all[last].n - head, llp::kAdamChunk) : 1;
+        if (last > first && chunks + own > (int64_t(1) << 30)) break;
+        all[last].first_chunk = static_cast<int>(chunks);
+        chunks += own;
+        ++last;
+      }
+      st = last - first <= static_cast<size_t>(llp::kAdamFew)
+               ? adamw_launch<llp::kAdamFew>(k, all, first, last, static_cast<int>(chunks), state_bits, dev, s)
+               : adamw_launch<llp::kAdamMany>(k, all, first, last, static_cast<int>(chunks), state_bits, dev, s);
+      if (st != LLP_OK) return st;
+      first = last;
+    }
+    return LLP_OK;
+  } catch (const std::bad_alloc&) {
+    return fail_cuda(__LINE__);
+  }
 }
 
 // One thread waits, with the production wait code, on a barrier that nothing

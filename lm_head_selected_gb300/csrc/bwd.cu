@@ -22,7 +22,7 @@
 // segments whose FP32 partials are summed in a fixed ascending order"); here
 // fp32 accumulation in TMEM has no length limit, the segments only fix the
 // reduction order and spread the long vocab reduction over more SMs.
-#include "gemm_core.cuh"
+#include "grad_gemm.cuh"
 
 namespace llp {
 
@@ -48,28 +48,13 @@ __device__ __forceinline__ float warp_column_sums(float (&x)[32], int lane) {
   return x[0];
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
-  __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Two floats rounded to the path's 16-bit type (fp16 when f16, else bf16).
-__device__ __forceinline__ uint32_t pack16x2(bool f16, float a, float b) {
-  return f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-}
-
 // ----------------------------------------------------------------------------
 // B1: dlogits
 // ----------------------------------------------------------------------------
 // PAIRED = false: single CTAs with 128-row tiles, for a batch that fits in one.
 // AROWS: hidden rows loaded per stage (kSmallARows for a batch that small).
 template <bool HAS_BIAS, bool PAIRED = kPairMMA, int AROWS = kTileM>
-struct DzCfg {
+struct DzCfg : PlainOperands {
   static constexpr bool A_MN = false;
   static constexpr bool B_MN = false;
   static constexpr bool PAIR = PAIRED;
@@ -213,114 +198,6 @@ struct DzCfg {
   static __device__ __forceinline__ void unit_end(const Params&, const UnitInfo&, int, int, RowState&) {}
 };
 
-// ----------------------------------------------------------------------------
-// B2 / B3: gradient GEMMs with fixed K segments.
-// ----------------------------------------------------------------------------
-template <bool A_MN_, bool B_MN_>
-struct GradCfg {
-  static constexpr bool A_MN = A_MN_;
-  static constexpr bool B_MN = B_MN_;
-  static_assert(B_MN, "half-width column tiles load B in 64-row MN-major boxes");
-  static constexpr bool PAIR = kPairMMA;
-  static constexpr int BN = kTileN;
-  static constexpr int A_ROWS = BM;
-  static constexpr int STAGES = PAIR ? kPairStages : 4;
-  static constexpr int EXTRA_SMEM = kEpiSmemBytes;
-  static constexpr int UM = kUnitM;
-  using Params = GradGemmParams;
-
-  struct RowState {
-    int r;
-  };
-
-  static __device__ __forceinline__ uint64_t policy_a() { return l2_policy_evict_normal(); }
-  // grad_weight's B, the hidden states, is re-read by every unit
-  static __device__ __forceinline__ uint64_t policy_b() {
-    return (A_MN && LLP_GW_H_EVICT_LAST) ? l2_policy_evict_last() : l2_policy_evict_normal();
-  }
-  // units are claimed in ascending order from a ticket counter, so the tiles
-  // that share A rows or a K window of B run together
-  static constexpr bool DYNAMIC = (LLP_DYNAMIC_SCHED & (A_MN ? 2 : 1)) != 0;
-  static __device__ __forceinline__ int* sched_counter(const Params& p) { return p.sched; }
-  static __device__ __forceinline__ unsigned int* progress_counter(const Params& p) { return p.progress; }
-  static __device__ __forceinline__ bool a_chunked(const Params& p) { return p.a_chunked != 0; }
-  static __device__ __forceinline__ bool b_chunked(const Params& p) { return p.b_chunked != 0; }
-  static __device__ __forceinline__ int kps(const Params& p) { return p.kps; }
-  // grad_weight's B is the hidden states
-  static __device__ __forceinline__ void on_launch(const Params&) {}
-
-  static __device__ __forceinline__ int num_units(const Params& p) { return p.nseg * p.num_m * p.num_d; }
-
-  // Segment is the slowest index, then M tile, then the output column tile, so the
-  // CTAs that run together share A rows and the same K window of B.
-  static __device__ __forceinline__ UnitInfo unit(const Params& p, int u) {
-    const int per_seg = p.num_m * p.num_d;
-    const int seg = u / per_seg;
-    const int r = u - seg * per_seg;
-    const int mt = r / p.num_d;
-    const int dt = r - mt * p.num_d;
-    const int total_kb = (p.K + BK - 1) / BK;
-    UnitInfo ui;
-    ui.m0 = mt * UM;
-    ui.n0 = dt * BN;
-    ui.ntiles = 1;
-    ui.kb0 = seg * p.kseg_blocks;
-    ui.nkb = min(p.kseg_blocks, total_kb - ui.kb0);
-    ui.bn = (LLP_HALF_TILE && p.D - ui.n0 <= BN / 2) ? BN / 2 : BN;  // ragged last column tile: half-width MMA
-    return ui;
-  }
-
-  static __device__ __forceinline__ void unit_begin(const Params&, const UnitInfo& ui, int, int row, RowState& rs) {
-    rs.r = ui.m0 + row;
-  }
-
-  // Output through 32-row slabs and TMA stores: bf16 [rows][D] with one
-  // segment, else the fp32 partial of this segment in [nseg][rows][D] (a 3-D
-  // tensor map, so rows past `rows` are clipped inside the segment).
-  static __device__ __forceinline__ void tile(const Params& p, const UnitInfo& ui, int u, int, int row, int lane,
-                                              uint32_t taddr, RowState&, EpiStore& es) {
-    const int seg = u / (p.num_m * p.num_d);
-    const int row0 = ui.m0 + row - lane;
-    if (row0 >= p.rows) return;  // this warp's rows are all past the end (warp-uniform)
-    if (p.nseg == 1 && !p.f32_out) {
-      const bool f16 = p.f16 != 0;
-#pragma unroll 1
-      for (int q = 0; q < BN / 64; ++q) {
-        const int d0 = ui.n0 + 64 * q;
-        if (d0 >= p.D) break;  // warp-uniform
-        const uint32_t sbuf = epi_slab_begin(es);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float a[32];
-          tmem_load_32cols(taddr + 64 * q + 32 * h, a);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            epi_slab_put(sbuf, lane, 4 * h + k, pack16x2(f16, a[8 * k + 0], a[8 * k + 1]),
-                         pack16x2(f16, a[8 * k + 2], a[8 * k + 3]), pack16x2(f16, a[8 * k + 4], a[8 * k + 5]),
-                         pack16x2(f16, a[8 * k + 6], a[8 * k + 7]));
-        }
-        epi_slab_store_2d(es, sbuf, d0, row0);
-      }
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        const int d0 = ui.n0 + 32 * c;
-        if (d0 >= p.D) break;  // warp-uniform
-        const uint32_t sbuf = epi_slab_begin(es);
-        float a[32];
-        tmem_load_32cols(taddr + 32 * c, a);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          epi_slab_put(sbuf, lane, k, __float_as_uint(a[4 * k + 0]), __float_as_uint(a[4 * k + 1]),
-                       __float_as_uint(a[4 * k + 2]), __float_as_uint(a[4 * k + 3]));
-        epi_slab_store_3d(es, sbuf, d0, row0, seg);
-      }
-    }
-  }
-
-  static __device__ __forceinline__ void unit_end(const Params&, const UnitInfo&, int, int, RowState&) {}
-};
-
 // out[i] = bf16 (fp16 when f16) of sum_{s ascending} part[s][i], 4 elements per thread step.
 __global__ void __launch_bounds__(256) segment_sum_kernel(const float* __restrict__ part, int nseg, long long count,
                                                           __nv_bfloat16* __restrict__ out, int f16) {
@@ -368,13 +245,6 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__
   out[v] = acc;
 }
 
-template <class Cfg>
-static cudaError_t launch_units(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                                const typename Cfg::Params& p, long long units, int groups, cudaStream_t s) {
-  const long long g = units < groups ? units : groups;
-  return launch_gemm<Cfg>(a, b, c, p, static_cast<int>(g) * Plan<Cfg>::NCTA, s);
-}
-
 cudaError_t bwd_setup(LaunchCaps* caps) {
   cudaError_t e;
   if ((e = setup_gemm<DzCfg<false>>(&caps->dz_groups[0])) != cudaSuccess) return e;
@@ -390,24 +260,24 @@ cudaError_t bwd_setup(LaunchCaps* caps) {
 cudaError_t launch_dlogits(const CUtensorMap& tm_h, const CUtensorMap& tm_w, const CUtensorMap& tm_dz_out,
                            const DzParams& p, long long units, const LaunchCaps& caps, cudaStream_t s, bool single) {
   if (single && hidden_box_rows(p.N, true) == kSmallARows)
-    return p.bias ? launch_units<DzCfg<true, false, kSmallARows>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_small[1], s)
-                  : launch_units<DzCfg<false, false, kSmallARows>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_small[0],
+    return p.bias ? launch_units<DzCfg<true, false, kSmallARows>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_small[1], s)
+                  : launch_units<DzCfg<false, false, kSmallARows>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_small[0],
                                                                    s);
   if (single)
-    return p.bias ? launch_units<DzCfg<true, false>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_single[1], s)
-                  : launch_units<DzCfg<false, false>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_single[0], s);
-  return p.bias ? launch_units<DzCfg<true>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_groups[1], s)
-                : launch_units<DzCfg<false>>(tm_h, tm_w, tm_dz_out, p, units, caps.dz_groups[0], s);
+    return p.bias ? launch_units<DzCfg<true, false>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_single[1], s)
+                  : launch_units<DzCfg<false, false>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_single[0], s);
+  return p.bias ? launch_units<DzCfg<true>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_groups[1], s)
+                : launch_units<DzCfg<false>>({tm_h, tm_w, tm_dz_out}, p, units, caps.dz_groups[0], s);
 }
 
 cudaError_t launch_grad_hidden(const CUtensorMap& tm_dz, const CUtensorMap& tm_w_mn, const CUtensorMap& tm_out,
                                const GradGemmParams& p, long long units, const LaunchCaps& caps, cudaStream_t s) {
-  return launch_units<GradCfg<false, true>>(tm_dz, tm_w_mn, tm_out, p, units, caps.gh_groups, s);
+  return launch_units<GradCfg<false, true>>({tm_dz, tm_w_mn, tm_out}, p, units, caps.gh_groups, s);
 }
 
 cudaError_t launch_grad_weight(const CUtensorMap& tm_dz_mn, const CUtensorMap& tm_h_mn, const CUtensorMap& tm_out,
                                const GradGemmParams& p, long long units, const LaunchCaps& caps, cudaStream_t s) {
-  return launch_units<GradCfg<true, true>>(tm_dz_mn, tm_h_mn, tm_out, p, units, caps.gw_groups, s);
+  return launch_units<GradCfg<true, true>>({tm_dz_mn, tm_h_mn, tm_out}, p, units, caps.gw_groups, s);
 }
 
 // Grid-stride kernels: enough blocks to fill the device (16 per SM), never more than the work.

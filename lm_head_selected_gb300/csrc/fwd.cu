@@ -32,7 +32,7 @@ __device__ __forceinline__ bool target_valid(long long t, int V, long long ignor
 // in one of them (a pair's second CTA would hold only padding rows).  AROWS:
 // hidden rows loaded per stage (kSmallARows for a batch that small).
 template <bool HAS_BIAS, bool PAIRED = kPairMMA, int AROWS = kTileM>
-struct FwdCfg {
+struct FwdCfg : PlainOperands {
   static constexpr bool A_MN = false;
   static constexpr bool B_MN = false;
   static constexpr bool PAIR = PAIRED;
@@ -342,7 +342,7 @@ template <class Cfg>
 static cudaError_t launch_units(const CUtensorMap& a, const CUtensorMap& b, const typename Cfg::Params& p,
                                 long long units, int groups, cudaStream_t s) {
   const long long g = units < groups ? units : groups;
-  return launch_gemm<Cfg>(a, b, a, p, static_cast<int>(g) * Plan<Cfg>::NCTA, s);  // no tensor stores
+  return launch_gemm<Cfg>({a, b, a}, p, static_cast<int>(g) * Plan<Cfg>::NCTA, s);  // no tensor stores
 }
 
 cudaError_t launch_fwd_partials(const CUtensorMap& tm_h, const CUtensorMap& tm_w, const FwdParams& p,

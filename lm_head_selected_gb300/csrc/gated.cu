@@ -1,0 +1,281 @@
+// Gated linear layer y = act(x Wg^T) * (x Wu^T) and its gradient, on the tcgen05 core.
+//
+// Forward: one GEMM over both projections.  A CTA pair's 256 x 256 tile has 128 columns of each:
+// of the tile's B rows the even CTA loads its half from Wg and the odd CTA its half from Wu, so
+// that the accumulator's columns 0..127 are the gate and 128..255 the up projection of the same
+// 128 columns of y, and every thread of the epilogue holds both factors of its row.  The
+// projections never leave the SM unless they are kept for the gradient; y is formed from the
+// fp32 accumulators.
+//
+// Backward, from the kept projections:
+//   dG = grad_y * up * act'(gate),  dU = grad_y * act(gate)       one elementwise pass
+//   grad_x   = dG . Wg + dU . Wu        one GEMM over K = 2 F: the K blocks of the first half
+//                                       take B from Wg, those of the second from Wu
+//   grad_Wg  = dG^T . x,  grad_Wu = dU^T . x      one launch over the tiles of both
+// dG and dU are rounded to the tensors' 16-bit type, as the tensor cores take them; they lie in
+// one workspace [N][2][F_pad], F_pad a multiple of 128 with zeros in the padding, so that a
+// double k-block never straddles the halves.
+#include "gated.h"
+
+#include "grad_gemm.cuh"
+
+#include "elem.cuh"
+#include "gated.cuh"
+
+namespace llp {
+
+namespace {
+
+constexpr int kGatedCols = kTileN / 2;  // columns of y in a tile
+
+struct GatedMaps {
+  CUtensorMap a, b, c;  // x, Wg, y
+  CUtensorMap b2, c2;   // Wu, the kept projections [2][N][F]
+};
+
+struct GatedFwdCfg : PlainOperands {
+  using Maps = GatedMaps;
+  using Params = GatedFwdParams;
+  static constexpr bool A_MN = false;
+  static constexpr bool B_MN = false;
+  static constexpr bool PAIR = true;
+  static constexpr int BN = kTileN;
+  static constexpr int A_ROWS = kTileM;
+  static constexpr int STAGES = kPairStages;
+  static constexpr int EXTRA_SMEM = kEpiSmemBytes;
+
+  struct RowState {};
+
+  static __device__ __forceinline__ const CUtensorMap* b_map(const Maps& m, const Params&, uint32_t rank, int) {
+    return rank == 0 ? &m.b : &m.b2;
+  }
+  static __device__ __forceinline__ int b_row(int n0, int, int, int, int) { return n0; }
+  static __device__ __forceinline__ const CUtensorMap* c_map2(const Maps& m) { return &m.c2; }
+  static __device__ __forceinline__ uint64_t policy_a() { return l2_policy_evict_last(); }
+  static __device__ __forceinline__ uint64_t policy_b() { return l2_policy_evict_normal(); }
+  static constexpr bool DYNAMIC = false;
+  static __device__ __forceinline__ int* sched_counter(const Params&) { return nullptr; }
+  static __device__ __forceinline__ unsigned int* progress_counter(const Params&) { return nullptr; }
+  static __device__ __forceinline__ bool a_chunked(const Params&) { return false; }
+  static __device__ __forceinline__ bool b_chunked(const Params&) { return false; }
+  static __device__ __forceinline__ int kps(const Params& p) { return p.kps; }
+  static __device__ __forceinline__ void on_launch(const Params&) {}
+
+  static __device__ __forceinline__ int num_units(const Params& p) { return p.num_m * p.num_ft; }
+
+  // groups of group_m row tiles; inside a group the column tile is the slow index, so that the
+  // pairs that run together share weight tiles in L2
+  static __device__ __forceinline__ UnitInfo unit(const Params& p, int u) {
+    const int gsize = p.group_m * p.num_ft;
+    const int grp = u / gsize;
+    const int r = u - grp * gsize;
+    const int gm = min(p.group_m, p.num_m - grp * p.group_m);
+    const int ft = r / gm;
+    UnitInfo ui;
+    ui.m0 = (grp * p.group_m + (r - ft * gm)) * kUnitM;
+    ui.n0 = ft * kGatedCols;
+    ui.ntiles = 1;
+    ui.kb0 = 0;
+    ui.nkb = (p.D + BK - 1) / BK;
+    ui.bn = BN;
+    return ui;
+  }
+
+  static __device__ __forceinline__ void unit_begin(const Params&, const UnitInfo&, int, int, RowState&) {}
+  static __device__ __forceinline__ void unit_end(const Params&, const UnitInfo&, int, int, RowState&) {}
+
+  static __device__ __forceinline__ void put32(uint32_t sbuf, int lane, int h, bool f16, const float (&z)[32]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      epi_slab_put(sbuf, lane, 4 * h + k, pack16x2(f16, z[8 * k + 0], z[8 * k + 1]),
+                   pack16x2(f16, z[8 * k + 2], z[8 * k + 3]), pack16x2(f16, z[8 * k + 4], z[8 * k + 5]),
+                   pack16x2(f16, z[8 * k + 6], z[8 * k + 7]));
+  }
+
+  template <int ACT>
+  static __device__ __forceinline__ void product(float (&g)[32], const float (&u)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] = gated_act<ACT>(g[i]) * u[i];
+  }
+
+  static __device__ __forceinline__ void tile(const Params& p, const UnitInfo& ui, int, int, int row, int lane,
+                                              uint32_t taddr, RowState&, EpiStore& es) {
+    const int row0 = ui.m0 + row - lane;
+    if (row0 >= p.N) return;  // this warp's rows are all past the end (warp-uniform)
+    const bool f16 = p.f16 != 0;
+#pragma unroll 1
+    for (int q = 0; q < kGatedCols / 64; ++q) {  // 64-column slabs; rows and columns past the end are clipped
+      const int f0 = ui.n0 + 64 * q;
+      if (f0 >= p.F) break;  // warp-uniform
+      if (p.keep) {
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t sbuf = epi_slab_begin(es);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_load_32cols(taddr + kGatedCols * z + 64 * q + 32 * h, v);
+            put32(sbuf, lane, h, f16, v);
+          }
+          epi_slab_store_3d_to(es, es.map2, sbuf, f0, row0, z);
+        }
+      }
+      const uint32_t sbuf = epi_slab_begin(es);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float g[32], u[32];
+        tmem_load_32cols(taddr + 64 * q + 32 * h, g);
+        tmem_load_32cols(taddr + kGatedCols + 64 * q + 32 * h, u);
+        if (p.act == kActSilu)
+          product<kActSilu>(g, u);
+        else if (p.act == kActGelu)
+          product<kActGelu>(g, u);
+        else
+          product<kActGeluTanh>(g, u);
+        put32(sbuf, lane, h, f16, g);
+      }
+      epi_slab_store_2d(es, sbuf, f0, row0);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- backward
+
+// grad_x: the K blocks of the second half come from Wu.
+struct GatedGradXCfg : GradCfg<false, true> {
+  struct Maps {
+    CUtensorMap a, b, c;  // dG and dU side by side, Wg, grad_x
+    CUtensorMap b2;       // Wu
+  };
+  using Params = GatedGradXParams;
+  static __device__ __forceinline__ const CUtensorMap* b_map(const Maps& m, const Params& p, uint32_t, int kb) {
+    return kb < p.half_blocks ? &m.b : &m.b2;
+  }
+  static __device__ __forceinline__ int b_kx(const Params& p, int kb) {
+    return (kb < p.half_blocks ? kb : kb - p.half_blocks) * BK;
+  }
+};
+
+// grad_Wg and grad_Wu: row tiles [0, tiles) are of Wg, [tiles, 2 tiles) of Wu.
+struct GatedGradWCfg : GradCfg<true, true> {
+  using Base = GradCfg<true, true>;
+  struct Maps {
+    CUtensorMap a, b, c;  // dG and dU side by side, x, grad_Wg
+    CUtensorMap c2;       // grad_Wu
+  };
+  using Params = GatedGradWParams;
+  static __device__ __forceinline__ const CUtensorMap* c_map2(const Maps& m) { return &m.c2; }
+  static __device__ __forceinline__ UnitInfo unit(const Params& p, int u) {
+    UnitInfo ui = Base::unit(p, u);
+    const int mt = ui.m0 / kUnitM + p.first_tile;
+    ui.m0 = mt < p.tiles ? mt * kUnitM : p.F_pad + (mt - p.tiles) * kUnitM;
+    return ui;
+  }
+  static __device__ __forceinline__ void tile(const Params& p, const UnitInfo& ui, int u, int j, int row, int lane,
+                                              uint32_t taddr, RowState& rs, EpiStore& es) {
+    const CUtensorMap* const gate = es.map;
+    UnitInfo v = ui;
+    // a tile of the first half may end past F_pad but starts before it
+    if (v.m0 >= p.F_pad) {
+      v.m0 -= p.F_pad;
+      es.map = es.map2;
+    }
+    Base::tile(p, v, u, j, row, lane, taddr, rs, es);
+    es.map = gate;
+  }
+};
+
+// dG and dU of 8 columns of a row per step.  Bound by memory: three tensors read, two written.
+constexpr int kDpreThreads = 256;
+template <int DT, int ACT>
+__global__ void __launch_bounds__(kDpreThreads) gated_dpre_kernel(const uint4* __restrict__ gy,
+                                                                  const uint4* __restrict__ gate,
+                                                                  const uint4* __restrict__ up, int N, int F, int F_pad,
+                                                                  uint4* __restrict__ dpre, int* sched) {
+  constexpr int W = 8;
+  if (blockIdx.x == 0 && threadIdx.x < kNumSchedCounters) sched[threadIdx.x] = 0;  // of the GEMMs that follow
+  const int vecs = F / W, pitch = F_pad / W;  // of a row, and with its padding
+  const long long step = static_cast<long long>(gridDim.x) * kDpreThreads;
+  const long long at = static_cast<long long>(blockIdx.x) * kDpreThreads + threadIdx.x;
+  long long n = at / pitch;
+  int c = static_cast<int>(at - n * pitch);
+  const long long n_step = step / pitch;
+  const int c_step = static_cast<int>(step - n_step * pitch);
+  while (n < N) {
+    uint4* const out = dpre + n * 2 * pitch + c;
+    if (c < vecs) {
+      const long long i = n * vecs + c;
+      float y[W], g[W], u[W];
+      Elem<DT>::unpack(__ldg(gy + i), y);
+      Elem<DT>::unpack(__ldg(gate + i), g);
+      Elem<DT>::unpack(__ldg(up + i), u);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        float a, slope;
+        gated_act_slope<ACT>(g[k], a, slope);
+        g[k] = y[k] * u[k] * slope;
+        u[k] = y[k] * a;
+      }
+      out[0] = Elem<DT>::pack(g);
+      out[pitch] = Elem<DT>::pack(u);
+    } else {
+      out[0] = out[pitch] = make_uint4(0, 0, 0, 0);
+    }
+    n += n_step;
+    c += c_step;
+    if (c >= pitch) {
+      c -= pitch;
+      ++n;
+    }
+  }
+}
+
+template <int DT>
+cudaError_t dpre(const GatedBwdParams& p, int blocks, cudaStream_t s) {
+  const uint4* const gy = static_cast<const uint4*>(p.gy);
+  const uint4* const gate = static_cast<const uint4*>(p.pre);
+  const uint4* const up = gate + static_cast<size_t>(p.N) * p.F / 8;
+  const auto kernel = p.act == kActSilu   ? gated_dpre_kernel<DT, kActSilu>
+                      : p.act == kActGelu ? gated_dpre_kernel<DT, kActGelu>
+                                          : gated_dpre_kernel<DT, kActGeluTanh>;
+  kernel<<<blocks, kDpreThreads, 0, s>>>(gy, gate, up, p.N, p.F, p.F_pad, static_cast<uint4*>(p.dpre), p.sched);
+  return launch_result();
+}
+
+}  // namespace
+
+cudaError_t gated_setup(GatedCaps* caps) {
+  cudaError_t e = note_cuda(setup_gemm<GatedFwdCfg>(&caps->fwd_groups));
+  if (e == cudaSuccess) e = note_cuda(setup_gemm<GatedGradXCfg>(&caps->gx_groups));
+  if (e == cudaSuccess) e = note_cuda(setup_gemm<GatedGradWCfg>(&caps->gw_groups));
+  return e;
+}
+
+cudaError_t launch_gated_fwd(const CUtensorMap& x, const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& y,
+                             const CUtensorMap& pre, const GatedFwdParams& p, const GatedCaps& caps, cudaStream_t s) {
+  return launch_units<GatedFwdCfg>({x, wg, y, wu, pre}, p, static_cast<long long>(p.num_m) * p.num_ft, caps.fwd_groups,
+                                   s);
+}
+
+cudaError_t launch_gated_dpre(const GatedBwdParams& p, int num_sms, cudaStream_t s) {
+  const long long vecs = static_cast<long long>(p.N) * (p.F_pad / 8);
+  const long long want = (vecs + kDpreThreads - 1) / kDpreThreads, most = 8LL * num_sms;
+  const int blocks = static_cast<int>(want < most ? want : most);
+  return p.dtype == kDtypeF16 ? dpre<kDtypeF16>(p, blocks, s) : dpre<kDtypeBF16>(p, blocks, s);
+}
+
+cudaError_t launch_gated_grad_x(const CUtensorMap& dpre, const CUtensorMap& wg, const CUtensorMap& wu,
+                                const CUtensorMap& gx, const GatedGradXParams& p, const GatedCaps& caps,
+                                cudaStream_t s) {
+  return launch_units<GatedGradXCfg>({dpre, wg, gx, wu}, p, static_cast<long long>(p.num_m) * p.num_d, caps.gx_groups,
+                                     s);
+}
+
+cudaError_t launch_gated_grad_w(const CUtensorMap& dpre, const CUtensorMap& x, const CUtensorMap& gwg,
+                                const CUtensorMap& gwu, const GatedGradWParams& p, const GatedCaps& caps,
+                                cudaStream_t s) {
+  return launch_units<GatedGradWCfg>({dpre, x, gwg, gwu}, p, static_cast<long long>(p.num_m) * p.num_d, caps.gw_groups,
+                                     s);
+}
+
+}  // namespace llp

@@ -1,5 +1,5 @@
 // Warp-specialised, persistent tcgen05 GEMM core shared by every contraction
-// of the fused linear log-prob path.
+// of the fused linear log-prob path and of the gated linear layer.
 //
 //   warp 0      : TMA producer (one lane) streaming A/B k-blocks into a ring of
 //                 shared-memory stages, completion on mbarriers.
@@ -71,6 +71,32 @@ struct UnitInfo {
   int bn;      // MMA N of the unit's tiles: Cfg::BN, or Cfg::BN / 2 for a ragged last column tile
 };
 
+// The tensor maps of a launch and where a configuration's operands come from.  Most have one map
+// for each operand and the output; one whose B lies in two tensors hides these with its own.
+struct GemmMaps {
+  CUtensorMap a, b, c;
+};
+struct PlainOperands {
+  using Maps = GemmMaps;
+  // the map that B's k-block kb comes from in the pair's CTA `rank`, and its first K element there
+  template <class M, class P>
+  static __device__ __forceinline__ const CUtensorMap* b_map(const M& m, const P&, uint32_t, int) {
+    return &m.b;
+  }
+  template <class P>
+  static __device__ __forceinline__ int b_kx(const P&, int kb) {
+    return kb * kTileK;
+  }
+  // first B row that the pair's CTA `rank` loads for the unit's tile j
+  static __device__ __forceinline__ int b_row(int n0, int j, int bn, int rank, int rows) {
+    return n0 + j * bn + rank * rows;
+  }
+  template <class M>
+  static __device__ __forceinline__ const CUtensorMap* c_map2(const M&) {
+    return nullptr;
+  }
+};
+
 constexpr int kSchedDepth = 4;  // unit-id slots between the ticket drawer and the other roles
 constexpr int kLockChunk = 16;                     // k-blocks between progress reports (advisory lockstep)
 constexpr unsigned long long kLockMaxWaitNs = 20000;  // longest nap per report
@@ -131,6 +157,7 @@ constexpr int kEpiSmemBytes = 4 * 2 * kEpiStageBytes;  // 4 epilogue warps x 2 b
 
 struct EpiStore {
   const CUtensorMap* map;
+  const CUtensorMap* map2;  // of a second output
   uint32_t buf0;  // this warp's first staging buffer (shared address, 1024-aligned)
   uint32_t next;  // buffer the next slab goes to
   int lane;
@@ -175,14 +202,18 @@ __device__ __forceinline__ void epi_slab_store_2d_hint(EpiStore& es, uint32_t bu
   es.next ^= 1u;
 }
 
-__device__ __forceinline__ void epi_slab_store_3d(EpiStore& es, uint32_t buf, int x, int y, int z) {
+__device__ __forceinline__ void epi_slab_store_3d_to(EpiStore& es, const CUtensorMap* map, uint32_t buf, int x, int y,
+                                                     int z) {
   fence_proxy_async_smem();
   __syncwarp();
   if (es.lane == 0) {
-    tma_store_3d(es.map, buf, x, y, z);
+    tma_store_3d(map, buf, x, y, z);
     bulk_commit_group();
   }
   es.next ^= 1u;
+}
+__device__ __forceinline__ void epi_slab_store_3d(EpiStore& es, uint32_t buf, int x, int y, int z) {
+  epi_slab_store_3d_to(es, es.map, buf, x, y, z);
 }
 
 // ----------------------------------------------------------------------------
@@ -238,9 +269,10 @@ __device__ __forceinline__ int static_unit(const SharedState& st, const typename
 // k-blocks each (one copy per operand per stage; same bytes in flight).  A
 // template parameter, so that each form compiles to straight-line code.
 template <class Cfg, int kps>
-__device__ __forceinline__ void run_producer_k(const SharedState& st, const CUtensorMap* tmA, const CUtensorMap* tmB,
+__device__ __forceinline__ void run_producer_k(const SharedState& st, const typename Cfg::Maps& maps,
                                                const typename Cfg::Params& p) {
   using P = Plan<Cfg>;
+  const CUtensorMap* const tmA = &maps.a;
   const uint64_t polA = Cfg::policy_a();
   const uint64_t polB = Cfg::policy_b();
   const bool leader = st.rank == 0;
@@ -277,7 +309,7 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const CUte
     // hides behind the loads still to issue
     const int draw_at = ui.nkb > 4 ? ui.nkb - 4 : 0;
     for (int j = 0; j < ui.ntiles; ++j) {
-      const int b_row = ui.n0 + j * Cfg::BN + static_cast<int>(st.rank) * b_rows;
+      const int b_row = Cfg::b_row(ui.n0, j, Cfg::BN, static_cast<int>(st.rank), b_rows);
       for (int kb = 0; kb < ui.nkb; kb += kps) {
         if (dyn && leader && j == ui.ntiles - 1 && kb <= draw_at && draw_at < kb + kps)
           ticket = atomicAdd(Cfg::sched_counter(p), 1);
@@ -300,6 +332,8 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const CUte
         const uint32_t sA = smem_u32(st.tiles + stage * stage_bytes);
         const uint32_t sB = sA + P::A_BYTES * kps;
         const int kx = (ui.kb0 + kb) * BK;
+        const CUtensorMap* const tmB = Cfg::b_map(maps, p, st.rank, ui.kb0 + kb);
+        const int bx = Cfg::b_kx(p, ui.kb0 + kb);
         // K-major with kps == 2: the 3-D map's third dimension steps over 64-wide
         // K chunks; MN-major chunked: over 64-wide MN chunks, K rows in the box
         if (P::PAIR) {
@@ -318,13 +352,13 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const CUte
           }
           if (!Cfg::B_MN) {
             if (kps == 2)
-              tma_load_3d_pair(sB, tmB, bar, 0, b_row, kx / 64, polB);
+              tma_load_3d_pair(sB, tmB, bar, 0, b_row, bx / 64, polB);
             else
-              tma_load_2d_pair(sB, tmB, bar, kx, b_row, polB);
+              tma_load_2d_pair(sB, tmB, bar, bx, b_row, polB);
           } else if (Cfg::b_chunked(p)) {
-            tma_load_3d_pair(sB, tmB, bar, 0, kx, b_row / 64, polB);
+            tma_load_3d_pair(sB, tmB, bar, 0, bx, b_row / 64, polB);
           } else {
-            for (int i = 0; i < b_rows / 64; ++i) tma_load_2d_pair(sB + i * 8192, tmB, bar, b_row + 64 * i, kx, polB);
+            for (int i = 0; i < b_rows / 64; ++i) tma_load_2d_pair(sB + i * 8192, tmB, bar, b_row + 64 * i, bx, polB);
           }
         } else {
           mbar_arrive_expect_tx(&st.full[stage], tx);
@@ -342,14 +376,14 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const CUte
           }
           if (!Cfg::B_MN) {
             if (kps == 2)
-              tma_load_3d(sB, tmB, &st.full[stage], 0, b_row, kx / 64, polB);
+              tma_load_3d(sB, tmB, &st.full[stage], 0, b_row, bx / 64, polB);
             else
-              tma_load_2d(sB, tmB, &st.full[stage], kx, b_row, polB);
+              tma_load_2d(sB, tmB, &st.full[stage], bx, b_row, polB);
           } else if (Cfg::b_chunked(p)) {
-            tma_load_3d(sB, tmB, &st.full[stage], 0, kx, b_row / 64, polB);
+            tma_load_3d(sB, tmB, &st.full[stage], 0, bx, b_row / 64, polB);
           } else {
             for (int i = 0; i < b_rows / 64; ++i)
-              tma_load_2d(sB + i * 8192, tmB, &st.full[stage], b_row + 64 * i, kx, polB);
+              tma_load_2d(sB + i * 8192, tmB, &st.full[stage], b_row + 64 * i, bx, polB);
           }
         }
         if (++stage == nstages) {
@@ -362,12 +396,12 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const CUte
 }
 
 template <class Cfg>
-__device__ __forceinline__ void run_producer(const SharedState& st, const CUtensorMap* tmA, const CUtensorMap* tmB,
+__device__ __forceinline__ void run_producer(const SharedState& st, const typename Cfg::Maps& maps,
                                              const typename Cfg::Params& p) {
   if (Cfg::kps(p) == 2)  // STAGES / 2 double stages (an odd last buffer goes unused)
-    run_producer_k<Cfg, 2>(st, tmA, tmB, p);
+    run_producer_k<Cfg, 2>(st, maps, p);
   else
-    run_producer_k<Cfg, 1>(st, tmA, tmB, p);
+    run_producer_k<Cfg, 1>(st, maps, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -472,7 +506,7 @@ __device__ __forceinline__ void run_mma(const SharedState& st, const typename Cf
 // Epilogue: warps 2..5 of every CTA.
 // ----------------------------------------------------------------------------
 template <class Cfg>
-__device__ __forceinline__ void run_epilogue(const SharedState& st, const CUtensorMap* tmC,
+__device__ __forceinline__ void run_epilogue(const SharedState& st, const typename Cfg::Maps& maps,
                                              const typename Cfg::Params& p) {
   using P = Plan<Cfg>;
   const int warp = threadIdx.x >> 5;
@@ -480,7 +514,8 @@ __device__ __forceinline__ void run_epilogue(const SharedState& st, const CUtens
   const int g = warp & 3;                                          // TMEM lane group of this warp
   const int row = static_cast<int>(st.rank) * BM + g * 32 + lane;  // accumulator row within the unit
   EpiStore es;
-  es.map = tmC;
+  es.map = &maps.c;
+  es.map2 = Cfg::c_map2(maps);
   es.buf0 = smem_u32(st.extra) + static_cast<uint32_t>(g) * 2u * kEpiStageBytes;
   es.next = 0;
   es.lane = lane;
@@ -527,8 +562,7 @@ __device__ __forceinline__ void run_epilogue(const SharedState& st, const CUtens
 
 template <class Cfg>
 __global__ void __launch_bounds__(kNumThreads, 1)
-    tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const typename Cfg::Params p) {
+    tc_gemm_kernel(const __grid_constant__ typename Cfg::Maps maps, const typename Cfg::Params p) {
   using P = Plan<Cfg>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -573,9 +607,9 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     if (blockIdx.x == 0) Cfg::on_launch(p);
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    if (Cfg::EXTRA_SMEM > 0) tma_prefetch_desc(&tmC);
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+    if (Cfg::EXTRA_SMEM > 0) tma_prefetch_desc(&maps.c);
   }
   __syncwarp();  // the .aligned barriers and tcgen05 allocation below need converged warps
   if (warp == 1) {
@@ -598,7 +632,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
   st.tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) run_producer<Cfg>(st, &tmA, &tmB, p);
+    if (lane == 0) run_producer<Cfg>(st, maps, p);
   } else if (warp == 1) {
     if (lane == 0 && st.rank == 0) {
       run_mma<Cfg>(st, p);
@@ -611,7 +645,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       if (!mbar_wait_drain(st.drain, 0, 100000000ull)) atomicCAS(st.err, 0u, kDevTimeoutDrain);
     }
   } else {
-    run_epilogue<Cfg>(st, &tmC, p);
+    run_epilogue<Cfg>(st, maps, p);
   }
 
   tc_fence_before_sync();
@@ -633,8 +667,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
 
 // Launch helper: pair configurations run as 2-CTA clusters.
 template <class Cfg>
-inline cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                               const typename Cfg::Params& p, int grid, cudaStream_t s) {
+inline cudaError_t launch_gemm(const typename Cfg::Maps& maps, const typename Cfg::Params& p, int grid, cudaStream_t s) {
   using P = Plan<Cfg>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -648,7 +681,7 @@ inline cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return note_cuda(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<Cfg>, a, b, c, p));
+  return note_cuda(cudaLaunchKernelEx(&cfg, tc_gemm_kernel<Cfg>, maps, p));
 }
 
 // One-time set-up per kernel: shared-memory opt-in and the number of clusters

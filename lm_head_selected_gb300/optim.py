@@ -1,0 +1,149 @@
+"""PyTorch-facing wrappers of the AdamW step (include/adamw.h).
+
+Argument marshalling only; the computation runs in ``liblinear_logp.so``: one launch for
+up to 320 tensors, with nothing copied to the device.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import List, Optional, Sequence, Tuple, Union
+
+import torch
+
+from . import _lib
+from .ops import _DTYPE_CODES, _need_cuda, _raw_stream
+
+BLOCK = 256  # elements of a tensor that share a scale of the 8-bit states
+CODE = torch.float8_e4m3fn
+
+Tensors = Sequence[torch.Tensor]
+
+
+def adamw_state(params: Tensors, bits: int = 32, masters: bool = False) -> dict:
+    """Zero states for ``adamw_step(params, grads, **state, ...)``: exp_avg and exp_avg_sq in fp32, or with
+    ``bits=8`` as e4m3 codes with their scales, exp_avg_scale and exp_avg_sq_scale; with ``masters``, an fp32
+    copy of every parameter that is not fp32 itself."""
+    if bits not in (32, 8):
+        raise ValueError(f"bits must be 32 or 8, got {bits}")
+    for i, p in enumerate(params):
+        _need_cuda(p, f"params[{i}]")
+
+    def zeros(dtype, size):
+        return [torch.zeros(size(p), dtype=dtype, device=p.device) for p in params]
+
+    whole, blocks = (lambda p: p.shape), (lambda p: -(-p.numel() // BLOCK))
+    state = {"exp_avg": zeros(torch.float32 if bits == 32 else CODE, whole),
+             "exp_avg_sq": zeros(torch.float32 if bits == 32 else CODE, whole)}
+    if bits == 8:
+        state["exp_avg_scale"] = zeros(torch.float32, blocks)
+        state["exp_avg_sq_scale"] = zeros(torch.float32, blocks)
+    if masters:
+        state["masters"] = [None if p.dtype == torch.float32 else p.detach().float().contiguous() for p in params]
+    return state
+
+
+def _scalar(t, name: str, dtype: torch.dtype, device: torch.device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != 1 or t.device != device:
+        raise ValueError(f"{name} must be one {dtype} value on the parameters' device")
+    return t.data_ptr()
+
+
+def _pointers(name: str, tensors, sizes: List[int], device, dtype, blocks: bool = False, optional: bool = False):
+    """The tensors' addresses, after their checks."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name} must have {len(sizes)} entries, got {len(tensors)}")
+    out = (ctypes.c_void_p * len(sizes))()
+    for i, t in enumerate(tensors):
+        if t is None and optional:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+            raise TypeError(f"{name}[{i}] must be a tensor of {dtype}")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous, on {device}")
+        if t.numel() != (-(-sizes[i] // BLOCK) if blocks else sizes[i]):
+            raise ValueError(f"{name}[{i}] has {t.numel()} elements, which does not go with params[{i}]")
+        out[i] = t.data_ptr()
+    return out
+
+
+def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Tensors, step: int, lr: float = 1e-3,
+               betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+               weight_decay: Union[float, Sequence[float]] = 0.01, masters: Optional[Sequence] = None,
+               exp_avg_scale: Optional[Tensors] = None, exp_avg_sq_scale: Optional[Tensors] = None,
+               device_step: Optional[torch.Tensor] = None, device_lr: Optional[torch.Tensor] = None,
+               grad_scale: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step, in place, over all tensors (bf16, fp16 or fp32, each its own; gradients of the same
+    dtype or fp32; contiguous, on one CUDA device; none listed twice).  ``step`` counts from 1.  States as
+    ``adamw_state`` makes them, in 8 bits where the scales are given.  ``weight_decay``: one value, or one
+    per tensor.  On the device, read when the kernel runs, so that a captured graph can advance them:
+    ``device_step`` (int64, added to step), ``device_lr`` and ``grad_scale`` (fp32, factors of lr and of the
+    gradients)."""
+    params, grads = list(params), list(grads)
+    count = len(params)
+    if len(grads) != count:
+        raise ValueError(f"grads must have {count} entries, got {len(grads)}")
+    if (exp_avg_scale is None) != (exp_avg_sq_scale is None):
+        raise ValueError("exp_avg_scale and exp_avg_sq_scale must be given together")
+    beta1, beta2 = float(betas[0]), float(betas[1])
+    if not (0.0 <= beta1 < 1.0 and 0.0 <= beta2 < 1.0):
+        raise ValueError(f"betas must lie in [0, 1), got {betas}")
+    lr, eps, step = float(lr), float(eps), int(step)
+    if not math.isfinite(lr) or not math.isfinite(eps) or eps < 0.0:
+        raise ValueError("lr and eps must be finite, eps not negative")
+    if step < (1 if device_step is None else 0):
+        raise ValueError("step counts from 1")
+    if count == 0:
+        return
+    _need_cuda(params[0], "params[0]")
+    device = params[0].device
+    p_ptr, g_ptr = (ctypes.c_void_p * count)(), (ctypes.c_void_p * count)()
+    p_code, g_code = (ctypes.c_int32 * count)(), (ctypes.c_int32 * count)()
+    sizes = []
+    for i, (p, g) in enumerate(zip(params, grads)):
+        if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
+            raise TypeError(f"params[{i}] and grads[{i}] must be tensors")
+        code, g_c = _DTYPE_CODES.get(p.dtype), _DTYPE_CODES.get(g.dtype)
+        if code is None or (g_c != code and g_c != 1):
+            raise TypeError(f"params[{i}] must be bf16, fp16 or fp32, grads[{i}] of the same dtype or fp32")
+        if p.device != device or g.device != device or not p.is_contiguous() or not g.is_contiguous():
+            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous, on {device}")
+        n = p.numel()
+        if g.shape != p.shape:
+            raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
+        p_ptr[i], g_ptr[i], p_code[i], g_code[i] = p.data_ptr(), g.data_ptr(), code, g_c
+        sizes.append(n)
+    starts = [a for a, n in zip(p_ptr, sizes) if n]
+    if len(set(starts)) != len(starts):
+        raise ValueError("a parameter is listed twice")
+    packed = exp_avg_scale is not None
+    dtype = CODE if packed else torch.float32
+    m = _pointers("exp_avg", exp_avg, sizes, device, dtype)
+    v = _pointers("exp_avg_sq", exp_avg_sq, sizes, device, dtype)
+    ms = _pointers("exp_avg_scale", exp_avg_scale, sizes, device, torch.float32, blocks=True) if packed else None
+    vs = _pointers("exp_avg_sq_scale", exp_avg_sq_scale, sizes, device, torch.float32, blocks=True) if packed else None
+    top = None if masters is None else _pointers("masters", masters, sizes, device, torch.float32, optional=True)
+    if isinstance(weight_decay, (int, float)):
+        weight_decay = [weight_decay] * count
+    if len(weight_decay) != count or not all(math.isfinite(w) for w in weight_decay):
+        raise ValueError(f"weight_decay must be finite, one value or {count}")
+    decay = (ctypes.c_double * count)(*weight_decay)
+    scalars = (_scalar(device_step, "device_step", torch.int64, device),
+               _scalar(device_lr, "device_lr", torch.float32, device),
+               _scalar(grad_scale, "grad_scale", torch.float32, device))
+
+    def call():
+        st = _lib.load().adamw_step(count, p_ptr, g_ptr, m, v, ms, vs, top, (ctypes.c_int64 * count)(*sizes), p_code,
+                                    g_code, decay, 8 if packed else 32, lr, beta1, beta2, eps, step, *scalars,
+                                    _raw_stream(device.index))
+        _lib.check("adamw_step", st)
+
+    if device.index == torch._C._cuda_getDevice():
+        call()
+    else:
+        with torch.cuda.device(device):
+            call()
+    # autograd learns that they have changed
+    torch.autograd.graph.increment_version(params)
