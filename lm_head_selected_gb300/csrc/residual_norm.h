@@ -40,6 +40,8 @@ struct ResidualNormGrads {
   void* workspace;
 };
 
+cudaError_t residual_norm_fwd_setup();
+cudaError_t residual_norm_bwd_setup();
 cudaError_t launch_residual_norm_fwd(const ResidualNormParams& p, const ResidualNormOut& o, cudaStream_t s);
 size_t residual_norm_bwd_workspace(long long N, long long D);
 cudaError_t launch_residual_norm_bwd(const ResidualNormParams& p, const ResidualNormGrads& o, cudaStream_t s);
