@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "gh_small.cu", "logits.cu", "indexed.cu",
            "embedding.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu", "dropout.cu",
-           "gated.cu", "residual_norm_fwd.cu", "residual_norm_bwd.cu", "adamw.cu"]
+           "gated.cu", "gated_small.cu", "residual_norm_fwd.cu", "residual_norm_bwd.cu", "adamw.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
                 "-I", INCLUDE, "-I", CSRC]

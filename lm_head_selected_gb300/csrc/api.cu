@@ -125,7 +125,7 @@ int init_device(DeviceInit** out) {
                llp::small_grad_hidden_setup() != cudaSuccess || llp::embedding_setup() != cudaSuccess ||
                llp::layer_norm_fwd_setup() != cudaSuccess || llp::layer_norm_bwd_setup() != cudaSuccess ||
                llp::gated_setup(&d.gated) != cudaSuccess || llp::residual_norm_fwd_setup() != cudaSuccess ||
-               llp::residual_norm_bwd_setup() != cudaSuccess ||
+               llp::residual_norm_bwd_setup() != cudaSuccess || llp::gated_small_setup() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status_ptr), g_status_word) != cudaSuccess) {
       d.status = fail_cuda(__LINE__);
     } else {
@@ -1447,8 +1447,31 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
   if ((st = init_device(&dev)) != LLP_OK) return st;
   if ((st = load_encode_fn()) != LLP_OK) return st;
   const bool f16 = dtype == llp::kDtypeF16;
-  const int kps = k_blocks_per_stage(D, false);
   CUtensorMap tm_x, tm_wg, tm_wu, tm_y, tm_pre;
+  llp::GatedSmallParams q = {};
+  if (N <= llp::kSmallGatedMaxN &&
+      llp::gated_small_plan(static_cast<int>(N), static_cast<int>(D), static_cast<int>(F), dev->num_sms, &q)) {
+    // few tokens: the weights' rows on the MMA's M side
+    q.chunked = (D % 64) == 0 ? 1 : 0;
+    const void* const base[3] = {w_gate, w_up, x};
+    CUtensorMap* const map[3] = {&tm_wg, &tm_wu, &tm_x};
+    for (int i = 0; i < 3; ++i) {
+      const int64_t rows = i == 2 ? N : F;
+      const uint32_t box = static_cast<uint32_t>(i == 2 ? q.BN : q.R);
+      const int r = q.chunked ? make_map_chunked(map[i], base[i], D, rows, D * 2, box, static_cast<uint32_t>(q.c), f16)
+                              : make_map(map[i], base[i], D, rows, D * 2, 64, box, f16);
+      if (r != LLP_OK) return fail_cuda(__LINE__);
+    }
+    q.act = act;
+    q.f16 = f16 ? 1 : 0;
+    q.y = static_cast<uint16_t*>(y);
+    q.pre = static_cast<uint16_t*>(pre);
+    q.err = dev->status_ptr;
+    const cudaError_t e =
+        llp::launch_gated_small(tm_wg, tm_wu, tm_x, q, dev->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
+  }
+  const int kps = k_blocks_per_stage(D, false);
   if (make_kmajor_maps(&tm_x, &tm_wg, x, w_gate, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
       make_kmajor_maps(&tm_x, &tm_wu, x, w_up, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
       make_map(&tm_y, y, F, N, F * 2, 64, 32, f16) != LLP_OK)

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include "sm103_ptx.cuh"
+
 namespace llp {
 
 enum GatedAct { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kNumActs = 3 };

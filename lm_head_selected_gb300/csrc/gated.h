@@ -19,6 +19,30 @@ struct GatedFwdParams {
   unsigned int* err;
 };
 
+// The forward of few tokens, weights on the MMA's M side (gated_small.cu).
+constexpr int kSmallGatedMaxN = 128;
+constexpr int kGatedSmallSmem = 232448;
+
+struct GatedSmallParams {
+  int N, D, F;
+  int BN;      // MMA N: N rounded up to 16
+  int R;       // rows of each weight to a CTA (height of the weights' boxes)
+  int units;   // of R rows
+  int c;       // K blocks of a stage
+  int stages;
+  int tmem_cols;
+  int chunked;  // the maps are 3-D {64, rows, D / 64}: one copy per operand and stage (D % 64 == 0), else 2-D
+  int act, f16;
+  uint16_t* y;
+  uint16_t* pre;  // [2][N][F], or nullptr
+  unsigned int* err;
+};
+// Fills all up to tmem_cols; false when the batch is too large for the kernel.
+bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p);
+cudaError_t gated_small_setup();
+cudaError_t launch_gated_small(const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& x,
+                               const GatedSmallParams& p, int num_sms, cudaStream_t s);
+
 struct GatedBwdParams {
   const void* gy;
   const void* pre;   // [2][N][F]
