@@ -14,6 +14,8 @@ namespace llp {
 namespace {
 
 constexpr int kAdamThreads = 256;
+template <int BITS>
+constexpr int kAdamResident = BITS == 8 ? 3 : 4;  // CTAs to an SM: 80 or 64 registers per thread
 constexpr int W = 8;  // elements of a thread's step
 constexpr float kTop8 = 448.f;              // largest e4m3 value
 constexpr float kLeast8 = 0.001953125f;     // smallest above 0, 2^-9
@@ -87,7 +89,7 @@ __device__ __forceinline__ void update(const Step& s, float shrink, float g, flo
   g *= s.scale;
   m = fmaf(s.b1, m, s.c1 * g);
   v = fmaf(s.b2, v, s.c2 * g * g);
-  root = __fsqrt_rn(v);
+  root = sqrtf(v);
   p = fmaf(p, shrink, -s.rate_m * __fdividef(m, fmaf(root, s.root_v, s.eps)));
 }
 
@@ -133,7 +135,8 @@ __device__ __forceinline__ void plain_elements(const AdamTensor& t, const Step& 
 }
 
 template <int PD, int GD>
-__device__ __forceinline__ void plain_chunk(const AdamTensor& t, const Step& s, int chunk) {
+__device__ __forceinline__ void plain_chunk(const AdamTensor& t, const Step* shared, int chunk) {
+  const Step s = *shared;
   const float shrink = 1.f - s.rate * t.decay;
   const int head = t.head < 0 ? 0 : t.head;
   const long long at = head + static_cast<long long>(chunk) * kAdamChunk;
@@ -153,26 +156,13 @@ __device__ __forceinline__ void plain_chunk(const AdamTensor& t, const Step& s, 
   }
 }
 
-// Eight e4m3 codes as fp32: e4m3 widens to fp16 exactly.
-__device__ __forceinline__ void codes_to_float(uint2 c, float (&v)[W]) {
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))),
-                                                     __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+// Two e4m3 codes (the low or the high half of a word's four) as fp32: e4m3 widens to fp16 exactly.
+__device__ __forceinline__ F2 codes_to_f2(uint32_t word, int half) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(word >> (16 * half)), __NV_E4M3);
+  return __half22float2(__half2(h));
 }
-__device__ __forceinline__ uint2 float_to_codes(const float (&v)[W]) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    w[i / 2] |= c << (16 * (i & 1));
-  }
-  return make_uint2(w[0], w[1]);
+__device__ __forceinline__ uint32_t f2_to_codes(F2 v) {
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
 // The larger of two magnitudes; NaN if one is.
@@ -181,121 +171,270 @@ __device__ __forceinline__ float nan_max(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// Within two units in the last place; 0 and infinity are exact.
+__device__ __forceinline__ float root_approx(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
-// 8-bit states: a warp takes a block of kAdamBlock elements, eight per lane.
-template <int PD, int GD>
-__device__ __forceinline__ void block_elements(const AdamTensor& t, const Step& s, float shrink, long long block) {
-  using P = typename Elem<PD>::T;
-  using G = typename Elem<GD>::T;
+// A lane's eight elements of a block with 8-bit states, as they lie in memory.
+template <int PD, int GD, bool MASTER>
+struct Packed {
+  static constexpr int PV = MASTER || PD == kDtypeF32 ? 2 : 1, GV = GD == kDtypeF32 ? 2 : 1;
+  uint4 p[PV], g[GV];
+  uint2 m, v;
+  float ms, vs;
+};
+
+// The blocks to come are under way in a ring of shared memory, kAhead to a warp; every lane copies what it
+// will read itself.
+constexpr int kAhead = 3;
+constexpr int kSlotWords = 4;  // 16-byte words of a lane's slot at most: two of the parameter, two of the gradient
+struct WarpRing {
+  uint4 wide[kAhead][kSlotWords][32];
+  uint2 m[kAhead][32];
+  uint2 v[kAhead][32];
+};
+
+__device__ __forceinline__ void copy_async8(void* slot, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(p)
+               : "memory");
+}
+
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void copy_packed(const AdamTensor& t, long long block, WarpRing* ring, int slot) {
+  using R = Packed<PD, GD, MASTER>;
   const int lane = threadIdx.x & 31;
   const long long at = block * kAdamBlock + lane * W;
-  const int n = static_cast<int>(t.n - at < W ? (t.n - at > 0 ? t.n - at : 0) : W);
-  P* const p = static_cast<P*>(t.p) + at;
-  const G* const g = static_cast<const G*>(t.g) + at;
-  unsigned char* const mc = static_cast<unsigned char*>(t.m) + at;
-  unsigned char* const vc = static_cast<unsigned char*>(t.v) + at;
-  const bool wide = t.head == 0 && n == W;
-  float pv[W], gv[W], mv[W], vv[W], root[W];
-  uint2 m8 = make_uint2(0, 0), v8 = make_uint2(0, 0);
-  if (wide) {
-    load_wide<GD, W>(g, gv);
-    m8 = *reinterpret_cast<const uint2*>(mc);
-    v8 = *reinterpret_cast<const uint2*>(vc);
-    if (t.master != nullptr)
-      load_wide<kDtypeF32, W>(t.master + at, pv);
-    else
-      load_wide<PD, W>(p, pv);
-  } else {
-    load_few<GD, W>(g, n, gv);
-    if (t.master != nullptr)
-      load_few<kDtypeF32, W>(t.master + at, n, pv);
-    else
-      load_few<PD, W>(p, n, pv);
+  const uint4* const p = MASTER ? reinterpret_cast<const uint4*>(t.master + at)
+                                : reinterpret_cast<const uint4*>(static_cast<const typename Elem<PD>::T*>(t.p) + at);
+  const uint4* const g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GD>::T*>(t.g) + at);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const uint32_t a = i < n ? mc[i] : 0, b = i < n ? vc[i] : 0;
-      if (i < 4) m8.x |= a << (8 * i), v8.x |= b << (8 * i);
-      else m8.y |= a << (8 * i - 32), v8.y |= b << (8 * i - 32);
-    }
+  for (int i = 0; i < R::PV; ++i) copy_async(&ring->wide[slot][i][lane], p + i);
+#pragma unroll
+  for (int i = 0; i < R::GV; ++i) copy_async(&ring->wide[slot][2 + i][lane], g + i);
+  copy_async8(&ring->m[slot][lane], static_cast<const unsigned char*>(t.m) + at);
+  copy_async8(&ring->v[slot][lane], static_cast<const unsigned char*>(t.v) + at);
+}
+
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void read_packed(const WarpRing* ring, int slot, Packed<PD, GD, MASTER>& r) {
+  using R = Packed<PD, GD, MASTER>;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < R::PV; ++i) r.p[i] = ring->wide[slot][i][lane];
+#pragma unroll
+  for (int i = 0; i < R::GV; ++i) r.g[i] = ring->wide[slot][2 + i][lane];
+  r.m = ring->m[slot][lane];
+  r.v = ring->v[slot][lane];
+}
+
+// A block at the tensor's end or off the vectors' boundaries, element by element; what is not there is 0.
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void load_packed_few(const AdamTensor& t, long long block, int n, Packed<PD, GD, MASTER>& r) {
+  using P = typename Elem<PD>::T;
+  using G = typename Elem<GD>::T;
+  using R = Packed<PD, GD, MASTER>;
+  const long long at = block * kAdamBlock + (threadIdx.x & 31) * W;
+  r.ms = t.m_scale[block];
+  r.vs = t.v_scale[block];
+  float f[8];
+  load_few<GD, W>(static_cast<const G*>(t.g) + at, n, f);
+#pragma unroll
+  for (int i = 0; i < R::GV; ++i) {
+    float part[Elem<GD>::W];
+#pragma unroll
+    for (int j = 0; j < Elem<GD>::W; ++j) part[j] = f[i * Elem<GD>::W + j];
+    r.g[i] = Elem<GD>::pack(part);
   }
-  const float ms = t.m_scale[block], vs = t.v_scale[block];
-  codes_to_float(m8, mv);
-  codes_to_float(v8, vv);
-  float mt = 0.f, vt = 0.f;  // largest |m| and root of v
+  constexpr int PDT = MASTER ? kDtypeF32 : PD;
+  if constexpr (MASTER)
+    load_few<kDtypeF32, W>(t.master + at, n, f);
+  else
+    load_few<PD, W>(static_cast<const P*>(t.p) + at, n, f);
+#pragma unroll
+  for (int i = 0; i < R::PV; ++i) {
+    float part[Elem<PDT>::W];
+#pragma unroll
+    for (int j = 0; j < Elem<PDT>::W; ++j) part[j] = f[i * Elem<PDT>::W + j];
+    r.p[i] = Elem<PDT>::pack(part);
+  }
+  const unsigned char* const mc = static_cast<const unsigned char*>(t.m) + at;
+  const unsigned char* const vc = static_cast<const unsigned char*>(t.v) + at;
+  r.m = r.v = make_uint2(0, 0);
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    mv[i] *= ms;
-    vv[i] *= vs;
-    vv[i] *= vv[i];
-    update(s, shrink, gv[i], mv[i], vv[i], root[i], pv[i]);
-    mt = nan_max(mt, fabsf(mv[i]));
-    vt = nan_max(vt, root[i]);
+    const uint32_t a = i < n ? mc[i] : 0u, c = i < n ? vc[i] : 0u;
+    if (i < 4) {
+      r.m.x |= a << (8 * i);
+      r.v.x |= c << (8 * i);
+    } else {
+      r.m.y |= a << (8 * i - 32);
+      r.v.y |= c << (8 * i - 32);
+    }
+  }
+}
+
+// A block's step, of which n elements are this lane's (W where WHOLE).  The warp's lanes share the two
+// maxima; all of them must come here.
+template <int PD, int GD, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void step_packed(const AdamTensor& t, const Step& s, float shrink, long long block, int n,
+                                            const Packed<PD, GD, MASTER>& r) {
+  using P = typename Elem<PD>::T;
+  using R = Packed<PD, GD, MASTER>;
+  constexpr int H = W / 2, PDT = MASTER ? kDtypeF32 : PD;
+  F2 p[H], m[H], u[H];
+#pragma unroll
+  for (int i = 0; i < R::PV; ++i) {
+    F2 part[H / R::PV];
+    unpack2<PDT, W / R::PV>(r.p[i], part);
+#pragma unroll
+    for (int j = 0; j < H / R::PV; ++j) p[i * (H / R::PV) + j] = part[j];
+  }
+#pragma unroll
+  for (int i = 0; i < R::GV; ++i) {
+    F2 part[H / R::GV];
+    unpack2<GD, W / R::GV>(r.g[i], part);
+#pragma unroll
+    for (int j = 0; j < H / R::GV; ++j) u[i * (H / R::GV) + j] = part[j];
+  }
+  float mt = 0.f, ut = 0.f;  // largest |m| and root of v
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const F2 g = mul2(u[i], f2(s.scale));
+    F2 v = mul2(codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), f2(r.vs));
+    v = fma2(mul2(v, v), f2(s.b2), mul2(mul2(g, g), f2(s.c2)));
+    m[i] = fma2(mul2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(r.ms)), f2(s.b1), mul2(g, f2(s.c1)));
+    u[i] = f2(root_approx(v.x), root_approx(v.y));
+    const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
+    p[i] = fma2(p[i], f2(shrink), mul2(f2(__fdividef(m[i].x, d.x), __fdividef(m[i].y, d.y)), f2(-s.rate_m)));
+    mt = nan_max(mt, nan_max(fabsf(m[i].x), fabsf(m[i].y)));
+    ut = nan_max(ut, nan_max(u[i].x, u[i].y));
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) {
     mt = nan_max(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-    vt = nan_max(vt, __shfl_xor_sync(0xffffffffu, vt, off));
+    ut = nan_max(ut, __shfl_xor_sync(0xffffffffu, ut, off));
   }
-  const float m_new = __fdiv_rn(mt, kTop8), v_new = __fdiv_rn(vt, kTop8);
-  const float m_by = m_new != 0.f ? m_new : 1.f, v_by = v_new != 0.f ? v_new : 1.f;
-  if (fminf(m_by, v_by) > kSmall8 && fmaxf(m_by, v_by) < 1.f / kSmall8) {
-    const float m_inv = __fdiv_rn(1.f, m_by), v_inv = __fdiv_rn(1.f, v_by);
+  const float ms = __fdiv_rn(mt, kTop8), us = __fdiv_rn(ut, kTop8);
+  const float m_by = ms != 0.f ? ms : 1.f, u_by = us != 0.f ? us : 1.f;
+  // the least code in the root's units; a root that is 0 stays 0
+  if (fminf(m_by, u_by) > kSmall8 && fmaxf(m_by, u_by) < 1.f / kSmall8) {
+    const float m_inv = __fdividef(1.f, m_by), u_inv = __fdividef(1.f, u_by);
 #pragma unroll
-    for (int i = 0; i < W; ++i) mv[i] *= m_inv, vv[i] = root[i] * v_inv;
+    for (int i = 0; i < H; ++i) m[i] = mul2(m[i], f2(m_inv)), u[i] = mul2(u[i], f2(u_inv));
   } else {  // the reciprocal would be infinite or lose digits (or a value is not finite)
 #pragma unroll
-    for (int i = 0; i < W; ++i) mv[i] = __fdiv_rn(mv[i], m_by), vv[i] = __fdiv_rn(root[i], v_by);
+    for (int i = 0; i < H; ++i) {
+      m[i] = f2(__fdiv_rn(m[i].x, m_by), __fdiv_rn(m[i].y, m_by));
+      u[i] = f2(__fdiv_rn(u[i].x, u_by), __fdiv_rn(u[i].y, u_by));
+    }
   }
 #pragma unroll
-  for (int i = 0; i < W; ++i) vv[i] = vv[i] > 0.f ? fmaxf(vv[i], kLeast8) : vv[i];
-  m8 = float_to_codes(mv);
-  v8 = float_to_codes(vv);
-  if (wide) {
+  for (int i = 0; i < H; ++i)
+    u[i] = f2(u[i].x > 0.f ? fmaxf(u[i].x, kLeast8) : u[i].x, u[i].y > 0.f ? fmaxf(u[i].y, kLeast8) : u[i].y);
+  const uint2 m8 = make_uint2(f2_to_codes(m[0]) | f2_to_codes(m[1]) << 16, f2_to_codes(m[2]) | f2_to_codes(m[3]) << 16);
+  const uint2 v8 = make_uint2(f2_to_codes(u[0]) | f2_to_codes(u[1]) << 16, f2_to_codes(u[2]) | f2_to_codes(u[3]) << 16);
+  const long long at = block * kAdamBlock + (threadIdx.x & 31) * W;
+  P* const out = static_cast<P*>(t.p) + at;
+  unsigned char* const mc = static_cast<unsigned char*>(t.m) + at;
+  unsigned char* const vc = static_cast<unsigned char*>(t.v) + at;
+  float pv[W];
+#pragma unroll
+  for (int i = 0; i < H; ++i) pv[2 * i] = p[i].x, pv[2 * i + 1] = p[i].y;
+  if (WHOLE) {
     *reinterpret_cast<uint2*>(mc) = m8;
     *reinterpret_cast<uint2*>(vc) = v8;
-    if (t.master != nullptr) store_wide<kDtypeF32, W>(t.master + at, pv);
-    store_wide<PD, W>(p, pv);
+    if (MASTER) store_wide<kDtypeF32, W>(t.master + at, pv);
+    store_wide<PD, W>(out, pv);
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       if (i < n) {
-        mc[i] = static_cast<unsigned char>((i < 4 ? m8.x >> (8 * i) : m8.y >> (8 * i - 32)) & 0xFF);
-        vc[i] = static_cast<unsigned char>((i < 4 ? v8.x >> (8 * i) : v8.y >> (8 * i - 32)) & 0xFF);
+        mc[i] = static_cast<unsigned char>((i < 4 ? m8.x : m8.y) >> (8 * (i & 3)));
+        vc[i] = static_cast<unsigned char>((i < 4 ? v8.x : v8.y) >> (8 * (i & 3)));
       }
     }
-    if (t.master != nullptr) store_few<kDtypeF32, W>(t.master + at, n, pv);
-    store_few<PD, W>(p, n, pv);
+    if (MASTER) store_few<kDtypeF32, W>(t.master + at, n, pv);
+    store_few<PD, W>(out, n, pv);
   }
-  if (lane == 0) {
-    t.m_scale[block] = m_new;
-    t.v_scale[block] = v_new;
+  if ((threadIdx.x & 31) == 0) {
+    t.m_scale[block] = ms;
+    t.v_scale[block] = us;
   }
 }
 
-template <int PD, int GD>
-__device__ __forceinline__ void block_chunk(const AdamTensor& t, const Step& s, int chunk) {
+// 8-bit states: warp w of the CTA takes the chunk's blocks w, w + 8, ...
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* shared, int chunk) {
+  extern __shared__ uint4 adam_ring[];
+  WarpRing* const ring = reinterpret_cast<WarpRing*>(adam_ring) + (threadIdx.x >> 5);
+  const Step s = *shared;
   const float shrink = 1.f - s.rate * t.decay;
   const long long blocks = (t.n + kAdamBlock - 1) / kAdamBlock;
-  long long b = static_cast<long long>(chunk) * (kAdamChunk / kAdamBlock) + (threadIdx.x >> 5);
+  constexpr int warps = kAdamThreads / 32, per = kAdamPackedChunk / kAdamBlock;
+  const long long first = static_cast<long long>(chunk) * per;
+  const long long end = first + per < blocks ? first + per : blocks;
+  const long long whole = t.head < 0 ? 0 : t.n / kAdamBlock;  // blocks that come in whole vectors
+  long long b = first + (threadIdx.x >> 5);
+  const long long stop = end < whole ? end : whole;
+  // blocks b, b + 8, ... below stop
+  const int count = b < stop ? static_cast<int>((stop - b + warps - 1) / warps) : 0;
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) {
+    if (i < count) copy_packed<PD, GD, MASTER>(t, b + i * warps, ring, i);
+    copy_commit();
+  }
+  Packed<PD, GD, MASTER> r;
+  float ms = 0.f, vs = 0.f;  // of the next block
+  if (count > 0) ms = t.m_scale[b], vs = t.v_scale[b];
+  int slot = 0;
 #pragma unroll 1
-  for (int i = 0; i < kAdamChunk / kAdamBlock / (kAdamThreads / 32); ++i, b += kAdamThreads / 32)
-    if (b < blocks) block_elements<PD, GD>(t, s, shrink, b);
+  for (int i = 0; i < count; ++i, b += warps) {
+    if (i + kAhead - 1 < count)
+      copy_packed<PD, GD, MASTER>(t, b + (kAhead - 1) * warps, ring, slot == 0 ? kAhead - 1 : slot - 1);
+    copy_commit();
+    copy_wait<kAhead - 1>();
+    read_packed(ring, slot, r);
+    r.ms = ms;
+    r.vs = vs;
+    if (i + 1 < count) ms = t.m_scale[b + warps], vs = t.v_scale[b + warps];
+    step_packed<PD, GD, MASTER, true>(t, s, shrink, b, W, r);
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+  }
+  copy_wait<0>();
+#pragma unroll 1
+  for (; b < end; b += warps) {
+    const long long left = t.n - (b * kAdamBlock + (threadIdx.x & 31) * W);
+    const int n = left < W ? (left > 0 ? static_cast<int>(left) : 0) : W;
+    load_packed_few(t, b, n, r);
+    step_packed<PD, GD, MASTER, false>(t, s, shrink, b, n, r);
+  }
+}
+template <int PD, int GD>
+__device__ __forceinline__ void block_chunk(const AdamTensor& t, const Step* shared, int chunk) {
+  if (t.master != nullptr)
+    packed_chunk<PD, GD, true>(t, shared, chunk);
+  else
+    packed_chunk<PD, GD, false>(t, shared, chunk);
 }
 
 template <int PD, int GD, int BITS>
-__device__ __forceinline__ void chunk_of(const AdamTensor& t, const Step& s, int chunk) {
+__device__ __forceinline__ void chunk_of(const AdamTensor& t, const Step* shared, int chunk) {
   if constexpr (BITS == 8)
-    block_chunk<PD, GD>(t, s, chunk);
+    block_chunk<PD, GD>(t, shared, chunk);
   else
-    plain_chunk<PD, GD>(t, s, chunk);
+    plain_chunk<PD, GD>(t, shared, chunk);
 }
 
 template <int MOST, int BITS>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
+__global__ void __launch_bounds__(kAdamThreads, kAdamResident<BITS>) adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
   __shared__ Step shared;
   if (threadIdx.x == 0) shared = read_step(table.k);
   __syncthreads();
-  const Step s = shared;
   for (int c = blockIdx.x; c < table.chunks; c += gridDim.x) {
     int lo = 0, hi = table.count;  // the last tensor whose first chunk is not past c
     while (hi - lo > 1) {
@@ -305,25 +444,33 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     }
     const AdamTensor& t = table.t[lo];
     const int chunk = c - t.first_chunk;
-    if (t.param_dtype == kDtypeF32) chunk_of<kDtypeF32, kDtypeF32, BITS>(t, s, chunk);
+    if (t.param_dtype == kDtypeF32) chunk_of<kDtypeF32, kDtypeF32, BITS>(t, &shared, chunk);
     else if (t.param_dtype == kDtypeBF16) {
-      if (t.grad_dtype == kDtypeBF16) chunk_of<kDtypeBF16, kDtypeBF16, BITS>(t, s, chunk);
-      else chunk_of<kDtypeBF16, kDtypeF32, BITS>(t, s, chunk);
+      if (t.grad_dtype == kDtypeBF16) chunk_of<kDtypeBF16, kDtypeBF16, BITS>(t, &shared, chunk);
+      else chunk_of<kDtypeBF16, kDtypeF32, BITS>(t, &shared, chunk);
     } else {
-      if (t.grad_dtype == kDtypeF16) chunk_of<kDtypeF16, kDtypeF16, BITS>(t, s, chunk);
-      else chunk_of<kDtypeF16, kDtypeF32, BITS>(t, s, chunk);
+      if (t.grad_dtype == kDtypeF16) chunk_of<kDtypeF16, kDtypeF16, BITS>(t, &shared, chunk);
+      else chunk_of<kDtypeF16, kDtypeF32, BITS>(t, &shared, chunk);
     }
   }
 }
 
 }  // namespace
 
+cudaError_t adamw_setup() {
+  const int bytes = kAdamThreads / 32 * sizeof(WarpRing);
+  cudaError_t e = note_cuda(cudaFuncSetAttribute(adamw_kernel<kAdamFew, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (e == cudaSuccess)
+    e = note_cuda(cudaFuncSetAttribute(adamw_kernel<kAdamMany, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  return e;
+}
+
 template <int MOST>
 cudaError_t launch_adamw(const AdamTable<MOST>& table, int bits, int num_sms, cudaStream_t s) {
-  const int most = 8 * num_sms;
+  const int most = (bits == 8 ? kAdamResident<8> : kAdamResident<32>) * num_sms;
   const int blocks = table.chunks < most ? table.chunks : most;
   if (bits == 8)
-    adamw_kernel<MOST, 8><<<blocks, kAdamThreads, 0, s>>>(table);
+    adamw_kernel<MOST, 8><<<blocks, kAdamThreads, kAdamThreads / 32 * sizeof(WarpRing), s>>>(table);
   else
     adamw_kernel<MOST, 32><<<blocks, kAdamThreads, 0, s>>>(table);
   return launch_result();

@@ -6,7 +6,8 @@
 namespace llp {
 
 constexpr int kAdamBlock = 256;   // values of an 8-bit state that share a scale
-constexpr int kAdamChunk = 4096;  // elements that a CTA takes at a time
+constexpr int kAdamChunk = 8192;         // elements that a CTA takes at a time, states in 32 bits
+constexpr int kAdamPackedChunk = 16384;  // and in 8
 
 // One tensor, as the kernel's parameters hold it.
 struct AdamTensor {
@@ -44,6 +45,7 @@ struct AdamTable {
   AdamTensor t[MOST];
 };
 
+cudaError_t adamw_setup();
 template <int MOST>
 cudaError_t launch_adamw(const AdamTable<MOST>& table, int bits, int num_sms, cudaStream_t s);
 

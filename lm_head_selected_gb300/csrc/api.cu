@@ -126,6 +126,7 @@ int init_device(DeviceInit** out) {
                llp::layer_norm_fwd_setup() != cudaSuccess || llp::layer_norm_bwd_setup() != cudaSuccess ||
                llp::gated_setup(&d.gated) != cudaSuccess || llp::residual_norm_fwd_setup() != cudaSuccess ||
                llp::residual_norm_bwd_setup() != cudaSuccess || llp::gated_small_setup() != cudaSuccess ||
+               llp::adamw_setup() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status_ptr), g_status_word) != cudaSuccess) {
       d.status = fail_cuda(__LINE__);
     } else {
@@ -1870,7 +1871,7 @@ int adamw_step(int64_t count, void* const* params, const void* const* grads, voi
       int64_t chunks = 0;
       while (last < all.size() && last - first < static_cast<size_t>(llp::kAdamMany)) {
         const int64_t head = all[last].head > 0 ? all[last].head : 0;
-        const int64_t own = all[last].n > head ? cdiv(all[last].n - head, llp::kAdamChunk) : 1;
+        const int64_t own = all[last].n > head ? cdiv(all[last].n - head, state_bits == 8 ? llp::kAdamPackedChunk : llp::kAdamChunk) : 1;
         if (last > first && chunks + own > (int64_t(1) << 30)) break;
         all[last].first_chunk = static_cast<int>(chunks);
         chunks += own;

@@ -5,7 +5,7 @@ up to 320 tensors, with nothing copied to the device.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import math
 from typing import List, Optional, Sequence, Tuple, Union
 
@@ -51,22 +51,23 @@ def _scalar(t, name: str, dtype: torch.dtype, device: torch.device):
     return t.data_ptr()
 
 
-def _pointers(name: str, tensors, sizes: List[int], device, dtype, blocks: bool = False, optional: bool = False):
-    """The tensors' addresses, after their checks."""
+def _addresses(tensors) -> array.array:
+    return array.array("Q", [0 if t is None else t.data_ptr() for t in tensors])
+
+
+def _need_all(name: str, tensors, sizes: List[int], index: int, dtype: torch.dtype) -> List[torch.Tensor]:
+    """The tensors, once they are known to be contiguous ones of dtype and of these sizes on one device."""
+    tensors = list(tensors)
     if len(tensors) != len(sizes):
         raise ValueError(f"{name} must have {len(sizes)} entries, got {len(tensors)}")
-    out = (ctypes.c_void_p * len(sizes))()
     for i, t in enumerate(tensors):
-        if t is None and optional:
-            continue
         if not isinstance(t, torch.Tensor) or t.dtype != dtype:
             raise TypeError(f"{name}[{i}] must be a tensor of {dtype}")
-        if t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous, on {device}")
-        if t.numel() != (-(-sizes[i] // BLOCK) if blocks else sizes[i]):
+        if t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous, on cuda:{index}")
+        if t.numel() != sizes[i]:
             raise ValueError(f"{name}[{i}] has {t.numel()} elements, which does not go with params[{i}]")
-        out[i] = t.data_ptr()
-    return out
+    return tensors
 
 
 def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Tensors, step: int, lr: float = 1e-3,
@@ -99,48 +100,59 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         return
     _need_cuda(params[0], "params[0]")
     device = params[0].device
-    p_ptr, g_ptr = (ctypes.c_void_p * count)(), (ctypes.c_void_p * count)()
-    p_code, g_code = (ctypes.c_int32 * count)(), (ctypes.c_int32 * count)()
-    sizes = []
+    index = device.index
+    p_code, g_code, sizes = [], [], []
     for i, (p, g) in enumerate(zip(params, grads)):
         if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
             raise TypeError(f"params[{i}] and grads[{i}] must be tensors")
         code, g_c = _DTYPE_CODES.get(p.dtype), _DTYPE_CODES.get(g.dtype)
         if code is None or (g_c != code and g_c != 1):
             raise TypeError(f"params[{i}] must be bf16, fp16 or fp32, grads[{i}] of the same dtype or fp32")
-        if p.device != device or g.device != device or not p.is_contiguous() or not g.is_contiguous():
+        if p.get_device() != index or g.get_device() != index or not p.is_contiguous() or not g.is_contiguous():
             raise ValueError(f"params[{i}] and grads[{i}] must be contiguous, on {device}")
-        n = p.numel()
         if g.shape != p.shape:
             raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
-        p_ptr[i], g_ptr[i], p_code[i], g_code[i] = p.data_ptr(), g.data_ptr(), code, g_c
-        sizes.append(n)
+        p_code.append(code)
+        g_code.append(g_c)
+        sizes.append(p.numel())
+    p_ptr = _addresses(params)
     starts = [a for a, n in zip(p_ptr, sizes) if n]
     if len(set(starts)) != len(starts):
         raise ValueError("a parameter is listed twice")
     packed = exp_avg_scale is not None
     dtype = CODE if packed else torch.float32
-    m = _pointers("exp_avg", exp_avg, sizes, device, dtype)
-    v = _pointers("exp_avg_sq", exp_avg_sq, sizes, device, dtype)
-    ms = _pointers("exp_avg_scale", exp_avg_scale, sizes, device, torch.float32, blocks=True) if packed else None
-    vs = _pointers("exp_avg_sq_scale", exp_avg_sq_scale, sizes, device, torch.float32, blocks=True) if packed else None
-    top = None if masters is None else _pointers("masters", masters, sizes, device, torch.float32, optional=True)
-    if isinstance(weight_decay, (int, float)):
-        weight_decay = [weight_decay] * count
-    if len(weight_decay) != count or not all(math.isfinite(w) for w in weight_decay):
+    arrays = [p_ptr, _addresses(grads), _addresses(_need_all("exp_avg", exp_avg, sizes, index, dtype)),
+              _addresses(_need_all("exp_avg_sq", exp_avg_sq, sizes, index, dtype))]
+    if packed:
+        blocks = [-(-n // BLOCK) for n in sizes]
+        arrays += [_addresses(_need_all(name, t, blocks, index, torch.float32)) for name, t in
+                   (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale))]
+    else:
+        arrays += [None, None]
+    if masters is None:
+        arrays.append(None)
+    else:
+        masters = list(masters)
+        if len(masters) != count:
+            raise ValueError(f"masters must have {count} entries, got {len(masters)}")
+        there = [i for i, t in enumerate(masters) if t is not None]
+        _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
+        arrays.append(_addresses(masters))
+    weight_decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else weight_decay
+    decay = array.array("d", weight_decay)
+    if len(decay) != count or not all(map(math.isfinite, decay)):
         raise ValueError(f"weight_decay must be finite, one value or {count}")
-    decay = (ctypes.c_double * count)(*weight_decay)
+    arrays += [array.array("q", sizes), array.array("i", p_code), array.array("i", g_code), decay]
     scalars = (_scalar(device_step, "device_step", torch.int64, device),
                _scalar(device_lr, "device_lr", torch.float32, device),
                _scalar(grad_scale, "grad_scale", torch.float32, device))
 
     def call():
-        st = _lib.load().adamw_step(count, p_ptr, g_ptr, m, v, ms, vs, top, (ctypes.c_int64 * count)(*sizes), p_code,
-                                    g_code, decay, 8 if packed else 32, lr, beta1, beta2, eps, step, *scalars,
-                                    _raw_stream(device.index))
+        st = _lib.load().adamw_step(count, *[None if a is None else a.buffer_info()[0] for a in arrays],
+                                    8 if packed else 32, lr, beta1, beta2, eps, step, *scalars, _raw_stream(index))
         _lib.check("adamw_step", st)
 
-    if device.index == torch._C._cuda_getDevice():
+    if index == torch._C._cuda_getDevice():
         call()
     else:
         with torch.cuda.device(device):

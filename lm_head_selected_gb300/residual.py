@@ -22,46 +22,56 @@ _NONE, _COLUMNS, _ROWS = 0, 1, 2
 def _rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> int:
     """Row stride of an optional tensor of like's shape and dtype."""
     if t is None:
-        return like.shape[1]
+        return 0
     if not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.shape != like.shape:
         raise ValueError(f"{name} must have x's shape and dtype")
+    if t.is_contiguous() and t.get_device() == like.get_device():
+        return t.stride(0)
     return _need_rows(t, name, like.device)
 
 
+def _column(t: torch.Tensor, name: str, x: torch.Tensor, D: int, dtype):
+    """dtype, or t's where that is None, once t is known to be a [D] parameter of it."""
+    if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
+        raise TypeError(f"{name} must be a tensor of x's dtype or fp32")
+    dtype = dtype or t.dtype
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.get_device() != x.get_device():
+        _need(t, name, dtype, x.device, 1)
+    if t.numel() != D:
+        raise ValueError(f"{name} must have {D} entries")
+    return dtype
+
+
 def _check(x: torch.Tensor, branch, gate, post_weight, weight, scale: float):
-    """(dtype code, parameters' dtype, its code, gate kind, row strides of x, branch and gate)."""
+    """(dtype code, parameters' dtype, its code, gate kind, row strides of x, branch and gate, N, D)."""
     _need_cuda(x, "x")
     code = _dtype_code(x, "x")
     stride = _need_rows(x, "x", x.device)
-    if x.shape[1] < 1:
+    N, D = x.shape
+    if D < 1:
         raise ValueError("x must have at least one column")
-    if branch is None and (gate is not None or post_weight is not None):
-        raise ValueError("gate and post_weight need a branch")
-    if branch is None and weight is None:
-        raise ValueError("a branch, a weight or both must be given")
+    if branch is None:
+        if gate is not None or post_weight is not None:
+            raise ValueError("gate and post_weight need a branch")
+        if weight is None:
+            raise ValueError("a branch, a weight or both must be given")
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
     b_stride = _rows(branch, "branch", x)
-    kind, g_stride, column_gate = _NONE, x.shape[1], None
+    kind, g_stride, dtype = _NONE, 0, None
     if gate is not None:
         if not isinstance(gate, torch.Tensor):
             raise TypeError("gate must be a torch.Tensor")
         if gate.dim() == 1:
-            kind, column_gate = _COLUMNS, gate
+            kind, dtype = _COLUMNS, _column(gate, "gate", x, D, None)
         else:
             kind, g_stride = _ROWS, _rows(gate, "gate", x)
-    dtype = None
-    for name, t in (("gate", column_gate), ("post_weight", post_weight), ("weight", weight)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
-            raise TypeError(f"{name} must be a tensor of x's dtype or fp32")
-        dtype = dtype or t.dtype
-        _need(t, name, dtype, x.device, 1)
-        if t.shape[0] != x.shape[1]:
-            raise ValueError(f"{name} must have {x.shape[1]} entries")
+    if post_weight is not None:
+        dtype = _column(post_weight, "post_weight", x, D, dtype)
+    if weight is not None:
+        dtype = _column(weight, "weight", x, D, dtype)
     dtype = dtype or x.dtype
-    return code, dtype, code if dtype == x.dtype else 1, kind, stride, b_stride, g_stride
+    return code, dtype, code if dtype == x.dtype else 1, kind, stride, b_stride, g_stride, N, D
 
 
 @on_tensor_device
@@ -72,9 +82,8 @@ def residual_rms_norm_fwd(x: torch.Tensor, branch: Optional[torch.Tensor] = None
     is given), h = s normed, times weight; h and rstd are None without a weight, post_rstd without a
     post_weight, and s is x itself without a branch."""
     scale = float(scale)
-    code, _, pcode, kind, xs, bs, gs = _check(x, branch, gate, post_weight, weight, scale)
+    code, _, pcode, kind, xs, bs, gs, N, D = _check(x, branch, gate, post_weight, weight, scale)
     dev = x.device
-    N, D = x.shape
     s = None if branch is None else torch.empty((N, D), dtype=x.dtype, device=dev)
     h = None if weight is None else torch.empty((N, D), dtype=x.dtype, device=dev)
     post_rstd = None if post_weight is None else torch.empty(N, dtype=torch.float32, device=dev)
@@ -98,9 +107,8 @@ def residual_rms_norm_bwd(grad_s: Optional[torch.Tensor], grad_h: Optional[torch
     whose input is None, from the forward's s (x itself without a branch) and statistics.  grad_s may be
     None; grad_h and rstd go with weight."""
     scale = float(scale)
-    code, pdt, pcode, kind, ss, bs, gts = _check(s, branch, gate, post_weight, weight, scale)
+    code, pdt, pcode, kind, ss, bs, gts, N, D = _check(s, branch, gate, post_weight, weight, scale)
     dev = s.device
-    N, D = s.shape
     if (grad_h is None) != (weight is None) or (rstd is None) != (weight is None):
         raise ValueError("grad_h and rstd must be given with weight, and only then")
     if (post_rstd is None) != (post_weight is None):
@@ -111,7 +119,7 @@ def residual_rms_norm_bwd(grad_s: Optional[torch.Tensor], grad_h: Optional[torch
     for name, t in (("post_rstd", post_rstd), ("rstd", rstd)):
         if t is not None:
             _need(t, name, torch.float32, dev, 1)
-            if t.shape[0] != N:
+            if t.numel() != N:
                 raise ValueError(f"{name} must have N entries")
 
     def rows(wanted):
