@@ -13,13 +13,15 @@ namespace llp {
 
 namespace {
 
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 256;   // of a CTA, states in 32 bits
+constexpr int kPackedThreads = 128;  // and in 8
+constexpr int kWarpBlocks = kAdamPackedChunk / kAdamBlock / (kPackedThreads / 32);  // to a warp of a chunk
+static_assert(kAdamPackedChunk % (2 * kAdamBlock * (kPackedThreads / 32)) == 0 && kWarpBlocks <= 16, "a lane for each scale");
 template <int BITS>
-constexpr int kAdamResident = BITS == 8 ? 3 : 4;  // CTAs to an SM: 80 or 64 registers per thread
+constexpr int kAdamResident = BITS == 8 ? 5 : 4;  // CTAs to an SM: 96 or 64 registers per thread
 constexpr int W = 8;  // elements of a thread's step
 constexpr float kTop8 = 448.f;              // largest e4m3 value
 constexpr float kLeast8 = 0.001953125f;     // smallest above 0, 2^-9
-constexpr float kSmall8 = 1e-30f;           // scales above this and below its reciprocal have a normal reciprocal
 
 struct Step {
   float b1, c1, b2, c2, eps, rate, rate_m, root_v, scale;
@@ -171,10 +173,26 @@ __device__ __forceinline__ float nan_max(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Within two units in the last place; 0 and infinity are exact.
-__device__ __forceinline__ float root_approx(float v) {
+// Of three, in one instruction: max.NaN of magnitudes, and min.
+__device__ __forceinline__ float nan_max3_abs(float a, float b, float c) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// One instruction each, within two units in the last place; subnormals count as 0.
+__device__ __forceinline__ float root_ftz(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float inverse_ftz(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -187,52 +205,74 @@ struct Packed {
   float ms, vs;
 };
 
-// The blocks to come are under way in a ring of shared memory, kAhead to a warp; every lane copies what it
-// will read itself.
-constexpr int kAhead = 3;
-constexpr int kSlotWords = 4;  // 16-byte words of a lane's slot at most: two of the parameter, two of the gradient
-struct WarpRing {
-  uint4 wide[kAhead][kSlotWords][32];
-  uint2 m[kAhead][32];
-  uint2 v[kAhead][32];
+// The blocks to come are under way in a ring of shared memory, two neighbours to a slot, so that their codes
+// too come in 16-byte copies, which go past L1 (8-byte ones need lines of it, and there is little left
+// beside the ring).
+template <int PD, int GD, bool MASTER>
+struct Slot8 {
+  using R = Packed<PD, GD, MASTER>;
+  uint4 p[2][R::PV][32];
+  uint4 g[2][R::GV][32];
+  uint2 m[2][32];
+  uint2 v[2][32];
 };
+constexpr int kWarpRing = 9216;  // bytes of a warp's ring: three slots of 16-bit parameters and gradients, one or two of others
 
-__device__ __forceinline__ void copy_async8(void* slot, const void* p) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
-               "l"(p)
-               : "memory");
+// The pair's blocks below `stop`.
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void copy_pair(const AdamTensor& t, long long block, long long stop, Slot8<PD, GD, MASTER>* slot) {
+  using R = Packed<PD, GD, MASTER>;
+  const int lane = threadIdx.x & 31;
+  const bool both = block + 1 < stop;
+  const long long at = block * kAdamBlock;
+  const uint4* const p = MASTER ? reinterpret_cast<const uint4*>(t.master + at + lane * W)
+                                : reinterpret_cast<const uint4*>(static_cast<const typename Elem<PD>::T*>(t.p) + at + lane * W);
+  const uint4* const g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GD>::T*>(t.g) + at + lane * W);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k == 0 || both) {
+#pragma unroll
+      for (int i = 0; i < R::PV; ++i) copy_async(&slot->p[k][i][lane], p + k * 32 * R::PV + i);
+#pragma unroll
+      for (int i = 0; i < R::GV; ++i) copy_async(&slot->g[k][i][lane], g + k * 32 * R::GV + i);
+    }
+  }
+  if (lane < 16 || both) {
+    copy_async(reinterpret_cast<uint4*>(slot->m) + lane, static_cast<const unsigned char*>(t.m) + at + 16 * lane);
+    copy_async(reinterpret_cast<uint4*>(slot->v) + lane, static_cast<const unsigned char*>(t.v) + at + 16 * lane);
+  }
 }
 
 template <int PD, int GD, bool MASTER>
-__device__ __forceinline__ void copy_packed(const AdamTensor& t, long long block, WarpRing* ring, int slot) {
+__device__ __forceinline__ void read_packed(const Slot8<PD, GD, MASTER>* slot, int k, Packed<PD, GD, MASTER>& r) {
   using R = Packed<PD, GD, MASTER>;
   const int lane = threadIdx.x & 31;
-  const long long at = block * kAdamBlock + lane * W;
+#pragma unroll
+  for (int i = 0; i < R::PV; ++i) r.p[i] = slot->p[k][i][lane];
+#pragma unroll
+  for (int i = 0; i < R::GV; ++i) r.g[i] = slot->g[k][i][lane];
+  r.m = slot->m[k][lane];
+  r.v = slot->v[k][lane];
+}
+
+// A block's elements straight from memory: whole vectors, or at the tensor's end and off the vectors'
+// boundaries one by one; what is not there is 0.
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void load_packed(const AdamTensor& t, long long block, Packed<PD, GD, MASTER>& r) {
+  using R = Packed<PD, GD, MASTER>;
+  const long long at = block * kAdamBlock + (threadIdx.x & 31) * W;
   const uint4* const p = MASTER ? reinterpret_cast<const uint4*>(t.master + at)
                                 : reinterpret_cast<const uint4*>(static_cast<const typename Elem<PD>::T*>(t.p) + at);
   const uint4* const g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GD>::T*>(t.g) + at);
 #pragma unroll
-  for (int i = 0; i < R::PV; ++i) copy_async(&ring->wide[slot][i][lane], p + i);
+  for (int i = 0; i < R::PV; ++i) r.p[i] = p[i];
 #pragma unroll
-  for (int i = 0; i < R::GV; ++i) copy_async(&ring->wide[slot][2 + i][lane], g + i);
-  copy_async8(&ring->m[slot][lane], static_cast<const unsigned char*>(t.m) + at);
-  copy_async8(&ring->v[slot][lane], static_cast<const unsigned char*>(t.v) + at);
+  for (int i = 0; i < R::GV; ++i) r.g[i] = g[i];
+  r.m = *reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(t.m) + at);
+  r.v = *reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(t.v) + at);
+  r.ms = t.m_scale[block];
+  r.vs = t.v_scale[block];
 }
-
-template <int PD, int GD, bool MASTER>
-__device__ __forceinline__ void read_packed(const WarpRing* ring, int slot, Packed<PD, GD, MASTER>& r) {
-  using R = Packed<PD, GD, MASTER>;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < R::PV; ++i) r.p[i] = ring->wide[slot][i][lane];
-#pragma unroll
-  for (int i = 0; i < R::GV; ++i) r.g[i] = ring->wide[slot][2 + i][lane];
-  r.m = ring->m[slot][lane];
-  r.v = ring->v[slot][lane];
-}
-
-// A block at the tensor's end or off the vectors' boundaries, element by element; what is not there is 0.
 template <int PD, int GD, bool MASTER>
 __device__ __forceinline__ void load_packed_few(const AdamTensor& t, long long block, int n, Packed<PD, GD, MASTER>& r) {
   using P = typename Elem<PD>::T;
@@ -278,15 +318,10 @@ __device__ __forceinline__ void load_packed_few(const AdamTensor& t, long long b
   }
 }
 
-// A block's step, of which n elements are this lane's (W where WHOLE).  The warp's lanes share the two
-// maxima; all of them must come here.
-template <int PD, int GD, bool MASTER, bool WHOLE>
-__device__ __forceinline__ void step_packed(const AdamTensor& t, const Step& s, float shrink, long long block, int n,
-                                            const Packed<PD, GD, MASTER>& r) {
-  using P = typename Elem<PD>::T;
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void unpack_packed(const Packed<PD, GD, MASTER>& r, F2 (&p)[W / 2], F2 (&g)[W / 2]) {
   using R = Packed<PD, GD, MASTER>;
   constexpr int H = W / 2, PDT = MASTER ? kDtypeF32 : PD;
-  F2 p[H], m[H], u[H];
 #pragma unroll
   for (int i = 0; i < R::PV; ++i) {
     F2 part[H / R::PV];
@@ -299,43 +334,15 @@ __device__ __forceinline__ void step_packed(const AdamTensor& t, const Step& s, 
     F2 part[H / R::GV];
     unpack2<GD, W / R::GV>(r.g[i], part);
 #pragma unroll
-    for (int j = 0; j < H / R::GV; ++j) u[i * (H / R::GV) + j] = part[j];
+    for (int j = 0; j < H / R::GV; ++j) g[i * (H / R::GV) + j] = part[j];
   }
-  float mt = 0.f, ut = 0.f;  // largest |m| and root of v
-#pragma unroll
-  for (int i = 0; i < H; ++i) {
-    const F2 g = mul2(u[i], f2(s.scale));
-    F2 v = mul2(codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), f2(r.vs));
-    v = fma2(mul2(v, v), f2(s.b2), mul2(mul2(g, g), f2(s.c2)));
-    m[i] = fma2(mul2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(r.ms)), f2(s.b1), mul2(g, f2(s.c1)));
-    u[i] = f2(root_approx(v.x), root_approx(v.y));
-    const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
-    p[i] = fma2(p[i], f2(shrink), mul2(f2(__fdividef(m[i].x, d.x), __fdividef(m[i].y, d.y)), f2(-s.rate_m)));
-    mt = nan_max(mt, nan_max(fabsf(m[i].x), fabsf(m[i].y)));
-    ut = nan_max(ut, nan_max(u[i].x, u[i].y));
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    mt = nan_max(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-    ut = nan_max(ut, __shfl_xor_sync(0xffffffffu, ut, off));
-  }
-  const float ms = __fdiv_rn(mt, kTop8), us = __fdiv_rn(ut, kTop8);
-  const float m_by = ms != 0.f ? ms : 1.f, u_by = us != 0.f ? us : 1.f;
-  // the least code in the root's units; a root that is 0 stays 0
-  if (fminf(m_by, u_by) > kSmall8 && fmaxf(m_by, u_by) < 1.f / kSmall8) {
-    const float m_inv = __fdividef(1.f, m_by), u_inv = __fdividef(1.f, u_by);
-#pragma unroll
-    for (int i = 0; i < H; ++i) m[i] = mul2(m[i], f2(m_inv)), u[i] = mul2(u[i], f2(u_inv));
-  } else {  // the reciprocal would be infinite or lose digits (or a value is not finite)
-#pragma unroll
-    for (int i = 0; i < H; ++i) {
-      m[i] = f2(__fdiv_rn(m[i].x, m_by), __fdiv_rn(m[i].y, m_by));
-      u[i] = f2(__fdiv_rn(u[i].x, u_by), __fdiv_rn(u[i].y, u_by));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < H; ++i)
-    u[i] = f2(u[i].x > 0.f ? fmaxf(u[i].x, kLeast8) : u[i].x, u[i].y > 0.f ? fmaxf(u[i].y, kLeast8) : u[i].y);
+}
+
+// n of the lane's elements (W where WHOLE) and their codes.
+template <int PD, int GD, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void store_packed(const AdamTensor& t, long long block, int n, const F2 (&p)[W / 2],
+                                             const F2 (&m)[W / 2], const F2 (&u)[W / 2]) {
+  using P = typename Elem<PD>::T;
   const uint2 m8 = make_uint2(f2_to_codes(m[0]) | f2_to_codes(m[1]) << 16, f2_to_codes(m[2]) | f2_to_codes(m[3]) << 16);
   const uint2 v8 = make_uint2(f2_to_codes(u[0]) | f2_to_codes(u[1]) << 16, f2_to_codes(u[2]) | f2_to_codes(u[3]) << 16);
   const long long at = block * kAdamBlock + (threadIdx.x & 31) * W;
@@ -344,7 +351,7 @@ __device__ __forceinline__ void step_packed(const AdamTensor& t, const Step& s, 
   unsigned char* const vc = static_cast<unsigned char*>(t.v) + at;
   float pv[W];
 #pragma unroll
-  for (int i = 0; i < H; ++i) pv[2 * i] = p[i].x, pv[2 * i + 1] = p[i].y;
+  for (int i = 0; i < W / 2; ++i) pv[2 * i] = p[i].x, pv[2 * i + 1] = p[i].y;
   if (WHOLE) {
     *reinterpret_cast<uint2*>(mc) = m8;
     *reinterpret_cast<uint2*>(vc) = v8;
@@ -361,58 +368,182 @@ __device__ __forceinline__ void step_packed(const AdamTensor& t, const Step& s, 
     if (MASTER) store_few<kDtypeF32, W>(t.master + at, n, pv);
     store_few<PD, W>(out, n, pv);
   }
+}
+__device__ __forceinline__ void store_scales(const AdamTensor& t, long long block, float ms, float us) {
   if ((threadIdx.x & 31) == 0) {
     t.m_scale[block] = ms;
     t.v_scale[block] = us;
   }
 }
 
-// 8-bit states: warp w of the CTA takes the chunk's blocks w, w + 8, ...
+// The block's largest of non-negative values; NaN, whose bits are above infinity's, wins.
+__device__ __forceinline__ float warp_top(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
+
+// A block's step for any values.  The warp's lanes share the two maxima; all of them must come here.
+template <int PD, int GD, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, float shrink, long long block, int n,
+                                         const Packed<PD, GD, MASTER>& r) {
+  constexpr int H = W / 2;
+  F2 p[H], m[H], u[H];
+  unpack_packed(r, p, u);
+  float mt = 0.f, ut = 0.f;  // largest |m| and root of v
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const F2 g = mul2(u[i], f2(s.scale));
+    F2 v = mul2(codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), f2(r.vs));
+    v = fma2(mul2(v, v), f2(s.b2), mul2(mul2(g, g), f2(s.c2)));
+    m[i] = fma2(mul2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(r.ms)), f2(s.b1), mul2(g, f2(s.c1)));
+    u[i] = f2(sqrtf(v.x), sqrtf(v.y));
+    const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
+    p[i] = fma2(p[i], f2(shrink), mul2(f2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y)), f2(-s.rate_m)));
+    mt = nan_max(mt, nan_max(fabsf(m[i].x), fabsf(m[i].y)));
+    ut = nan_max(ut, nan_max(u[i].x, u[i].y));
+  }
+  const float ms = __fdiv_rn(warp_top(mt), kTop8), us = __fdiv_rn(warp_top(ut), kTop8);
+  const float m_by = ms != 0.f ? ms : 1.f, u_by = us != 0.f ? us : 1.f;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    m[i] = f2(__fdiv_rn(m[i].x, m_by), __fdiv_rn(m[i].y, m_by));
+    u[i] = f2(__fdiv_rn(u[i].x, u_by), __fdiv_rn(u[i].y, u_by));
+    // a root above 0 is not stored as 0
+    u[i] = f2(u[i].x > 0.f ? fmaxf(u[i].x, kLeast8) : u[i].x, u[i].y > 0.f ? fmaxf(u[i].y, kLeast8) : u[i].y);
+  }
+  store_packed<PD, GD, MASTER, WHOLE>(t, block, n, p, m, u);
+  store_scales(t, block, ms, us);
+}
+
+// The same of a whole block whose values lie in the middle of fp32's range and whose roots are all above 0,
+// in fewer instructions (395 -> 220 for 256 elements): the scales' factors are taken into the betas',
+// and roots and reciprocals come from the instructions that flush subnormals to 0.  The new scales are
+// the caller's to store.  False, and nothing written, where a value lies outside.
+template <int PD, int GD, bool MASTER, bool WHOLE>
+__device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, float shrink, long long block,
+                                           const Packed<PD, GD, MASTER>& r, float& ms, float& us) {
+  constexpr int H = W / 2;
+  constexpr float kLow = 1e-15f, kHigh = 1e15f;
+  if (!(r.vs > kLow && r.vs < kHigh && r.ms < kHigh)) return false;  // the same in all lanes
+  F2 p[H], m[H], u[H];
+  unpack_packed(r, p, u);
+  const float mb = r.ms * s.b1, vb = r.vs * r.vs * s.b2;
+  float mt = 0.f, ut = 0.f, least = kHigh;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const F2 c = codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1);
+    const F2 g = mul2(u[i], f2(s.scale));
+    const F2 v = fma2(mul2(c, c), f2(vb), mul2(mul2(g, g), f2(s.c2)));
+    m[i] = fma2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(mb), mul2(g, f2(s.c1)));
+    u[i] = f2(root_ftz(v.x), root_ftz(v.y));
+    const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
+    p[i] = fma2(mul2(m[i], f2(inverse_ftz(d.x), inverse_ftz(d.y))), f2(-s.rate_m), mul2(p[i], f2(shrink)));
+    mt = nan_max3_abs(mt, m[i].x, m[i].y);
+    ut = nan_max3_abs(ut, u[i].x, u[i].y);
+    least = min3(least, u[i].x, u[i].y);
+  }
+  mt = warp_top(mt);
+  ut = warp_top(ut);
+  const bool fine = least > 1e-18f && mt > 1e-25f && mt < kHigh && ut < kHigh;  // no: a NaN too
+  if (!__all_sync(0xffffffffu, fine)) return false;
+  const float m_inv = kTop8 * inverse_ftz(mt), u_inv = kTop8 * inverse_ftz(ut);
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    m[i] = mul2(m[i], f2(m_inv));
+    u[i] = mul2(u[i], f2(u_inv));
+    u[i] = f2(fmaxf(u[i].x, kLeast8), fmaxf(u[i].y, kLeast8));
+  }
+  store_packed<PD, GD, MASTER, WHOLE>(t, block, W, p, m, u);
+  ms = mt * (1.f / kTop8);
+  us = ut * (1.f / kTop8);
+  return true;
+}
+
+// What step_usual left of a warp's blocks of a chunk (bit i of `done`: the i-th is not), those off the vectors' boundaries and the tensor's last.  A call, so that its registers are not the whole blocks'.
 template <int PD, int GD, bool MASTER>
-__device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* shared, int chunk) {
-  extern __shared__ uint4 adam_ring[];
-  WarpRing* const ring = reinterpret_cast<WarpRing*>(adam_ring) + (threadIdx.x >> 5);
+__device__ __noinline__ void packed_rest(const AdamTensor& t, const Step* shared, long long mine, long long end,
+                                         long long stop, unsigned done) {
   const Step s = *shared;
   const float shrink = 1.f - s.rate * t.decay;
-  const long long blocks = (t.n + kAdamBlock - 1) / kAdamBlock;
-  constexpr int warps = kAdamThreads / 32, per = kAdamPackedChunk / kAdamBlock;
-  const long long first = static_cast<long long>(chunk) * per;
-  const long long end = first + per < blocks ? first + per : blocks;
-  const long long whole = t.head < 0 ? 0 : t.n / kAdamBlock;  // blocks that come in whole vectors
-  long long b = first + (threadIdx.x >> 5);
-  const long long stop = end < whole ? end : whole;
-  // blocks b, b + 8, ... below stop
-  const int count = b < stop ? static_cast<int>((stop - b + warps - 1) / warps) : 0;
-#pragma unroll
-  for (int i = 0; i < kAhead - 1; ++i) {
-    if (i < count) copy_packed<PD, GD, MASTER>(t, b + i * warps, ring, i);
-    copy_commit();
-  }
   Packed<PD, GD, MASTER> r;
-  float ms = 0.f, vs = 0.f;  // of the next block
-  if (count > 0) ms = t.m_scale[b], vs = t.v_scale[b];
-  int slot = 0;
 #pragma unroll 1
-  for (int i = 0; i < count; ++i, b += warps) {
-    if (i + kAhead - 1 < count)
-      copy_packed<PD, GD, MASTER>(t, b + (kAhead - 1) * warps, ring, slot == 0 ? kAhead - 1 : slot - 1);
-    copy_commit();
-    copy_wait<kAhead - 1>();
-    read_packed(ring, slot, r);
-    r.ms = ms;
-    r.vs = vs;
-    if (i + 1 < count) ms = t.m_scale[b + warps], vs = t.v_scale[b + warps];
-    step_packed<PD, GD, MASTER, true>(t, s, shrink, b, W, r);
-    slot = slot + 1 == kAhead ? 0 : slot + 1;
+  for (int i = 0; i < kWarpBlocks && mine + i < end; ++i) {
+    const long long b = mine + i;
+    if (done >> i & 1) continue;
+    if (b < stop) {
+      load_packed(t, b, r);
+      step_any<PD, GD, MASTER, true>(t, s, shrink, b, W, r);
+    } else {
+      const long long left = t.n - (b * kAdamBlock + (threadIdx.x & 31) * W);
+      const int n = left < W ? (left > 0 ? static_cast<int>(left) : 0) : W;
+      load_packed_few(t, b, n, r);
+      // wherever a block lies, the same steps give the same bits
+      float ms, us;
+      if ((b + 1) * kAdamBlock <= t.n && step_usual<PD, GD, MASTER, false>(t, s, shrink, b, r, ms, us))
+        store_scales(t, b, ms, us);
+      else
+        step_any<PD, GD, MASTER, false>(t, s, shrink, b, n, r);
+    }
   }
-  copy_wait<0>();
+}
+
+// 8-bit states: each warp of the CTA takes kWarpBlocks neighbouring blocks of the chunk, two at a time.  Their
+// scales, a 32-byte sector of each array, are read and written at once: four bytes at a time the writes
+// alone cost a sixth of the time.  Lane i holds the i-th block's scale of m, lane 16 + i that of the root.
+template <int PD, int GD, bool MASTER>
+__device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* shared, int chunk) {
+  using Ring = Slot8<PD, GD, MASTER>;
+  extern __shared__ uint4 adam_ring[];
+  Ring* const ring = reinterpret_cast<Ring*>(reinterpret_cast<unsigned char*>(adam_ring) + (threadIdx.x >> 5) * kWarpRing);
+  constexpr int kAhead = kWarpRing / sizeof(Ring);
+  static_assert(kAhead >= 1 && sizeof(Ring) % 16 == 0 && kWarpRing % 16 == 0, "slots of the ring");
+  const int lane = threadIdx.x & 31;
+  const long long blocks = (t.n + kAdamBlock - 1) / kAdamBlock;
+  const long long mine = static_cast<long long>(chunk) * (kAdamPackedChunk / kAdamBlock) + (threadIdx.x >> 5) * kWarpBlocks;
+  const long long end = mine + kWarpBlocks < blocks ? mine + kWarpBlocks : blocks;
+  const long long whole = t.head < 0 ? 0 : t.n / kAdamBlock;  // blocks that come in whole vectors
+  const long long stop = end < whole ? end : whole;
+  if (mine >= end) return;
+  unsigned done = 0;
+  if (mine < stop) {
+    const Step s = *shared;
+    const float shrink = 1.f - s.rate * t.decay;
+    const int count = static_cast<int>(stop - mine);
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) {
+      if (2 * i < count) copy_pair<PD, GD, MASTER>(t, mine + 2 * i, stop, ring + i);
+      copy_commit();
+    }
+    const int j = lane & 15;
+    float* const scale_at = (lane < 16 ? t.m_scale : t.v_scale) + mine + j;
+    float scales = j < count ? *scale_at : 0.f;
+    int slot = 0;
 #pragma unroll 1
-  for (; b < end; b += warps) {
-    const long long left = t.n - (b * kAdamBlock + (threadIdx.x & 31) * W);
-    const int n = left < W ? (left > 0 ? static_cast<int>(left) : 0) : W;
-    load_packed_few(t, b, n, r);
-    step_packed<PD, GD, MASTER, false>(t, s, shrink, b, n, r);
+    for (int i = 0; i < count; i += 2) {
+      // lanes read what others copied: all of them are past the last reading of the slot, and through with
+      // their copies, before any goes on
+      __syncwarp();
+      if (i + 2 * (kAhead - 1) < count)
+        copy_pair<PD, GD, MASTER>(t, mine + i + 2 * (kAhead - 1), stop, ring + (slot == 0 ? kAhead - 1 : slot - 1));
+      copy_commit();
+      copy_wait<kAhead - 1>();
+      __syncwarp();
+#pragma unroll 1
+      for (int k = i; k < i + 2 && k < count; ++k) {
+        Packed<PD, GD, MASTER> r;
+        read_packed(ring + slot, k - i, r);
+        r.ms = __shfl_sync(0xffffffffu, scales, k);
+        r.vs = __shfl_sync(0xffffffffu, scales, 16 + k);
+        float ms, us;
+        if (step_usual<PD, GD, MASTER, true>(t, s, shrink, mine + k, r, ms, us)) {
+          done |= 1u << k;
+          if (j == k) scales = lane < 16 ? ms : us;
+        }
+      }
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+    __syncwarp();  // before the next chunk's copies
+    if (done >> j & 1) *scale_at = scales;
   }
+  if (done != (1u << (end - mine)) - 1) packed_rest<PD, GD, MASTER>(t, shared, mine, end, stop, done);
 }
 template <int PD, int GD>
 __device__ __forceinline__ void block_chunk(const AdamTensor& t, const Step* shared, int chunk) {
@@ -431,7 +562,7 @@ __device__ __forceinline__ void chunk_of(const AdamTensor& t, const Step* shared
 }
 
 template <int MOST, int BITS>
-__global__ void __launch_bounds__(kAdamThreads, kAdamResident<BITS>) adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
+__global__ void __launch_bounds__(BITS == 8 ? kPackedThreads : kAdamThreads, kAdamResident<BITS>) adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
   __shared__ Step shared;
   if (threadIdx.x == 0) shared = read_step(table.k);
   __syncthreads();
@@ -458,7 +589,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamResident<BITS>) adamw_kerne
 }  // namespace
 
 cudaError_t adamw_setup() {
-  const int bytes = kAdamThreads / 32 * sizeof(WarpRing);
+  const int bytes = kPackedThreads / 32 * kWarpRing;
   cudaError_t e = note_cuda(cudaFuncSetAttribute(adamw_kernel<kAdamFew, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   if (e == cudaSuccess)
     e = note_cuda(cudaFuncSetAttribute(adamw_kernel<kAdamMany, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
@@ -470,7 +601,7 @@ cudaError_t launch_adamw(const AdamTable<MOST>& table, int bits, int num_sms, cu
   const int most = (bits == 8 ? kAdamResident<8> : kAdamResident<32>) * num_sms;
   const int blocks = table.chunks < most ? table.chunks : most;
   if (bits == 8)
-    adamw_kernel<MOST, 8><<<blocks, kAdamThreads, kAdamThreads / 32 * sizeof(WarpRing), s>>>(table);
+    adamw_kernel<MOST, 8><<<blocks, kPackedThreads, kPackedThreads / 32 * kWarpRing, s>>>(table);
   else
     adamw_kernel<MOST, 32><<<blocks, kAdamThreads, 0, s>>>(table);
   return launch_result();

@@ -1810,7 +1810,7 @@ int adamw_checked(int64_t count, void* const* params, const void* const* grads, 
         !aligned(t.v, ss) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4) || !aligned(t.master, 4))
       return LLP_ERR_MISALIGNED;
     if (bits == 8)
-      t.head = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.master, 16) && aligned(t.m, 8) && aligned(t.v, 8) ? 0 : -1;
+      t.head = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.master, 16) && aligned(t.m, 16) && aligned(t.v, 16) ? 0 : -1;
     else
       t.head = static_cast<short>(adamw_head(t));
     all->push_back(t);
