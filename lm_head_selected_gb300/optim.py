@@ -56,6 +56,7 @@ def _scalar(t, name: str, dtype: torch.dtype, device: torch.device):
 # step over 12 tensors).
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
 _device_of, _contiguous, _dtype = torch.Tensor.get_device, torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+_shape = operator.attrgetter("shape")
 
 
 def _alike(tensors: list, sizes: List[int], index: int, dtype: torch.dtype) -> bool:
@@ -67,8 +68,30 @@ def _alike(tensors: list, sizes: List[int], index: int, dtype: torch.dtype) -> b
         return False
 
 
-def _addresses(tensors) -> array.array:
-    return array.array("Q", map(_data_ptr, tensors))
+def _codes(params: list, grads: list, index: int):
+    """The dtype codes of the parameters and of the gradients, and the parameters' sizes, after their checks."""
+    try:
+        p_code = [_DTYPE_CODES[d] for d in map(_dtype, params)]
+        g_code = [_DTYPE_CODES[d] for d in map(_dtype, grads)]
+        n = len(params)
+        if ((p_code == g_code or all(g == c or g == 1 for c, g in zip(p_code, g_code))) and
+                list(map(_shape, params)) == list(map(_shape, grads)) and
+                list(map(_device_of, params)).count(index) == list(map(_device_of, grads)).count(index) == n and
+                all(map(_contiguous, params)) and all(map(_contiguous, grads))):
+            return p_code, g_code, list(map(_numel, params))
+    except (TypeError, AttributeError, KeyError):
+        pass
+    for i, (p, g) in enumerate(zip(params, grads)):  # one of them will not do
+        if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
+            raise TypeError(f"params[{i}] and grads[{i}] must be tensors")
+        code, g_c = _DTYPE_CODES.get(p.dtype), _DTYPE_CODES.get(g.dtype)
+        if code is None or (g_c != code and g_c != 1):
+            raise TypeError(f"params[{i}] must be bf16, fp16 or fp32, grads[{i}] of the same dtype or fp32")
+        if p.get_device() != index or g.get_device() != index or not p.is_contiguous() or not g.is_contiguous():
+            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous, on cuda:{index}")
+        if g.shape != p.shape:
+            raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
+    raise ValueError("params and grads must be tensors")
 
 
 def _need_all(name: str, tensors, sizes: List[int], index: int, dtype: torch.dtype) -> List[torch.Tensor]:
@@ -119,55 +142,48 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
     _need_cuda(params[0], "params[0]")
     device = params[0].device
     index = device.index
-    p_code, g_code, sizes = [], [], []
-    for i, (p, g) in enumerate(zip(params, grads)):  # each its own dtype
-        if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
-            raise TypeError(f"params[{i}] and grads[{i}] must be tensors")
-        code, g_c = _DTYPE_CODES.get(p.dtype), _DTYPE_CODES.get(g.dtype)
-        if code is None or (g_c != code and g_c != 1):
-            raise TypeError(f"params[{i}] must be bf16, fp16 or fp32, grads[{i}] of the same dtype or fp32")
-        if p.get_device() != index or g.get_device() != index or not p.is_contiguous() or not g.is_contiguous():
-            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous, on {device}")
-        if g.shape != p.shape:
-            raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
-        p_code.append(code)
-        g_code.append(g_c)
-        sizes.append(p.numel())
-    p_ptr = _addresses(params)
-    starts = [a for a, n in zip(p_ptr, sizes) if n]
-    if len(set(starts)) != len(starts):
-        raise ValueError("a parameter is listed twice")
+    p_code, g_code, sizes = _codes(params, grads, index)
     packed = exp_avg_scale is not None
     dtype = CODE if packed else torch.float32
-    arrays = [p_ptr, _addresses(grads), _addresses(_need_all("exp_avg", exp_avg, sizes, index, dtype)),
-              _addresses(_need_all("exp_avg_sq", exp_avg_sq, sizes, index, dtype))]
+    # one array for all addresses and the sizes: a list after the other, `count` entries each
+    lists = [params, grads, _need_all("exp_avg", exp_avg, sizes, index, dtype),
+             _need_all("exp_avg_sq", exp_avg_sq, sizes, index, dtype)]
     if packed:
         blocks = [-(-n // BLOCK) for n in sizes]
-        arrays += [_addresses(_need_all(name, t, blocks, index, torch.float32)) for name, t in
-                   (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale))]
-    else:
-        arrays += [None, None]
-    if masters is None:
-        arrays.append(None)
-    else:
+        lists += [_need_all(name, t, blocks, index, torch.float32) for name, t in
+                  (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale))]
+    words = [a for t in lists for a in map(_data_ptr, t)]
+    starts = [a for a, n in zip(words, sizes) if n]
+    if len(set(starts)) != len(starts):
+        raise ValueError("a parameter is listed twice")
+    if masters is not None:
         masters = list(masters)
         if len(masters) != count:
             raise ValueError(f"masters must have {count} entries, got {len(masters)}")
         there = [i for i, t in enumerate(masters) if t is not None]
         _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
-        arrays.append(array.array("Q", [0 if t is None else t.data_ptr() for t in masters]))
-    weight_decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else weight_decay
-    decay = array.array("d", weight_decay)
+        words += [0 if t is None else t.data_ptr() for t in masters]
+    words = array.array("q", words + sizes)
+    codes = array.array("i", p_code + g_code)
+    one = isinstance(weight_decay, (int, float))
+    decay = array.array("d", [weight_decay] * count if one else weight_decay)
     if len(decay) != count or not all(map(math.isfinite, decay)):
         raise ValueError(f"weight_decay must be finite, one value or {count}")
-    arrays += [array.array("q", sizes), array.array("i", p_code), array.array("i", g_code), decay]
-    scalars = (_scalar(device_step, "device_step", torch.int64, device),
-               _scalar(device_lr, "device_lr", torch.float32, device),
-               _scalar(grad_scale, "grad_scale", torch.float32, device))
+    scalars = (None, None, None)
+    if device_step is not None or device_lr is not None or grad_scale is not None:
+        scalars = (_scalar(device_step, "device_step", torch.int64, device),
+                   _scalar(device_lr, "device_lr", torch.float32, device),
+                   _scalar(grad_scale, "grad_scale", torch.float32, device))
+    at, code_at, row = words.buffer_info()[0], codes.buffer_info()[0], 8 * count
+    n_lists = len(lists)
+    scale_at = (at + 4 * row, at + 5 * row) if packed else (None, None)
+    master_at = None if masters is None else at + n_lists * row
+    size_at = at + (n_lists + (masters is not None)) * row
 
     def call():
-        st = _lib.load().adamw_step(count, *[None if a is None else a.buffer_info()[0] for a in arrays],
-                                    8 if packed else 32, lr, beta1, beta2, eps, step, *scalars, _raw_stream(index))
+        st = _lib.load().adamw_step(count, at, at + row, at + 2 * row, at + 3 * row, *scale_at, master_at, size_at,
+                                    code_at, code_at + 4 * count, decay.buffer_info()[0], 8 if packed else 32, lr,
+                                    beta1, beta2, eps, step, *scalars, _raw_stream(index))
         _lib.check("adamw_step", st)
 
     if index == torch._C._cuda_getDevice():
