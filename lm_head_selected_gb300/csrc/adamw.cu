@@ -184,18 +184,6 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// One instruction each, within two units in the last place; subnormals count as 0.
-__device__ __forceinline__ float root_ftz(float v) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float inverse_ftz(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 // A lane's eight elements of a block with 8-bit states, as they lie in memory.
 template <int PD, int GD, bool MASTER>
 struct Packed {

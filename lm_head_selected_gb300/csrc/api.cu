@@ -1431,7 +1431,7 @@ static int gated_shapes(int dtype, int act, int64_t N, int64_t D, int64_t F) {
   if (!product_ok(N, D) || !product_ok(N, 4 * gated_pad(F)) || !product_ok(F, D)) return LLP_ERR_BAD_SHAPE;
   // every work-unit count and tile index must fit a 32-bit int
   const int64_t num_m = cdiv(N, llp::kUnitM), num_d = cdiv(D, llp::kTileN);
-  if (num_m * cdiv(F, llp::kTileN / 2) > kLim31 || num_m * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
+  if (num_m * cdiv(F, 64) > kLim31 || num_m * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
   if (2 * cdiv(F, llp::kUnitM) * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
   return LLP_OK;
 }
@@ -1473,8 +1473,9 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
     return e == cudaSuccess ? LLP_OK : fail_cuda(__LINE__);
   }
   const int kps = k_blocks_per_stage(D, false);
-  if (make_kmajor_maps(&tm_x, &tm_wg, x, w_gate, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
-      make_kmajor_maps(&tm_x, &tm_wu, x, w_up, N, D, F, llp::kBRows, kps, f16) != LLP_OK ||
+  const int cols = llp::gated_cols(N, F);
+  if (make_kmajor_maps(&tm_x, &tm_wg, x, w_gate, N, D, F, cols, kps, f16) != LLP_OK ||
+      make_kmajor_maps(&tm_x, &tm_wu, x, w_up, N, D, F, cols, kps, f16) != LLP_OK ||
       make_map(&tm_y, y, F, N, F * 2, 64, 32, f16) != LLP_OK)
     return fail_cuda(__LINE__);
   if (pre == nullptr)
@@ -1486,7 +1487,8 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
   p.D = static_cast<int>(D);
   p.F = static_cast<int>(F);
   p.num_m = static_cast<int>(cdiv(N, llp::kUnitM));
-  p.num_ft = static_cast<int>(cdiv(F, llp::kTileN / 2));
+  p.cols = cols;
+  p.num_ft = static_cast<int>(cdiv(F, cols));
   p.group_m = llp::kGroupM;
   p.keep = pre != nullptr;
   p.act = act;
@@ -1500,13 +1502,16 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
 
 namespace {
 struct GatedLayout {
-  size_t sched, dpre, total;
+  size_t sched, dpre, part, total;
+  int nseg;  // segments of grad_x's sum
 };
-GatedLayout gated_layout(int64_t N, int64_t F) {
+GatedLayout gated_layout(int64_t N, int64_t D, int64_t F) {
   Carver c;
   GatedLayout L;
   L.sched = c.take(llp::kNumSchedCounters * sizeof(int));
   L.dpre = c.take(static_cast<size_t>(N) * 2 * gated_pad(F) * 2);
+  L.nseg = llp::gated_segments(N, D, gated_pad(F));
+  L.part = L.nseg > 1 ? c.take(static_cast<size_t>(L.nseg) * N * D * sizeof(float)) : 0;
   L.total = c.off;
   return L;
 }
@@ -1514,7 +1519,7 @@ GatedLayout gated_layout(int64_t N, int64_t F) {
 
 size_t gated_linear_bwd_workspace_bytes(int64_t N, int64_t D, int64_t F) {
   if (N <= 0 || gated_shapes(llp::kDtypeBF16, 0, N, D, F) != LLP_OK) return 0;
-  return gated_layout(N, F).total;
+  return gated_layout(N, D, F).total;
 }
 
 int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const void* w_gate, const void* w_up,
@@ -1549,7 +1554,7 @@ int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const v
   if ((st = load_encode_fn()) != LLP_OK) return st;
   const bool f16 = dtype == llp::kDtypeF16;
   const int64_t P = gated_pad(F);
-  const GatedLayout L = gated_layout(N, F);
+  const GatedLayout L = gated_layout(N, D, F);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   int* const sched = reinterpret_cast<int*>(ws + L.sched);  // zeroed by the elementwise kernel
   uint8_t* const dpre = ws + L.dpre;
@@ -1576,8 +1581,9 @@ int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const v
     p.K = static_cast<int>(2 * P);
     p.num_m = static_cast<int>(cdiv(N, llp::kUnitM));
     p.num_d = static_cast<int>(cdiv(D, llp::kTileN));
-    p.nseg = 1;
-    p.kseg_blocks = static_cast<int>(2 * P / llp::kTileK);
+    p.nseg = L.nseg;
+    p.kseg_blocks = static_cast<int>(cdiv(2 * P / llp::kTileK, L.nseg));
+    p.part = L.nseg > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;
     p.half_blocks = static_cast<int>(P / llp::kTileK);
     p.out = static_cast<__nv_bfloat16*>(grad_x);
     p.err = dev->status_ptr;
@@ -1585,6 +1591,9 @@ int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const v
     p.sched = !force_static_schedule() && max_unit_kblocks(p) >= llp::kDynMinKBlocks ? sched + 0 : nullptr;
     if (make_map_grad_out(&tm_gx, p) != LLP_OK) return fail_cuda(__LINE__);
     if (llp::launch_gated_grad_x(tm_d, tm_wg, tm_wu, tm_gx, p, dev->gated, s) != cudaSuccess)
+      return fail_cuda(__LINE__);
+    if (p.nseg > 1 && llp::launch_segment_sum(p.part, p.nseg, static_cast<long long>(N) * D, p.out, dev->num_sms, s,
+                                              p.f16) != cudaSuccess)
       return fail_cuda(__LINE__);
   }
   if (want_w) {

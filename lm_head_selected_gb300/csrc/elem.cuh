@@ -92,6 +92,18 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float sum2(F2 a) { return __fadd_rn(a.x, a.y); }
 
+// One instruction each, within two units in the last place; subnormals count as 0.
+__device__ __forceinline__ float root_ftz(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float inverse_ftz(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int DT, int W>
 __device__ __forceinline__ void unpack2(const uint4& r, F2 (&v)[W / 2]) {
   float f[W];

@@ -26,22 +26,22 @@ namespace llp {
 
 namespace {
 
-constexpr int kGatedCols = kTileN / 2;  // columns of y in a tile
-
 struct GatedMaps {
   CUtensorMap a, b, c;  // x, Wg, y
   CUtensorMap b2, c2;   // Wu, the kept projections [2][N][F]
 };
 
+// COLS: columns of y in a tile, 128, or 64 where that fills the last wave of tiles better.
+template <int COLS>
 struct GatedFwdCfg : PlainOperands {
   using Maps = GatedMaps;
   using Params = GatedFwdParams;
   static constexpr bool A_MN = false;
   static constexpr bool B_MN = false;
   static constexpr bool PAIR = true;
-  static constexpr int BN = kTileN;
+  static constexpr int BN = 2 * COLS;
   static constexpr int A_ROWS = kTileM;
-  static constexpr int STAGES = kPairStages;
+  static constexpr int STAGES = COLS == 128 ? kPairStages : 8;  // of 32 or 24 KB
   static constexpr int EXTRA_SMEM = kEpiSmemBytes;
 
   struct RowState {};
@@ -73,7 +73,7 @@ struct GatedFwdCfg : PlainOperands {
     const int ft = r / gm;
     UnitInfo ui;
     ui.m0 = (grp * p.group_m + (r - ft * gm)) * kUnitM;
-    ui.n0 = ft * kGatedCols;
+    ui.n0 = ft * COLS;
     ui.ntiles = 1;
     ui.kb0 = 0;
     ui.nkb = (p.D + BK - 1) / BK;
@@ -95,7 +95,11 @@ struct GatedFwdCfg : PlainOperands {
   template <int ACT>
   static __device__ __forceinline__ void product(float (&g)[32], const float (&u)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) g[i] = gated_act<ACT>(g[i]) * u[i];
+    for (int i = 0; i < 32; i += 2) {
+      const F2 v = mul2(gated_act<ACT>(f2(g[i], g[i + 1])), f2(u[i], u[i + 1]));
+      g[i] = v.x;
+      g[i + 1] = v.y;
+    }
   }
 
   static __device__ __forceinline__ void tile(const Params& p, const UnitInfo& ui, int, int, int row, int lane,
@@ -104,7 +108,7 @@ struct GatedFwdCfg : PlainOperands {
     if (row0 >= p.N) return;  // this warp's rows are all past the end (warp-uniform)
     const bool f16 = p.f16 != 0;
 #pragma unroll 1
-    for (int q = 0; q < kGatedCols / 64; ++q) {  // 64-column slabs; rows and columns past the end are clipped
+    for (int q = 0; q < COLS / 64; ++q) {  // 64-column slabs; rows and columns past the end are clipped
       const int f0 = ui.n0 + 64 * q;
       if (f0 >= p.F) break;  // warp-uniform
       if (p.keep) {
@@ -114,7 +118,7 @@ struct GatedFwdCfg : PlainOperands {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[32];
-            tmem_load_32cols(taddr + kGatedCols * z + 64 * q + 32 * h, v);
+            tmem_load_32cols(taddr + COLS * z + 64 * q + 32 * h, v);
             put32(sbuf, lane, h, f16, v);
           }
           epi_slab_store_3d_to(es, es.map2, sbuf, f0, row0, z);
@@ -125,7 +129,7 @@ struct GatedFwdCfg : PlainOperands {
       for (int h = 0; h < 2; ++h) {
         float g[32], u[32];
         tmem_load_32cols(taddr + 64 * q + 32 * h, g);
-        tmem_load_32cols(taddr + kGatedCols + 64 * q + 32 * h, u);
+        tmem_load_32cols(taddr + COLS + 64 * q + 32 * h, u);
         if (p.act == kActSilu)
           product<kActSilu>(g, u);
         else if (p.act == kActGelu)
@@ -205,19 +209,19 @@ __global__ void __launch_bounds__(kDpreThreads) gated_dpre_kernel(const uint4* _
     uint4* const out = dpre + n * 2 * pitch + c;
     if (c < vecs) {
       const long long i = n * vecs + c;
-      float y[W], g[W], u[W];
-      Elem<DT>::unpack(__ldg(gy + i), y);
-      Elem<DT>::unpack(__ldg(gate + i), g);
-      Elem<DT>::unpack(__ldg(up + i), u);
+      F2 y[W / 2], g[W / 2], u[W / 2];
+      unpack2<DT, W>(__ldg(gy + i), y);
+      unpack2<DT, W>(__ldg(gate + i), g);
+      unpack2<DT, W>(__ldg(up + i), u);
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        float a, slope;
+      for (int k = 0; k < W / 2; ++k) {
+        F2 a, slope;
         gated_act_slope<ACT>(g[k], a, slope);
-        g[k] = y[k] * u[k] * slope;
-        u[k] = y[k] * a;
+        g[k] = mul2(mul2(y[k], u[k]), slope);
+        u[k] = mul2(y[k], a);
       }
-      out[0] = Elem<DT>::pack(g);
-      out[pitch] = Elem<DT>::pack(u);
+      out[0] = pack2<DT, W>(g);
+      out[pitch] = pack2<DT, W>(u);
     } else {
       out[0] = out[pitch] = make_uint4(0, 0, 0, 0);
     }
@@ -245,7 +249,8 @@ cudaError_t dpre(const GatedBwdParams& p, int blocks, cudaStream_t s) {
 }  // namespace
 
 cudaError_t gated_setup(GatedCaps* caps) {
-  cudaError_t e = note_cuda(setup_gemm<GatedFwdCfg>(&caps->fwd_groups));
+  cudaError_t e = note_cuda(setup_gemm<GatedFwdCfg<128>>(&caps->fwd_groups[0]));
+  if (e == cudaSuccess) e = note_cuda(setup_gemm<GatedFwdCfg<64>>(&caps->fwd_groups[1]));
   if (e == cudaSuccess) e = note_cuda(setup_gemm<GatedGradXCfg>(&caps->gx_groups));
   if (e == cudaSuccess) e = note_cuda(setup_gemm<GatedGradWCfg>(&caps->gw_groups));
   return e;
@@ -253,8 +258,9 @@ cudaError_t gated_setup(GatedCaps* caps) {
 
 cudaError_t launch_gated_fwd(const CUtensorMap& x, const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& y,
                              const CUtensorMap& pre, const GatedFwdParams& p, const GatedCaps& caps, cudaStream_t s) {
-  return launch_units<GatedFwdCfg>({x, wg, y, wu, pre}, p, static_cast<long long>(p.num_m) * p.num_ft, caps.fwd_groups,
-                                   s);
+  const long long units = static_cast<long long>(p.num_m) * p.num_ft;
+  return p.cols == 128 ? launch_units<GatedFwdCfg<128>>({x, wg, y, wu, pre}, p, units, caps.fwd_groups[0], s)
+                       : launch_units<GatedFwdCfg<64>>({x, wg, y, wu, pre}, p, units, caps.fwd_groups[1], s);
 }
 
 cudaError_t launch_gated_dpre(const GatedBwdParams& p, int num_sms, cudaStream_t s) {
@@ -267,8 +273,8 @@ cudaError_t launch_gated_dpre(const GatedBwdParams& p, int num_sms, cudaStream_t
 cudaError_t launch_gated_grad_x(const CUtensorMap& dpre, const CUtensorMap& wg, const CUtensorMap& wu,
                                 const CUtensorMap& gx, const GatedGradXParams& p, const GatedCaps& caps,
                                 cudaStream_t s) {
-  return launch_units<GatedGradXCfg>({dpre, wg, gx, wu}, p, static_cast<long long>(p.num_m) * p.num_d, caps.gx_groups,
-                                     s);
+  const long long units = static_cast<long long>(p.nseg) * p.num_m * p.num_d;
+  return launch_units<GatedGradXCfg>({dpre, wg, gx, wu}, p, units, caps.gx_groups, s);
 }
 
 cudaError_t launch_gated_grad_w(const CUtensorMap& dpre, const CUtensorMap& x, const CUtensorMap& gwg,

@@ -7,11 +7,40 @@ namespace llp {
 
 // Resident CTA pairs of each GEMM.
 struct GatedCaps {
-  int fwd_groups, gx_groups, gw_groups;
+  int fwd_groups[2];  // of 128 and of 64 columns of y to a tile
+  int gx_groups, gw_groups;
 };
+
+constexpr int kGatedPairs = 76;  // CTA pairs that the choices below are made for
+
+// Columns of y to a tile: 64 where tiles of 128 leave more of the pairs idle in their last wave than narrow
+// tiles cost (their MMAs read the same rows of x for half the columns).
+inline int gated_cols(long long N, long long F) {
+  const long long m = (N + kUnitM - 1) / kUnitM;
+  const long long wide = (m * ((F + 127) / 128) + kGatedPairs - 1) / kGatedPairs;
+  const long long narrow = (m * ((F + 63) / 64) + kGatedPairs - 1) / kGatedPairs;
+  return narrow * 75 < wide * 100 ? 64 : 128;
+}
+
+// Segments of the long sum of grad_x: with fewer tiles than pairs, the K blocks are split among pairs, and
+// the segments' fp32 partials are summed in ascending order.  In units of a K block's time on a pair
+// (0.27 us): a segment's blocks and about 8 for its start and end, for each wave; the partials' way
+// through memory at 5 TB/s.
+inline int gated_segments(long long N, long long D, long long F_pad) {
+  const long long tiles = ((N + kUnitM - 1) / kUnitM) * ((D + kTileN - 1) / kTileN), blocks = 2 * F_pad / kTileK;
+  long long best = 1, best_cost = ((tiles + kGatedPairs - 1) / kGatedPairs) * (blocks + 8);
+  for (long long n = 2; n <= 16 && n * tiles <= 2 * kGatedPairs; ++n) {
+    const long long per = (blocks + n - 1) / n;
+    if ((blocks + per - 1) / per != n) continue;
+    const long long cost = ((tiles * n + kGatedPairs - 1) / kGatedPairs) * (per + 8) + 16 + n * N * D * 8 / 1350000;
+    if (cost < best_cost) best = n, best_cost = cost;
+  }
+  return static_cast<int>(best);
+}
 
 struct GatedFwdParams {
   int N, D, F;
+  int cols;  // of y to a tile, 128 or 64
   int num_m, num_ft, group_m;
   int keep;  // the projections are stored too
   int act;

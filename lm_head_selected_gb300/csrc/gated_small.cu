@@ -36,7 +36,11 @@ __host__ __device__ inline int gs_stage_bytes(const GatedSmallParams& p) { retur
 template <int ACT>
 __device__ __forceinline__ void product32(float (&g)[32], const float (&u)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) g[i] = gated_act<ACT>(g[i]) * u[i];
+  for (int i = 0; i < 32; i += 2) {
+    const F2 v = mul2(gated_act<ACT>(f2(g[i], g[i + 1])), f2(u[i], u[i + 1]));
+    g[i] = v.x;
+    g[i + 1] = v.y;
+  }
 }
 
 __device__ __forceinline__ uint16_t to16(bool f16, float x) {
