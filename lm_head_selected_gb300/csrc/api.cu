@@ -270,6 +270,23 @@ int make_map_part(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows
   return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
 }
 
+// One map over two row-major 16-bit matrices [rows][cols] of the same shape, `apart` bytes from the first
+// to the second: box {64, box_rows, 2, box_chunks} of {64, rows, 2, cols / 64} with chunks (cols a
+// multiple of 64), else {64, box_rows, 2} of {cols, rows, 2}.  Nothing between the two is reached.
+int make_map_two(CUtensorMap* m, const void* first, uint64_t apart, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                 uint32_t box_chunks, bool chunked, bool f16) {
+  cuuint64_t dims[4] = {chunked ? 64 : cols, rows, 2, cols / 64};
+  cuuint64_t strides[3] = {cols * 2, apart, 128};
+  cuuint32_t box[4] = {64, box_rows, 2, box_chunks};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              chunked ? 4 : 3, const_cast<void*>(first), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) g_last_driver_result = static_cast<int>(r);
+  return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
+}
+
 // Output map of a stack of `planes` 16-bit matrices [rows][cols], box {64, 32, 1}: a store clips at
 // `rows` inside each.
 int make_map_planes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t planes, bool f16) {
@@ -1431,7 +1448,7 @@ static int gated_shapes(int dtype, int act, int64_t N, int64_t D, int64_t F) {
   if (!product_ok(N, D) || !product_ok(N, 4 * gated_pad(F)) || !product_ok(F, D)) return LLP_ERR_BAD_SHAPE;
   // every work-unit count and tile index must fit a 32-bit int
   const int64_t num_m = cdiv(N, llp::kUnitM), num_d = cdiv(D, llp::kTileN);
-  if (num_m * cdiv(F, 64) > kLim31 || num_m * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
+  if (num_m * cdiv(F, llp::kTileN / 2) > kLim31 || num_m * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
   if (2 * cdiv(F, llp::kUnitM) * num_d > kLim31) return LLP_ERR_BAD_SHAPE;
   return LLP_OK;
 }
@@ -1450,13 +1467,21 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
   const bool f16 = dtype == llp::kDtypeF16;
   CUtensorMap tm_x, tm_wg, tm_wu, tm_y, tm_pre;
   llp::GatedSmallParams q = {};
-  if (N <= llp::kSmallGatedMaxN &&
-      llp::gated_small_plan(static_cast<int>(N), static_cast<int>(D), static_cast<int>(F), dev->num_sms, &q)) {
+  // one map may reach both weights where they do not start at one place (nor 2^40 bytes apart)
+  const uintptr_t at_g = reinterpret_cast<uintptr_t>(w_gate), at_u = reinterpret_cast<uintptr_t>(w_up);
+  const uint64_t apart = at_u > at_g ? at_u - at_g : at_g - at_u;
+  q.joint = apart > 0 && apart < (uint64_t(1) << 40) ? 1 : 0;
+  q.up_first = at_u < at_g ? 1 : 0;
+  if (llp::gated_small_plan(static_cast<int>(N), static_cast<int>(D), static_cast<int>(F), dev->num_sms, &q)) {
     // few tokens: the weights' rows on the MMA's M side
     q.chunked = (D % 64) == 0 ? 1 : 0;
     const void* const base[3] = {w_gate, w_up, x};
     CUtensorMap* const map[3] = {&tm_wg, &tm_wu, &tm_x};
-    for (int i = 0; i < 3; ++i) {
+    if (q.joint && make_map_two(&tm_wg, q.up_first ? w_up : w_gate, apart, D, F, static_cast<uint32_t>(q.R),
+                                static_cast<uint32_t>(q.c), q.chunked != 0, f16) != LLP_OK)
+      return fail_cuda(__LINE__);
+    if (q.joint) tm_wu = tm_wg;  // not loaded through
+    for (int i = q.joint ? 2 : 0; i < 3; ++i) {
       const int64_t rows = i == 2 ? N : F;
       const uint32_t box = static_cast<uint32_t>(i == 2 ? q.BN : q.R);
       const int r = q.chunked ? make_map_chunked(map[i], base[i], D, rows, D * 2, box, static_cast<uint32_t>(q.c), f16)

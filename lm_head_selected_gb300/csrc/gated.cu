@@ -1,8 +1,8 @@
 // Gated linear layer y = act(x Wg^T) * (x Wu^T) and its gradient, on the tcgen05 core.
 //
-// Forward: one GEMM over both projections.  A CTA pair's 256 x 256 tile has 128 columns of each:
+// Forward: one GEMM over both projections.  A CTA pair's 256 x 256 (or 256 x 128) tile has 128 (64) columns of each:
 // of the tile's B rows the even CTA loads its half from Wg and the odd CTA its half from Wu, so
-// that the accumulator's columns 0..127 are the gate and 128..255 the up projection of the same
+// that the accumulator's first half is the gate and its second half the up projection of the same
 // 128 columns of y, and every thread of the epilogue holds both factors of its row.  The
 // projections never leave the SM unless they are kept for the gradient; y is formed from the
 // fp32 accumulators.
@@ -31,7 +31,7 @@ struct GatedMaps {
   CUtensorMap b2, c2;   // Wu, the kept projections [2][N][F]
 };
 
-// COLS: columns of y in a tile, 128, or 64 where that fills the last wave of tiles better.
+// COLS: columns of y in a tile, 128 or 64.
 template <int COLS>
 struct GatedFwdCfg : PlainOperands {
   using Maps = GatedMaps;

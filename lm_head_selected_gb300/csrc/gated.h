@@ -5,21 +5,19 @@
 
 namespace llp {
 
+constexpr int kGatedPairs = 76;  // CTA pairs that the choices below are made for
+
 // Resident CTA pairs of each GEMM.
 struct GatedCaps {
   int fwd_groups[2];  // of 128 and of 64 columns of y to a tile
   int gx_groups, gw_groups;
 };
 
-constexpr int kGatedPairs = 76;  // CTA pairs that the choices below are made for
-
-// Columns of y to a tile: 64 where tiles of 128 leave more of the pairs idle in their last wave than narrow
-// tiles cost (their MMAs read the same rows of x for half the columns).
+// Columns of y to a tile: 64 where all of those tiles run at once.  They take 0.73 of the time of 128 (512
+// tokens or fewer, 2048 x 4096: 12.5 us, 16.5 with 128); with more waves they lose (4096 x 4096 x 8192
+// 383 us, 288 with 128).
 inline int gated_cols(long long N, long long F) {
-  const long long m = (N + kUnitM - 1) / kUnitM;
-  const long long wide = (m * ((F + 127) / 128) + kGatedPairs - 1) / kGatedPairs;
-  const long long narrow = (m * ((F + 63) / 64) + kGatedPairs - 1) / kGatedPairs;
-  return narrow * 75 < wide * 100 ? 64 : 128;
+  return ((N + kUnitM - 1) / kUnitM) * ((F + 63) / 64) <= kGatedPairs ? 64 : 128;
 }
 
 // Segments of the long sum of grad_x: with fewer tiles than pairs, the K blocks are split among pairs, and
@@ -40,7 +38,7 @@ inline int gated_segments(long long N, long long D, long long F_pad) {
 
 struct GatedFwdParams {
   int N, D, F;
-  int cols;  // of y to a tile, 128 or 64
+  int cols;  // of y to a tile
   int num_m, num_ft, group_m;
   int keep;  // the projections are stored too
   int act;
@@ -49,13 +47,23 @@ struct GatedFwdParams {
 };
 
 // The forward of few tokens, weights on the MMA's M side (gated_small.cu).
-constexpr int kSmallGatedMaxN = 128;
 constexpr int kGatedSmallSmem = 232448;
+
+// Most tokens that it takes.  The CTA-pair tiles of 128 columns take one time whatever the batch up to 256
+// tokens, which is short where they all run at once and only half the pairs have one: 2048 x 4096 12.5 us,
+// this kernel 12.2 of 32 tokens, 13.6 of 64; 2048 x 8192 19.0, 17.8 of 96 and 20.0 of 128; with a second
+// wave 2688 x 10752 36.7, 34.9 of 224 and 37.9 of 256.
+inline int gated_small_most(long long F) {
+  const long long tiles = (F + 127) / 128;
+  return tiles <= kGatedPairs / 2 ? 32 : tiles <= kGatedPairs ? 96 : 224;
+}
 
 struct GatedSmallParams {
   int N, D, F;
   int BN;      // MMA N: N rounded up to 16
   int R;       // rows of each weight to a CTA (height of the weights' boxes)
+  int joint;   // both weights' rows in one MMA: asked for by the caller, kept where R is at most 64
+  int up_first;  // of the joint map: Wu lies below Wg in memory
   int units;   // of R rows
   int c;       // K blocks of a stage
   int stages;
@@ -66,7 +74,7 @@ struct GatedSmallParams {
   uint16_t* pre;  // [2][N][F], or nullptr
   unsigned int* err;
 };
-// Fills all up to tmem_cols; false when the batch is too large for the kernel.
+// Fills all up to tmem_cols, from joint as asked for; false when the batch is too large for the kernel.
 bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p);
 cudaError_t gated_small_setup();
 cudaError_t launch_gated_small(const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& x,

@@ -1,4 +1,4 @@
-// The gated linear layer's forward for few tokens (at most kSmallGatedMaxN), with the operands of the
+// The gated linear layer's forward for few tokens (gated_small_most), with the operands of the
 // contraction swapped:
 //
 //     gate^T [F, N] = Wg [F, D] . x^T [D, N],   up^T likewise
@@ -9,6 +9,12 @@
 // 72), one MMA each per 16-deep step into two accumulators, so that lane j of one holds the gate and of
 // the other the up projection of one column of y, for every token.  An MMA reads 128 rows: what lies
 // behind the R-th belongs to other operands and feeds only accumulator lanes that no one reads.
+//
+// Where R is at most 64 (JOINT) both weights' rows go into one MMA, lanes 0..R-1 and R..2R-1: an MMA of few
+// tokens takes about 80 cycles, mostly to read its 128 rows, and with two of them a step the K loop took
+// 0.34 us per K block whatever the weights' size (2048 x 4096 of one token 15.6 us; together 10.6).
+// One tensor map reaches both: its third dimension steps from one weight to the other.
+// The epilogue then brings the two halves together through shared memory.
 //
 // An SM issues only about four tensor copies per microsecond whatever their size, so a stage is c K blocks
 // of 64 (c = 1, 2 or 4) and comes as three 3-D copies: the gate's rows, the up projection's, x (in L2).
@@ -52,6 +58,9 @@ __device__ __forceinline__ uint16_t to16(bool f16, float x) {
   return *reinterpret_cast<const uint16_t*>(&b);
 }
 
+constexpr int kXchPitch = 33;  // floats of a row of the JOINT epilogue's exchange
+
+template <bool JOINT>
 __global__ void __launch_bounds__(kGsThreads, 1)
     gated_small_kernel(const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_u,
                        const __grid_constant__ CUtensorMap tm_x, const GatedSmallParams p) {
@@ -112,7 +121,18 @@ __global__ void __launch_bounds__(kGsThreads, 1)
           const uint32_t base = smem_u32(ring + st * stage_bytes);
           const uint32_t up = base + p.R * 128 * p.c, x = up + p.R * 128 * p.c;
           mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(stage_bytes));
-          if (p.chunked) {
+          if (JOINT) {
+            if (p.chunked) {
+              tma_load_4d(base, &tm_g, &full[st], 0, u * p.R, 0, g * p.c, pol_w);
+              tma_load_3d(x, &tm_x, &full[st], 0, 0, g * p.c, pol_x);
+            } else {
+              for (int c = 0; c < p.c; ++c) {
+                const int kx = (g * p.c + c) * 64;
+                tma_load_3d(base + c * 2 * p.R * 128, &tm_g, &full[st], kx, u * p.R, 0, pol_w);
+                tma_load_2d(x + c * p.BN * 128, &tm_x, &full[st], kx, 0, pol_x);
+              }
+            }
+          } else if (p.chunked) {
             tma_load_3d(base, &tm_g, &full[st], 0, u * p.R, g * p.c, pol_w);
             tma_load_3d(up, &tm_u, &full[st], 0, u * p.R, g * p.c, pol_w);
             tma_load_3d(x, &tm_x, &full[st], 0, 0, g * p.c, pol_x);
@@ -149,6 +169,14 @@ __global__ void __launch_bounds__(kGsThreads, 1)
           tc_fence_after_sync();
           const uint32_t base = smem_u32(ring + st * stage_bytes);
           for (int c = 0; c < p.c; ++c) {
+            if (JOINT) {
+              const uint64_t wd = make_smem_desc_sw128(base + c * 2 * p.R * 128, 16, 1024);
+              const uint64_t xd = make_smem_desc_sw128(base + 2 * p.c * p.R * 128 + c * p.BN * 128, 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_f32(tmem_base, wd + 2 * kk, xd + 2 * kk, idesc, (g > 0 || c > 0 || kk > 0) ? 1u : 0u);
+              continue;
+            }
             const uint64_t gd = make_smem_desc_sw128(base + c * p.R * 128, 16, 1024);
             const uint64_t ud = make_smem_desc_sw128(base + (p.c + c) * p.R * 128, 16, 1024);
             const uint64_t xd = make_smem_desc_sw128(base + 2 * p.c * p.R * 128 + c * p.BN * 128, 16, 1024);
@@ -177,8 +205,55 @@ __global__ void __launch_bounds__(kGsThreads, 1)
     const bool f16 = p.f16 != 0;
     uint32_t acc_ph = 0;
     for (int u = blockIdx.x; u < p.units; u += gridDim.x, acc_ph ^= 1u) {
-      if (!mbar_wait(tmem_full, acc_ph, abort_flag, p.err, kDevTimeoutTmemFull)) break;
+      bool ok = mbar_wait(tmem_full, acc_ph, abort_flag, p.err, kDevTimeoutTmemFull);
+      // the four warps meet at barriers below: all of them go on, or none
+      if (JOINT) ok = named_bar_and(1, 128, ok);
+      if (!ok) break;
       tc_fence_after_sync();
+      if (JOINT) {
+        // the ring is free: this CTA has one unit, and its MMAs are through
+        float* const xch = reinterpret_cast<float*>(ring);
+        const int tid = threadIdx.x - 64;  // warps 2..5
+        const int r = tid & 63, half = tid >> 6;
+        const long long f = static_cast<long long>(u) * p.R + r;
+        const bool mine = r < p.R && f < p.F;
+        const float* const gate_row = xch + (p.up_first ? p.R + r : r) * kXchPitch;
+        const float* const up_row = xch + (p.up_first ? r : p.R + r) * kXchPitch;
+        for (int n0 = 0; n0 < p.N; n0 += 32) {
+          if ((warp & 3) * 32 < 2 * p.R) {  // warp-uniform
+            float v[32];
+            tmem_load_32cols(taddr + n0, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) xch[row * kXchPitch + j] = v[j];
+          }
+          named_bar_sync(1, 128);
+          if (mine) {
+#pragma unroll 1
+            for (int j = 16 * half; j < 16 * half + 16 && n0 + j < p.N; j += 2) {
+              const bool two = n0 + j + 1 < p.N;
+              const F2 g = f2(gate_row[j], gate_row[j + 1]), v = f2(up_row[j], up_row[j + 1]);
+              const long long at = static_cast<long long>(n0 + j) * p.F + f;
+              if (p.pre != nullptr) {
+                uint16_t* const up = p.pre + static_cast<long long>(p.N) * p.F;
+                p.pre[at] = to16(f16, g.x);
+                up[at] = to16(f16, v.x);
+                if (two) {
+                  p.pre[at + p.F] = to16(f16, g.y);
+                  up[at + p.F] = to16(f16, v.y);
+                }
+              }
+              const F2 a = p.act == kActSilu   ? gated_act<kActSilu>(g)
+                           : p.act == kActGelu ? gated_act<kActGelu>(g)
+                                               : gated_act<kActGeluTanh>(g);
+              const F2 y = mul2(a, v);
+              p.y[at] = to16(f16, y.x);
+              if (two) p.y[at + p.F] = to16(f16, y.y);
+            }
+          }
+          named_bar_sync(1, 128);
+        }
+        break;
+      }
       const long long f = static_cast<long long>(u) * p.R + row;
       const bool mine = row < p.R && f < p.F;
       if ((warp & 3) * 32 < p.R) {  // warp-uniform
@@ -225,7 +300,7 @@ __global__ void __launch_bounds__(kGsThreads, 1)
 
 // What an MMA reads behind the last stage's last rows.
 int gs_slack(const GatedSmallParams& p) {
-  const int behind = p.R * 128 + p.c * p.BN * 128;
+  const int behind = (p.joint ? 2 : 1) * p.R * 128 + p.c * p.BN * 128;
   return behind < 16384 ? 16384 - behind : 0;
 }
 int gs_smem(const GatedSmallParams& p) { return 2048 + p.stages * gs_stage_bytes(p) + gs_slack(p); }
@@ -233,7 +308,7 @@ int gs_smem(const GatedSmallParams& p) { return 2048 + p.stages * gs_stage_bytes
 }  // namespace
 
 bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p) {
-  if (N < 1 || N > kSmallGatedMaxN) return false;
+  if (N < 1 || N > gated_small_most(F)) return false;
   p->N = N;
   p->D = D;
   p->F = F;
@@ -243,6 +318,7 @@ bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p) {
   const long long rows = (F + sms * waves - 1) / (sms * waves);
   p->R = static_cast<int>((rows + 7) / 8 * 8);
   p->units = (F + p->R - 1) / p->R;
+  if (p->R > 64) p->joint = 0;
   // K blocks per stage: as few as make a stage of 40 KB, at most four, and no more than there are
   const int blocks = (D + 63) / 64;
   p->c = 1;
@@ -256,19 +332,26 @@ bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p) {
     }
   }
   int cols = 32;
-  while (cols < 2 * gs_acc_cols(p->BN)) cols *= 2;
+  while (cols < (p->joint ? 1 : 2) * gs_acc_cols(p->BN)) cols *= 2;
   p->tmem_cols = cols;
   return p->stages >= 2;
 }
 
 cudaError_t gated_small_setup() {
-  return note_cuda(cudaFuncSetAttribute(gated_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedSmallSmem));
+  const cudaError_t e = note_cuda(cudaFuncSetAttribute(gated_small_kernel<false>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedSmallSmem));
+  return e != cudaSuccess ? e
+                          : note_cuda(cudaFuncSetAttribute(gated_small_kernel<true>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedSmallSmem));
 }
 
 cudaError_t launch_gated_small(const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& x,
                                const GatedSmallParams& p, int num_sms, cudaStream_t s) {
   const int grid = p.units < num_sms ? p.units : num_sms;
-  gated_small_kernel<<<grid, kGsThreads, gs_smem(p), s>>>(wg, wu, x, p);
+  if (p.joint)
+    gated_small_kernel<true><<<grid, kGsThreads, gs_smem(p), s>>>(wg, wu, x, p);
+  else
+    gated_small_kernel<false><<<grid, kGsThreads, gs_smem(p), s>>>(wg, wu, x, p);
   return launch_result();
 }
 

@@ -171,6 +171,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
+                                            int z, int w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // TMA stores (shared -> global), tracked per thread with bulk groups.  The
 // tensor map clips rows / columns outside the tensor, so partial tiles are safe.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -422,6 +431,19 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 // Named barrier among the epilogue warps only.
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+// The same, and whether `ok` held in all of its threads: one answer for all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(all)
+      : "r"(id), "r"(nthreads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
 }
 
 }  // namespace llp

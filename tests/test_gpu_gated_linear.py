@@ -161,6 +161,32 @@ def test_weights_as_halves_of_one_tensor():
     assert torch.equal(llp.gated_linear_fwd(x, both[:F], both[F:]), llp.gated_linear_fwd(x, wg, wu))
 
 
+@pytest.mark.parametrize("N", [3, 40, 300])
+@pytest.mark.parametrize("D,F", [(72, 136), (256, 8192), (256, 12288)])
+def test_weights_anywhere(N, D, F):
+    """The same weight twice, and the up projection's below the gate's in memory."""
+    x, wg, wu, _ = inputs(N, D, F, torch.bfloat16)
+    both = torch.cat([wu, wg])
+    y, pre = llp.gated_linear_fwd(x, both[F:], both[:F], keep=True)
+    want, want_pre = llp.gated_linear_fwd(x, wg, wu, keep=True)
+    assert torch.equal(y, want) and torch.equal(pre, want_pre)
+    y, pre = llp.gated_linear_fwd(x, wg, wg, keep=True)
+    assert torch.equal(pre[0], pre[1]) and torch.equal(pre[0], want_pre[0])
+    rows = slice(0, 3)
+    check_forward(y[rows], pre[:, rows], x[rows], wg, wg, "silu")
+
+
+@pytest.mark.parametrize("F", [64, 2048, 9728, 9736, 19464])
+def test_rows_of_every_height_do_not_depend_on_the_batch(F):
+    """Weights' rows spread over the SMs in boxes of 8 to 128."""
+    x, wg, wu, _ = inputs(300, 192, F, torch.float16)
+    whole, pre = llp.gated_linear_fwd(x, wg, wu, "gelu", keep=True)
+    check_forward(whole[:4], pre[:, :4], x[:4], wg, wu, "gelu")
+    for N in (1, 33, 128):
+        y, p = llp.gated_linear_fwd(x[7:7 + N], wg, wu, "gelu", keep=True)
+        assert torch.equal(y, whole[7:7 + N]) and torch.equal(p, pre[:, 7:7 + N])
+
+
 def test_many_tokens():
     """Tickets, double K blocks and several waves of tiles; sampled rows and columns."""
     N, D, F = 9000, 512, 1160
