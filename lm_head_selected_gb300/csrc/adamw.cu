@@ -18,7 +18,7 @@ constexpr int kPackedThreads = 128;  // and in 8
 constexpr int kWarpBlocks = kAdamPackedChunk / kAdamBlock / (kPackedThreads / 32);  // to a warp of a chunk
 static_assert(kAdamPackedChunk % (2 * kAdamBlock * (kPackedThreads / 32)) == 0 && kWarpBlocks <= 16, "a lane for each scale");
 template <int BITS>
-constexpr int kAdamResident = BITS == 8 ? 5 : 4;  // CTAs to an SM: 96 or 64 registers per thread
+constexpr int kAdamResident = BITS == 8 ? 4 : 2;  // CTAs to an SM
 constexpr int W = 8;  // elements of a thread's step
 constexpr float kTop8 = 448.f;              // largest e4m3 value
 constexpr float kLeast8 = 0.001953125f;     // smallest above 0, 2^-9
@@ -204,7 +204,7 @@ struct Slot8 {
   uint2 m[2][32];
   uint2 v[2][32];
 };
-constexpr int kWarpRing = 9216;  // bytes of a warp's ring: three slots of 16-bit parameters and gradients, one or two of others
+constexpr int kWarpRing = 12352;  // bytes of a warp's ring: four slots of 16-bit parameters and gradients, one or two of others
 
 // The pair's blocks below `stop`.
 template <int PD, int GD, bool MASTER>

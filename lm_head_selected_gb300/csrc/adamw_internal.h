@@ -6,7 +6,7 @@
 namespace llp {
 
 constexpr int kAdamBlock = 256;   // values of an 8-bit state that share a scale
-constexpr int kAdamChunk = 8192;         // elements that a CTA takes at a time, states in 32 bits
+constexpr int kAdamChunk = 4096;         // elements that a CTA takes at a time, states in 32 bits
 constexpr int kAdamPackedChunk = 16384;  // and in 8
 
 // One tensor, as the kernel's parameters hold it.
