@@ -17,11 +17,13 @@
  * elements of a tensor share: m, and the root of v, whose range is half as many
  * binades.  The step computes with the fp32 values and stores
  *
- *     scale = max |m| / 448,   code = e4m3(m / scale)         (all 0 where max |m| is 0)
+ *     scale = max |m| * (1 / 448),   code = e4m3(m / scale)         (all 0 where max |m| is 0)
  *
  * and the same of sqrt(v), of which no value above 0 is stored as 0: at an element
  * whose gradients are far below its block's largest, a step divides by no less than
- * the smallest code (2^-9 scale).  A gradient that is not finite spoils its
+ * the smallest code (2^-9 scale).  The moments and the scales are rounded operation
+ * by operation, so that the codes are those of the formulas in fp32, next to the
+ * border between two codes too.  A gradient that is not finite spoils its
  * element, in 8 bits its block.
  *
  * Conventions as in linear_logp.h: device pointers in host arrays of `count`

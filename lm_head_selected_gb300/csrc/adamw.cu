@@ -166,6 +166,9 @@ __device__ __forceinline__ F2 codes_to_f2(uint32_t word, int half) {
 __device__ __forceinline__ uint32_t f2_to_codes(F2 v) {
   return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint2 all_codes(const F2 (&v)[W / 2]) {
+  return make_uint2(f2_to_codes(v[0]) | f2_to_codes(v[1]) << 16, f2_to_codes(v[2]) | f2_to_codes(v[3]) << 16);
+}
 
 // The larger of two magnitudes; NaN if one is.
 __device__ __forceinline__ float nan_max(float a, float b) {
@@ -328,11 +331,9 @@ __device__ __forceinline__ void unpack_packed(const Packed<PD, GD, MASTER>& r, F
 
 // n of the lane's elements (W where WHOLE) and their codes.
 template <int PD, int GD, bool MASTER, bool WHOLE>
-__device__ __forceinline__ void store_packed(const AdamTensor& t, long long block, int n, const F2 (&p)[W / 2],
-                                             const F2 (&m)[W / 2], const F2 (&u)[W / 2]) {
+__device__ __forceinline__ void store_packed(const AdamTensor& t, long long block, int n, const F2 (&p)[W / 2], uint2 m8,
+                                             uint2 v8) {
   using P = typename Elem<PD>::T;
-  const uint2 m8 = make_uint2(f2_to_codes(m[0]) | f2_to_codes(m[1]) << 16, f2_to_codes(m[2]) | f2_to_codes(m[3]) << 16);
-  const uint2 v8 = make_uint2(f2_to_codes(u[0]) | f2_to_codes(u[1]) << 16, f2_to_codes(u[2]) | f2_to_codes(u[3]) << 16);
   const long long at = block * kAdamBlock + (threadIdx.x & 31) * W;
   P* const out = static_cast<P*>(t.p) + at;
   unsigned char* const mc = static_cast<unsigned char*>(t.m) + at;
@@ -367,7 +368,23 @@ __device__ __forceinline__ void store_scales(const AdamTensor& t, long long bloc
 // The block's largest of non-negative values; NaN, whose bits are above infinity's, wins.
 __device__ __forceinline__ float warp_top(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
 
-// A block's step for any values.  The warp's lanes share the two maxima; all of them must come here.
+// a b + c d, each operation rounded by itself.  The sums are scalar: a packed product and a packed sum were
+// contracted into one operation, with the instructions' explicit rounding too (seen in the results).
+__device__ __forceinline__ F2 sum_of_products(F2 a, F2 b, F2 c, F2 d) {
+  const F2 u = mul2(a, b), v = mul2(c, d);
+  return f2(__fadd_rn(u.x, v.x), __fadd_rn(u.y, v.y));
+}
+__device__ __forceinline__ F2 first_moment(const Step& s, F2 code, float scale, F2 g) {
+  return sum_of_products(mul2(code, f2(scale)), f2(s.b1), g, f2(s.c1));
+}
+__device__ __forceinline__ F2 second_moment(const Step& s, F2 code, float scale, F2 g) {
+  const F2 root = mul2(code, f2(scale));
+  return sum_of_products(mul2(root, root), f2(s.b2), mul2(g, g), f2(s.c2));
+}
+
+// A block's step for any values, each operation rounded by itself: a stored code then is what the
+// definition in fp32 gives, which a value next to the border between two codes would otherwise miss by
+// an eighth.  The warp's lanes share the two maxima; all of them must come here.
 template <int PD, int GD, bool MASTER, bool WHOLE>
 __device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, float shrink, long long block, int n,
                                          const Packed<PD, GD, MASTER>& r) {
@@ -378,16 +395,15 @@ __device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, flo
 #pragma unroll
   for (int i = 0; i < H; ++i) {
     const F2 g = mul2(u[i], f2(s.scale));
-    F2 v = mul2(codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), f2(r.vs));
-    v = fma2(mul2(v, v), f2(s.b2), mul2(mul2(g, g), f2(s.c2)));
-    m[i] = fma2(mul2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(r.ms)), f2(s.b1), mul2(g, f2(s.c1)));
+    const F2 v = second_moment(s, codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), r.vs, g);
+    m[i] = first_moment(s, codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), r.ms, g);
     u[i] = f2(sqrtf(v.x), sqrtf(v.y));
     const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
     p[i] = fma2(p[i], f2(shrink), mul2(f2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y)), f2(-s.rate_m)));
     mt = nan_max(mt, nan_max(fabsf(m[i].x), fabsf(m[i].y)));
     ut = nan_max(ut, nan_max(u[i].x, u[i].y));
   }
-  const float ms = __fdiv_rn(warp_top(mt), kTop8), us = __fdiv_rn(warp_top(ut), kTop8);
+  const float ms = warp_top(mt) * (1.f / kTop8), us = warp_top(ut) * (1.f / kTop8);
   const float m_by = ms != 0.f ? ms : 1.f, u_by = us != 0.f ? us : 1.f;
 #pragma unroll
   for (int i = 0; i < H; ++i) {
@@ -396,51 +412,61 @@ __device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, flo
     // a root above 0 is not stored as 0
     u[i] = f2(u[i].x > 0.f ? fmaxf(u[i].x, kLeast8) : u[i].x, u[i].y > 0.f ? fmaxf(u[i].y, kLeast8) : u[i].y);
   }
-  store_packed<PD, GD, MASTER, WHOLE>(t, block, n, p, m, u);
+  store_packed<PD, GD, MASTER, WHOLE>(t, block, n, p, all_codes(m), all_codes(u));
   store_scales(t, block, ms, us);
 }
 
 // The same of a whole block whose values lie in the middle of fp32's range and whose roots are all above 0,
-// in fewer instructions (395 -> 220 for 256 elements): the scales' factors are taken into the betas',
-// and roots and reciprocals come from the instructions that flush subnormals to 0.  The new scales are
-// the caller's to store.  False, and nothing written, where a value lies outside.
+// in fewer instructions: roots and reciprocals come from the instructions that are within 2^-23 and flush
+// subnormals to 0, and values are multiplied by a reciprocal of the scale.  All in all a quotient is
+// within 13 2^-24 of the exactly rounded one; where 2^-19 to either side would give another code, the
+// block is left to step_any (about one in a hundred).  The new scales are the caller's to store.  False,
+// and nothing written, where this form will not do.
 template <int PD, int GD, bool MASTER, bool WHOLE>
 __device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, float shrink, long long block,
                                            const Packed<PD, GD, MASTER>& r, float& ms, float& us) {
   constexpr int H = W / 2;
-  constexpr float kLow = 1e-15f, kHigh = 1e15f;
+  constexpr float kLow = 1e-15f, kHigh = 1e15f, kMargin = 1.f / 524288.f;
   if (!(r.vs > kLow && r.vs < kHigh && r.ms < kHigh)) return false;  // the same in all lanes
   F2 p[H], m[H], u[H];
   unpack_packed(r, p, u);
-  const float mb = r.ms * s.b1, vb = r.vs * r.vs * s.b2;
-  float mt = 0.f, ut = 0.f, least = kHigh;
+  float mt = 0.f, vt = 0.f, least = kHigh;
 #pragma unroll
   for (int i = 0; i < H; ++i) {
-    const F2 c = codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1);
     const F2 g = mul2(u[i], f2(s.scale));
-    const F2 v = fma2(mul2(c, c), f2(vb), mul2(mul2(g, g), f2(s.c2)));
-    m[i] = fma2(codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), f2(mb), mul2(g, f2(s.c1)));
+    const F2 v = second_moment(s, codes_to_f2(i < 2 ? r.v.x : r.v.y, i & 1), r.vs, g);
+    m[i] = first_moment(s, codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), r.ms, g);
+    vt = nan_max3_abs(vt, v.x, v.y);
+    least = min3(least, v.x, v.y);
+    mt = nan_max3_abs(mt, m[i].x, m[i].y);
     u[i] = f2(root_ftz(v.x), root_ftz(v.y));
     const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
     p[i] = fma2(mul2(m[i], f2(inverse_ftz(d.x), inverse_ftz(d.y))), f2(-s.rate_m), mul2(p[i], f2(shrink)));
-    mt = nan_max3_abs(mt, m[i].x, m[i].y);
-    ut = nan_max3_abs(ut, u[i].x, u[i].y);
-    least = min3(least, u[i].x, u[i].y);
   }
   mt = warp_top(mt);
-  ut = warp_top(ut);
-  const bool fine = least > 1e-18f && mt > 1e-25f && mt < kHigh && ut < kHigh;  // no: a NaN too
-  if (!__all_sync(0xffffffffu, fine)) return false;
-  const float m_inv = kTop8 * inverse_ftz(mt), u_inv = kTop8 * inverse_ftz(ut);
-#pragma unroll
-  for (int i = 0; i < H; ++i) {
-    m[i] = mul2(m[i], f2(m_inv));
-    u[i] = mul2(u[i], f2(u_inv));
-    u[i] = f2(fmaxf(u[i].x, kLeast8), fmaxf(u[i].y, kLeast8));
-  }
-  store_packed<PD, GD, MASTER, WHOLE>(t, block, W, p, m, u);
+  vt = warp_top(vt);
+  bool fine = least > 1e-36f && mt > 1e-25f && mt < kHigh && vt < kHigh * kHigh;  // no: a NaN too
+  const float ut = __fsqrt_rn(vt);  // the largest root
   ms = mt * (1.f / kTop8);
   us = ut * (1.f / kTop8);
+  const float m_inv = kTop8 * inverse_ftz(mt), u_inv = kTop8 * inverse_ftz(ut);
+  const F2 m_lo = f2(m_inv * (1.f - kMargin)), m_hi = f2(m_inv * (1.f + kMargin));
+  const F2 u_lo = f2(u_inv * (1.f - kMargin)), u_hi = f2(u_inv * (1.f + kMargin));
+  uint2 m8 = make_uint2(0, 0), v8 = make_uint2(0, 0);
+  uint32_t differ = 0;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const uint32_t a = f2_to_codes(mul2(m[i], m_lo)), b = f2_to_codes(mul2(m[i], m_hi));
+    const F2 x = mul2(u[i], u_lo), y = mul2(u[i], u_hi);
+    const uint32_t c = f2_to_codes(f2(fmaxf(x.x, kLeast8), fmaxf(x.y, kLeast8)));
+    const uint32_t d = f2_to_codes(f2(fmaxf(y.x, kLeast8), fmaxf(y.y, kLeast8)));
+    differ |= (a ^ b) | (c ^ d);
+    (i < 2 ? m8.x : m8.y) |= a << (16 * (i & 1));
+    (i < 2 ? v8.x : v8.y) |= c << (16 * (i & 1));
+  }
+  fine = fine && differ == 0;
+  if (!__all_sync(0xffffffffu, fine)) return false;
+  store_packed<PD, GD, MASTER, WHOLE>(t, block, W, p, m8, v8);
   return true;
 }
 
