@@ -52,7 +52,8 @@ extern "C" {
  * exp_avg_scale[i], exp_avg_sq_scale[i] fp32 of ceil(sizes[i] / ADAMW_BLOCK)).
  * masters: NULL, or fp32 arrays, NULL entries without one.  weight_decay: one per
  * tensor.  0 <= beta1, beta2 < 1; eps, lr, weight_decay finite, eps >= 0.  step >= 1,
- * or step >= 0 beside device_step (int64 on the device); device_lr and grad_scale
+ * or step >= 0 beside device_step (int64 on the device; the sum counts from 1);
+ * device_lr and grad_scale
  * (fp32 on the device) may be NULL.  The three are read when the kernel runs, so that
  * a captured graph can advance them. */
 int adamw_step(int64_t count, void* const* params, const void* const* grads, void* const* exp_avg,

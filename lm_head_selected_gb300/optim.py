@@ -118,7 +118,8 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
                device_step: Optional[torch.Tensor] = None, device_lr: Optional[torch.Tensor] = None,
                grad_scale: Optional[torch.Tensor] = None) -> None:
     """One AdamW step, in place, over all tensors (bf16, fp16 or fp32, each its own; gradients of the same
-    dtype or fp32; contiguous, on one CUDA device; none listed twice).  ``step`` counts from 1.  States as
+    dtype or fp32; contiguous, on one CUDA device; none listed twice).  ``step`` counts from 1 (with
+    device_step, their sum does).  States as
     ``adamw_state`` makes them, in 8 bits where the scales are given.  ``weight_decay``: one value, or one
     per tensor.  On the device, read when the kernel runs, so that a captured graph can advance them:
     ``device_step`` (int64, added to step), ``device_lr`` and ``grad_scale`` (fp32, factors of lr and of the
@@ -192,4 +193,7 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         with torch.cuda.device(device):
             call()
     # autograd learns that they have changed
-    torch.autograd.graph.increment_version(params)
+    try:
+        torch.autograd.graph.increment_version(params)
+    except RuntimeError:  # tensors made under inference mode have no version to count
+        torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])

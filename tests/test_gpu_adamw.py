@@ -298,6 +298,43 @@ def test_another_stream_and_other_order():
         assert torch.equal(a, b)
 
 
+def codes_in_fp32(t, root):
+    """The header's formulas in torch's fp32, operation by operation: the stored codes and scales."""
+    b = torch.nn.functional.pad(t, (0, -t.numel() % BLOCK)).view(-1, BLOCK)
+    scale = b.abs().amax(1) * torch.tensor(1.0 / TOP, device=DEV)
+    c = b / torch.where(scale > 0, scale, 1.0)[:, None]
+    if root:
+        c = torch.where(c > 0, c.clamp(LEAST, TOP), 0.0)
+    return c.clamp(-TOP, TOP).to(torch.float8_e4m3fn).view(-1)[:t.numel()], scale
+
+
+@pytest.mark.parametrize("n", [256 * 3000, 100003])
+def test_codes_are_those_of_the_formulas_in_fp32(n):
+    """Next to a border between two codes a sum contracted into one rounding would choose the other one."""
+    params, grads = tensors([n], torch.bfloat16, torch.bfloat16)
+    state = filled(llp.adamw_state(params, 8), grads)
+    f = [state[k][0].float() * state[k + "_scale"][0].repeat_interleave(BLOCK)[:n] for k in ("exp_avg", "exp_avg_sq")]
+    g = grads[0].float()
+    b1, b2 = HYPER["betas"]
+    m = f[0] * b1 + g * (1.0 - b1)
+    v = f[1] * f[1]
+    v = v * b2 + (g * g) * (1.0 - b2)
+    llp.adamw_step(params, grads, **state, step=3, **HYPER)
+    for key, t, root in (("exp_avg", m, False), ("exp_avg_sq", torch.sqrt(v), True)):
+        code, scale = codes_in_fp32(t, root)
+        assert torch.equal(state[key + "_scale"][0], scale)
+        assert torch.equal(state[key][0].float(), code.float())
+
+
+def test_tensors_made_under_inference_mode():
+    with torch.inference_mode():
+        params, grads = tensors([300], torch.float32, torch.float32)
+        state = llp.adamw_state(params)
+        kept = params[0].clone()
+        llp.adamw_step(params, grads, **state, step=1, **HYPER)
+        assert not torch.equal(params[0], kept)
+
+
 def test_refusals():
     params, grads = tensors([64, 32], torch.bfloat16, torch.bfloat16)
     s = llp.adamw_state(params)
