@@ -84,13 +84,11 @@ __device__ __forceinline__ float group_sum(float v, float* sm, int warp, int war
   return v;
 }
 
-__device__ __forceinline__ void copies_left(int rows) {  // waits until at most `rows` (0, 1 or 2) groups are in flight
+__device__ __forceinline__ void copies_left(int rows) {  // waits until at most `rows` (0 or 1) groups are in flight
   if (rows == 0)
     copy_wait<0>();
-  else if (rows == 1)
-    copy_wait<1>();
   else
-    copy_wait<2>();
+    copy_wait<1>();
 }
 
 // Warps of a group and vectors of a thread for a row of `units` vectors, at most `most` vectors to a lane.
@@ -103,10 +101,8 @@ inline ResShape res_shape(int units, int most) {
   return {warps, (units + 32 * warps - 1) / (32 * warps)};
 }
 
-// Rows of the ring, at most three: as many as shared memory holds beside what is kept.
-inline int res_stages(size_t per_stage, size_t kept) {
-  const int n = static_cast<int>((kResSmem - kept) / per_stage);
-  return n > 3 ? 3 : n;
-}
+// Rows of the ring: two where shared memory holds them beside what is kept.  Three were slower (forward
+// 16384 x 2688 62.2 us, 58.5 with two; gradient 16384 x 4096 136.5 and 134.2).
+inline int res_stages(size_t per_stage, size_t kept) { return 2 * per_stage + kept <= kResSmem ? 2 : 1; }
 
 }  // namespace llp

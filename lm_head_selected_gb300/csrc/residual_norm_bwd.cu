@@ -12,6 +12,11 @@
 // launch joins the CTAs' sums in ascending order.  Rows of 1025 to 2048 vectors take four vectors per
 // thread and a third reading in place of the registers; wider ones take plain kernels: one CTA per row,
 // one thread per column over a range of rows.
+//
+// Bound by memory: four tensors read (five with a gate of the rows' own) and two (three) written.  Measured in
+// a captured graph: 16384 x 4096 bf16 134 us (6.0 TB/s, 89% of the measured copy peak; plain kernels 1047);
+// 2049 x 1001 fp32 with a gate of the rows' own 23.4 us (2.8 TB/s: odd rows come in 4-byte copies, whose
+// accesses to shared memory, not HBM, are the bound).
 #include "residual_norm.cuh"
 
 namespace llp {
