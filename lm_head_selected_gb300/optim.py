@@ -154,9 +154,6 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         lists += [_need_all(name, t, blocks, index, torch.float32) for name, t in
                   (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale))]
     words = [a for t in lists for a in map(_data_ptr, t)]
-    starts = [a for a, n in zip(words, sizes) if n]
-    if len(set(starts)) != len(starts):
-        raise ValueError("a parameter is listed twice")
     if masters is not None:
         masters = list(masters)
         if len(masters) != count:
@@ -164,6 +161,10 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         there = [i for i, t in enumerate(masters) if t is not None]
         _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
         words += [0 if t is None else t.data_ptr() for t in masters]
+    # what is written must be somewhere of its own
+    written = [a for a, n in zip(words[:count] + words[2 * count:], sizes * (len(words) // count)) if n and a]
+    if len(set(written)) != len(written):
+        raise ValueError("a parameter or a state is listed twice")
     words = array.array("q", words + sizes)
     codes = array.array("i", p_code + g_code)
     one = isinstance(weight_decay, (int, float))

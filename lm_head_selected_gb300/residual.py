@@ -84,9 +84,12 @@ def residual_rms_norm_fwd(x: torch.Tensor, branch: Optional[torch.Tensor] = None
     scale = float(scale)
     code, _, pcode, kind, xs, bs, gs, N, D = _check(x, branch, gate, post_weight, weight, scale)
     dev = x.device
-    like = x if xs == D else torch.empty((N, D), dtype=x.dtype, device=dev)  # contiguous
-    s = None if branch is None else torch.empty_like(like)
-    h = None if weight is None else torch.empty_like(like)
+
+    def rows():
+        return torch.empty_like(x) if xs == D else torch.empty((N, D), dtype=x.dtype, device=dev)
+
+    s = None if branch is None else rows()
+    h = None if weight is None else rows()
     post_rstd = None if post_weight is None else torch.empty(N, dtype=torch.float32, device=dev)
     rstd = None if weight is None else torch.empty(N, dtype=torch.float32, device=dev)
     st = _lib.load().residual_rms_norm_fwd(x.data_ptr(), xs, _ptr(branch), bs, _ptr(gate), gs, kind, _ptr(post_weight),

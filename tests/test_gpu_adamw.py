@@ -345,6 +345,8 @@ def test_refusals():
         llp.adamw_step(params, grads, **{**state, "step": 1, **over})
 
     for bad, error in ((dict(params=[params[0], params[0]], grads=[grads[0]] * 2), ValueError),
+                       (dict(params=[params[0], params[0][:32]]), ValueError),
+                       (dict(exp_avg_sq=s["exp_avg"]), ValueError), (dict(state=s8, exp_avg_sq_scale=s8["exp_avg_scale"]), ValueError),
                        (dict(grads=grads[:1]), ValueError), (dict(grads=[grads[0].half(), grads[1]]), TypeError),
                        (dict(grads=[grads[1], grads[0]]), ValueError), (dict(params=[params[0].double(), params[1]]), TypeError),
                        (dict(params=[params[0].cpu(), params[1]]), ValueError),

@@ -180,6 +180,19 @@ def test_a_repeated_row():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("D", [264, 77])
+def test_one_row_for_all_in_the_forward(D):
+    """Stride 0 of the stream, the branch or the gate."""
+    N = 30
+    args = inputs(N, D, torch.bfloat16, torch.bfloat16, "rows", True, True)
+    for k in range(3):
+        rep = list(args)
+        rep[k] = args[k][:1].expand(N, D)
+        plain = [t.contiguous() for t in rep]
+        for a, b in zip(llp.residual_rms_norm_fwd(*rep), llp.residual_rms_norm_fwd(*plain)):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_rows_of_zeros_and_of_large_values(dtype):
     args = inputs(6, 264, dtype, dtype, "columns", True, True)
