@@ -71,8 +71,8 @@ def _alike(tensors: list, sizes: List[int], index: int, dtype: torch.dtype) -> b
 def _codes(params: list, grads: list, index: int):
     """The dtype codes of the parameters and of the gradients, and the parameters' sizes, after their checks."""
     try:
-        p_code = [_DTYPE_CODES[d] for d in map(_dtype, params)]
-        g_code = [_DTYPE_CODES[d] for d in map(_dtype, grads)]
+        p_code = list(map(_DTYPE_CODES.__getitem__, map(_dtype, params)))
+        g_code = list(map(_DTYPE_CODES.__getitem__, map(_dtype, grads)))
         n = len(params)
         if ((p_code == g_code or all(g == c or g == 1 for c, g in zip(p_code, g_code))) and
                 list(map(_shape, params)) == list(map(_shape, grads)) and
@@ -162,14 +162,16 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
         words += [0 if t is None else t.data_ptr() for t in masters]
     # what is written must be somewhere of its own
-    written = [a for a, n in zip(words[:count] + words[2 * count:], sizes * (len(words) // count)) if n and a]
+    written = words[:count] + words[2 * count:]
     if len(set(written)) != len(written):
-        raise ValueError("a parameter or a state is listed twice")
+        written = [a for a, n in zip(written, sizes * (len(words) // count)) if n and a]
+        if len(set(written)) != len(written):
+            raise ValueError("a parameter or a state is listed twice")
     words = array.array("q", words + sizes)
     codes = array.array("i", p_code + g_code)
     one = isinstance(weight_decay, (int, float))
     decay = array.array("d", [weight_decay] * count if one else weight_decay)
-    if len(decay) != count or not all(map(math.isfinite, decay)):
+    if len(decay) != count or not (math.isfinite(sum(decay)) or all(map(math.isfinite, decay))):
         raise ValueError(f"weight_decay must be finite, one value or {count}")
     scalars = (None, None, None)
     if device_step is not None or device_lr is not None or grad_scale is not None:
