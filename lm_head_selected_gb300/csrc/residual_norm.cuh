@@ -37,7 +37,7 @@ __device__ __forceinline__ void coefficient_vector(const ResidualNormParams& p, 
   }
 }
 
-// Both as a CTA keeps them for all of its rows (K < 4), in fp32: [2][W / 4][units] float4, the first four
+// Both as a CTA keeps them for all of its rows, in fp32: [2][W / 4][units] float4, the first four
 // columns of every vector, then the others, so that neighbouring threads read neighbouring vectors.
 template <int DT, bool AL>
 __device__ __forceinline__ void keep_coefficients(float4* kept, const ResidualNormParams& p) {
@@ -104,5 +104,11 @@ inline ResShape res_shape(int units, int most) {
 // Rows of the ring: two where shared memory holds them beside what is kept.  Three were slower (forward
 // 16384 x 2688 62.2 us, 58.5 with two; gradient 16384 x 4096 136.5 and 134.2).
 inline int res_stages(size_t per_stage, size_t kept) { return 2 * per_stage + kept <= kResSmem ? 2 : 1; }
+
+// Whether rows of more than kPipeUnits vectors keep their coefficients too: where that costs no row of the
+// ring.  Otherwise they are read anew for each row, as much from L2 as the row itself has in HBM.
+inline bool res_keep(size_t per_stage, size_t kept) {
+  return res_stages(per_stage, 0) * per_stage + kept <= kResSmem;
+}
 
 }  // namespace llp

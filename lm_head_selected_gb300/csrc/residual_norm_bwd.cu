@@ -29,10 +29,12 @@ namespace {
 template <int DT, int K, bool AL, bool ROWS>
 __global__ void __launch_bounds__(kResThreads, 1) residual_norm_bwd_kernel(const ResidualNormParams p,
                                                                            const ResidualNormGrads o, int warps,
-                                                                           int stages, float* __restrict__ part) {
+                                                                           int stages, bool keep_wide,
+                                                                           float* __restrict__ part) {
   using T = typename Elem<DT>::T;
   constexpr int W = Elem<DT>::W, H = W / 2, N_IN = ROWS ? 5 : 4, threads = kResThreads;
-  constexpr bool KEEP = K < 4, HOLD = K < 4;
+  constexpr bool HOLD = K < 4;
+  const bool keep = K < 4 || keep_wide;  // the coefficients lie in shared memory
   using S = Slot<DT, AL>;
   extern __shared__ uint4 ring[];  // [stages][N_IN][K][threads]; then the coefficients; then the slots' fifth words
   __shared__ float red[2][2][threads / 32];
@@ -47,7 +49,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_bwd_kernel(const
   constexpr int pitch = N_IN * K * threads;  // of a stage
   uint4* const mine = ring + threadIdx.x;
   float4* const kept = reinterpret_cast<float4*>(ring + stages * pitch);
-  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + (KEEP ? W / 2 * units : 0)) + threadIdx.x;
+  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + (keep ? W / 2 * units : 0)) + threadIdx.x;
   const bool f32 = p.param_dtype == kDtypeF32, post = p.post_weight != nullptr;
   const bool has_gs = p.gs != nullptr, has_w = p.weight != nullptr;
   const bool has_b = p.branch != nullptr && (post || p.gate_kind != kGateNone);  // else k is of no use
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_bwd_kernel(const
     copy_commit();
   };
   for (int s = 0; s < stages - 1; ++s) issue(r0 + s * step, s);
-  if (KEEP) keep_coefficients<DT, AL>(kept, p);
+  if (keep) keep_coefficients<DT, AL>(kept, p);
   F2 aw[K][H], as[K][H];  // this thread's columns' sums
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -103,14 +105,14 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_bwd_kernel(const
     };
     auto weight = [&](int k, F2 (&v)[H]) {
       const int u = on(k) ? first + k * width : 0;
-      if (KEEP)
+      if (keep)
         kept_vector<W>(kept, 1, units, u, v);
       else
         param_vector<DT, W, AL>(p.weight, f32, u * W, on(k) ? left(k) : min(p.D, W), v);
     };
     auto coefficient = [&](int k, F2 (&v)[H]) {
       const int u = on(k) ? first + k * width : 0;
-      if (KEEP)
+      if (keep)
         kept_vector<W>(kept, 0, units, u, v);
       else
         coefficient_vector<DT, W, AL>(p, f32, u * W, on(k) ? left(k) : min(p.D, W), v);
@@ -385,12 +387,14 @@ cudaError_t rows(const ResidualNormParams& p, const ResidualNormGrads& o, int wa
   constexpr int W = Elem<DT>::W;
   const int units = (p.D + W - 1) / W, groups = kResThreads / 32 / warps;
   const size_t per_stage = res_bwd_stage(K, ROWS, al ? 16 : Slot<DT, false>::BYTES);
-  const size_t kept = K < 4 ? static_cast<size_t>(2) * units * W * sizeof(float) : 0;
+  size_t kept = static_cast<size_t>(2) * units * W * sizeof(float);
+  const bool keep = K < 4 || res_keep(per_stage, kept);
+  if (!keep) kept = 0;
   const int stages = res_stages(per_stage, kept);
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
   const auto kernel = al ? residual_norm_bwd_kernel<DT, K, true, ROWS> : residual_norm_bwd_kernel<DT, K, false, ROWS>;
-  kernel<<<grid, kResThreads, stages * per_stage + kept, s>>>(p, o, warps, stages, columns ? part : nullptr);
+  kernel<<<grid, kResThreads, stages * per_stage + kept, s>>>(p, o, warps, stages, keep, columns ? part : nullptr);
   const cudaError_t e = launch_result();
   if (e != cudaSuccess || !columns) return e;
   return p.param_dtype == kDtypeF32 ? join<kDtypeF32>(p, o, part, grid, s) : join<DT>(p, o, part, grid, s);

@@ -23,10 +23,10 @@ namespace {
 template <int DT, int K, bool AL, bool ROWS>
 __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const ResidualNormParams p,
                                                                            const ResidualNormOut o, int warps,
-                                                                           int stages) {
+                                                                           int stages, bool keep_wide) {
   using T = typename Elem<DT>::T;
   constexpr int W = Elem<DT>::W, H = W / 2, N_IN = ROWS ? 3 : 2, threads = kResThreads;
-  constexpr bool KEEP = K < 4;
+  const bool keep = K < 4 || keep_wide;  // the coefficients lie in shared memory
   using S = Slot<DT, AL>;
   extern __shared__ uint4 ring[];  // [stages][N_IN][K][threads]; then the coefficients; then the slots' fifth words
   __shared__ float red[2][2][threads / 32];
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
   constexpr int pitch = N_IN * K * threads;  // of a stage
   uint4* const mine = ring + threadIdx.x;
   float4* const kept = reinterpret_cast<float4*>(ring + stages * pitch);
-  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + (KEEP ? W / 2 * units : 0)) + threadIdx.x;
+  uint32_t* const fifth = reinterpret_cast<uint32_t*>(kept + (keep ? W / 2 * units : 0)) + threadIdx.x;
   const bool has_b = p.branch != nullptr, f32 = p.param_dtype == kDtypeF32;
   for (int i = 0; i < stages * N_IN; ++i)
 #pragma unroll
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
     copy_commit();
   };
   for (int s = 0; s < stages - 1; ++s) issue(r0 + s * step, s);
-  if (KEEP) keep_coefficients<DT, AL>(kept, p);
+  if (keep) keep_coefficients<DT, AL>(kept, p);
   __syncthreads();
   const float inv = 1.f / static_cast<float>(p.D);
   int stage = 0;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
       read(0, k, p.x, p.x_stride, x);
       if (has_b) {
         const int u = on(k) ? first + k * width : 0;
-        if (KEEP)
+        if (keep)
           kept_vector<W>(kept, 0, units, u, c);
         else
           coefficient_vector<DT, W, AL>(p, f32, u * W, on(k) ? left(k) : min(p.D, W), c);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
     for (int k = 0; k < K; ++k) {
       if (on(k)) {
         F2 w[H];
-        if (KEEP)
+        if (keep)
           kept_vector<W>(kept, 1, units, first + k * width, w);
         else
           param_vector<DT, W, AL>(p.weight, f32, (first + k * width) * W, left(k), w);
@@ -212,12 +212,14 @@ cudaError_t rows(const ResidualNormParams& p, const ResidualNormOut& o, int warp
   constexpr int W = Elem<DT>::W;
   const int units = (p.D + W - 1) / W, groups = kResThreads / 32 / warps;
   const size_t per_stage = static_cast<size_t>(ROWS ? 3 : 2) * K * kResThreads * (al ? 16 : Slot<DT, false>::BYTES);
-  const size_t kept = K < 4 ? static_cast<size_t>(2) * units * W * sizeof(float) : 0;
+  size_t kept = static_cast<size_t>(2) * units * W * sizeof(float);
+  const bool keep = K < 4 || res_keep(per_stage, kept);
+  if (!keep) kept = 0;
   const int stages = res_stages(per_stage, kept);
   const long long want = (static_cast<long long>(p.N) + groups - 1) / groups;
   const int grid = static_cast<int>(want < kPipeSMs ? want : kPipeSMs);
   const auto kernel = al ? residual_norm_fwd_kernel<DT, K, true, ROWS> : residual_norm_fwd_kernel<DT, K, false, ROWS>;
-  kernel<<<grid, kResThreads, stages * per_stage + kept, s>>>(p, o, warps, stages);
+  kernel<<<grid, kResThreads, stages * per_stage + kept, s>>>(p, o, warps, stages, keep);
   return launch_result();
 }
 
