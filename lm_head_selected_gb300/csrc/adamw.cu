@@ -5,10 +5,10 @@
 // Bound by memory.  States in 32 bits: 28 bytes per bf16 parameter with an fp32 master copy.  439 M of
 // them 1850 us (6.6 TB/s, 99% of the measured copy peak) with 512 threads and chunks of 4096 elements to an
 // SM; four CTAs of 256 took 2075: with more streams at once each has less of a DRAM page.
-// States in 8 bits: 10 bytes per bf16 parameter.  369 M of them 669 us (5.5 TB/s, 83%); the copies and stores
-// alone, without arithmetic, take 611.  What it took, from 1123 us: the blocks to come in a ring of shared
-// memory (828), codes in 16-byte copies and scales not loaded by themselves (755), scales stored 64 bytes
-// at a time (698), fewer warps with deeper rings and no spills (652), codes exact to the border (669).
+// States in 8 bits: 10 bytes per bf16 parameter.  369 M of them 600 us (6.2 TB/s, 92%).  What it took, from
+// 1123 us: the blocks to come in a ring of shared memory (828), codes in 16-byte copies and scales not
+// loaded by themselves (755), scales stored 64 bytes at a time (698), fewer warps with deeper rings and no
+// spills (652), codes exact to the border (669), the warps' rings on banks of their own (600).
 #include <cuda_fp8.h>
 
 #include "adamw_internal.h"
@@ -207,12 +207,15 @@ struct Packed {
 template <int PD, int GD, bool MASTER>
 struct Slot8 {
   using R = Packed<PD, GD, MASTER>;
-  uint4 p[2][R::PV][32];
-  uint4 g[2][R::GV][32];
+  uint4 p[2][R::PV * 32];  // as in memory: neighbouring lanes copy neighbouring vectors
+  uint4 g[2][R::GV * 32];
   uint2 m[2][32];
   uint2 v[2][32];
 };
-constexpr int kWarpRing = 12352;  // bytes of a warp's ring: four slots of 16-bit parameters and gradients, one or two of others
+// Bytes of a warp's ring: four slots of 16-bit parameters and gradients, two or three of others, and an odd
+// multiple of 16 bytes, so that the CTA's rings do not all start on the same banks (bf16, 186 M
+// parameters: 282 us, 306 with multiples of 32, 319 of 128).
+constexpr int kWarpRing = 12400;
 
 // The pair's blocks below `stop`.
 template <int PD, int GD, bool MASTER>
@@ -221,16 +224,16 @@ __device__ __forceinline__ void copy_pair(const AdamTensor& t, long long block, 
   const int lane = threadIdx.x & 31;
   const bool both = block + 1 < stop;
   const long long at = block * kAdamBlock;
-  const uint4* const p = MASTER ? reinterpret_cast<const uint4*>(t.master + at + lane * W)
-                                : reinterpret_cast<const uint4*>(static_cast<const typename Elem<PD>::T*>(t.p) + at + lane * W);
-  const uint4* const g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GD>::T*>(t.g) + at + lane * W);
+  const uint4* const p = (MASTER ? reinterpret_cast<const uint4*>(t.master + at)
+                                 : reinterpret_cast<const uint4*>(static_cast<const typename Elem<PD>::T*>(t.p) + at)) + lane;
+  const uint4* const g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GD>::T*>(t.g) + at) + lane;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (k == 0 || both) {
 #pragma unroll
-      for (int i = 0; i < R::PV; ++i) copy_async(&slot->p[k][i][lane], p + k * 32 * R::PV + i);
+      for (int i = 0; i < R::PV; ++i) copy_async(&slot->p[k][i * 32 + lane], p + (k * R::PV + i) * 32);
 #pragma unroll
-      for (int i = 0; i < R::GV; ++i) copy_async(&slot->g[k][i][lane], g + k * 32 * R::GV + i);
+      for (int i = 0; i < R::GV; ++i) copy_async(&slot->g[k][i * 32 + lane], g + (k * R::GV + i) * 32);
     }
   }
   if (lane < 16 || both) {
@@ -244,9 +247,9 @@ __device__ __forceinline__ void read_packed(const Slot8<PD, GD, MASTER>* slot, i
   using R = Packed<PD, GD, MASTER>;
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < R::PV; ++i) r.p[i] = slot->p[k][i][lane];
+  for (int i = 0; i < R::PV; ++i) r.p[i] = slot->p[k][lane * R::PV + i];
 #pragma unroll
-  for (int i = 0; i < R::GV; ++i) r.g[i] = slot->g[k][i][lane];
+  for (int i = 0; i < R::GV; ++i) r.g[i] = slot->g[k][lane * R::GV + i];
   r.m = slot->m[k][lane];
   r.v = slot->v[k][lane];
 }
@@ -512,7 +515,7 @@ __device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* sh
   extern __shared__ uint4 adam_ring[];
   Ring* const ring = reinterpret_cast<Ring*>(reinterpret_cast<unsigned char*>(adam_ring) + (threadIdx.x >> 5) * kWarpRing);
   constexpr int kAhead = kWarpRing / sizeof(Ring);
-  static_assert(kAhead >= 1 && sizeof(Ring) % 16 == 0 && kWarpRing % 16 == 0, "slots of the ring");
+  static_assert(kAhead >= 2 && sizeof(Ring) % 16 == 0 && kWarpRing % 16 == 0, "slots of the ring");
   const int lane = threadIdx.x & 31;
   const long long blocks = (t.n + kAdamBlock - 1) / kAdamBlock;
   const long long mine = static_cast<long long>(chunk) * (kAdamPackedChunk / kAdamBlock) + (threadIdx.x >> 5) * kWarpBlocks;
