@@ -99,12 +99,11 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
     for (int k = 0; k < K; ++k) {
       F2 x[H], c[H];
       read(0, k, p.x, p.x_stride, x);
-      if (has_b) {
-        const int u = on(k) ? first + k * width : 0;
+      if (has_b && on(k)) {  // past the row's end there is no coefficient, and any in its place might be infinite
         if (keep)
-          kept_vector<W>(kept, 0, units, u, c);
+          kept_vector<W>(kept, 0, units, first + k * width, c);
         else
-          coefficient_vector<DT, W, AL>(p, f32, u * W, on(k) ? left(k) : min(p.D, W), c);
+          coefficient_vector<DT, W, AL>(p, f32, (first + k * width) * W, left(k), c);
 #pragma unroll
         for (int j = 0; j < H; ++j) s[k][j] = mul2(mul2(s[k][j], f2(pr)), c[j]);
         if (ROWS) {

@@ -317,3 +317,38 @@ def test_refusals():
                        (lambda: llp.residual_rms_norm(x, b[:, :32], weight=w), ValueError)):
         with pytest.raises(error):
             bad()
+
+
+def same_places(name, got, ref):
+    """NaN and both infinities where the reference has them."""
+    got = np64(got)
+    assert (np.isnan(got) == np.isnan(ref)).all(), name
+    assert (np.where(np.isinf(got), got, 0) == np.where(np.isinf(ref), ref, 0)).all(), name
+
+
+@pytest.mark.parametrize("N,D,dtype", [(5, 200, torch.bfloat16), (3, 1001, torch.float32), (4, 640, torch.float16),
+                                       (3, 5000, torch.float32), (3, 5001, torch.bfloat16), (3, 8200, torch.float32)])
+def test_an_infinite_weight_of_the_first_column_stays_there(N, D, dtype):
+    args = inputs(N, D, dtype, torch.float32, "columns", True, True)
+    g = torch.Generator().manual_seed(5)
+    gs, gh = (torch.randn(N, D, generator=g).to(dtype).to(DEV) for _ in range(2))
+    clean = llp.residual_rms_norm_fwd(*args)
+    grads = llp.residual_rms_norm_bwd(gs, gh, clean[0], *args[1:], clean[2], clean[3])
+    for which in (3, 4):
+        bad = list(args)
+        bad[which] = args[which].clone()
+        bad[which][0] = float("inf")
+        with np.errstate(invalid="ignore", over="ignore"):
+            ref = bo.residual_forward(*(n64(t) for t in bad), 1.0, EPS)
+            back = bo.residual_backward(*(n64(t) for t in (gs, gh, clean[0], *bad[1:], clean[2], clean[3])), 1.0)
+        got = llp.residual_rms_norm_fwd(*bad)
+        for name, a, b in zip(("s", "h", "post_rstd", "rstd"), got, ref):
+            same_places(name, a, b)
+        assert torch.equal(got[0][:, 1:], clean[0][:, 1:]) and torch.equal(got[2], clean[2])
+        got = llp.residual_rms_norm_bwd(gs, gh, clean[0], *bad[1:], clean[2], clean[3])
+        same_places("grad_x", got[0], back[0])
+        same_places("grad_branch", got[1], back[1])
+        same_places("grad_post_weight", got[3], back[3])
+        assert torch.equal(got[4], grads[4])
+        if which == 3:
+            assert torch.equal(got[0], grads[0]) and torch.equal(got[3], grads[3])
