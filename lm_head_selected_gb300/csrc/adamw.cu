@@ -478,7 +478,8 @@ __device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, f
   return true;
 }
 
-// What step_usual left of a warp's blocks of a chunk (bit i of `done`: the i-th is not), those off the vectors' boundaries and the tensor's last.  A call, so that its registers are not the whole blocks'.
+// What step_usual left of a warp's blocks of a chunk (bit i of `done`: the i-th is not), those off the
+// vectors' boundaries and the tensor's last.  A call, so that its registers are not the whole blocks'.
 template <int PD, int GD, bool MASTER>
 __device__ __noinline__ void packed_rest(const AdamTensor& t, const Step* shared, long long mine, long long end,
                                          long long stop, unsigned done) {
@@ -584,7 +585,8 @@ __device__ __forceinline__ void chunk_of(const AdamTensor& t, const Step* shared
 }
 
 template <int MOST, int BITS>
-__global__ void __launch_bounds__(BITS == 8 ? kPackedThreads : kAdamThreads, kAdamResident<BITS>) adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
+__global__ void __launch_bounds__(BITS == 8 ? kPackedThreads : kAdamThreads, kAdamResident<BITS>)
+    adamw_kernel(const __grid_constant__ AdamTable<MOST> table) {
   __shared__ Step shared;
   if (threadIdx.x == 0) shared = read_step(table.k);
   __syncthreads();

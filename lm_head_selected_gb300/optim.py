@@ -118,10 +118,9 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
                device_step: Optional[torch.Tensor] = None, device_lr: Optional[torch.Tensor] = None,
                grad_scale: Optional[torch.Tensor] = None) -> None:
     """One AdamW step, in place, over all tensors (bf16, fp16 or fp32, each its own; gradients of the same
-    dtype or fp32; contiguous, on one CUDA device; none listed twice).  ``step`` counts from 1 (with
-    device_step, their sum does).  States as
-    ``adamw_state`` makes them, in 8 bits where the scales are given.  ``weight_decay``: one value, or one
-    per tensor.  On the device, read when the kernel runs, so that a captured graph can advance them:
+    dtype or fp32; contiguous, on one CUDA device; none listed twice, no gradient a parameter or a state
+    too).  ``step`` counts from 1 (with device_step, their sum does).  States as ``adamw_state`` makes
+    them, in 8 bits where the scales are given.  ``weight_decay``: one value, or one per tensor.  On the device, read when the kernel runs, so that a captured graph can advance them:
     ``device_step`` (int64, added to step), ``device_lr`` and ``grad_scale`` (fp32, factors of lr and of the
     gradients)."""
     params, grads = list(params), list(grads)
@@ -162,11 +161,15 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
         words += [0 if t is None else t.data_ptr() for t in masters]
     # what is written must be somewhere of its own
-    written = words[:count] + words[2 * count:]
-    if len(set(written)) != len(written):
+    written, read = words[:count] + words[2 * count:], words[count:2 * count]
+    places = set(written)
+    if len(places) != len(written) or not places.isdisjoint(read):
         written = [a for a, n in zip(written, sizes * (len(words) // count)) if n and a]
-        if len(set(written)) != len(written):
+        places = set(written)
+        if len(places) != len(written):
             raise ValueError("a parameter or a state is listed twice")
+        if not places.isdisjoint(a for a, n in zip(read, sizes) if n):
+            raise ValueError("a gradient is a parameter or a state too")
     words = array.array("q", words + sizes)
     codes = array.array("i", p_code + g_code)
     one = isinstance(weight_decay, (int, float))

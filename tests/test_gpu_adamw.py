@@ -366,3 +366,18 @@ def test_refusals():
     assert all(torch.equal(a, b) for a, b in zip(params, kept))
     with pytest.raises(ValueError):
         llp.adamw_state(params, 16)
+
+
+def test_a_gradient_that_is_written_too_is_refused():
+    params, grads = tensors([64, 0, 32, 0], torch.float32, torch.float32)
+    state = llp.adamw_state(params)
+    kept = [p.clone() for p in params]
+    for bad in ([params[0], *grads[1:]], [grads[0], grads[1], params[0][:32], grads[3]],
+                [state["exp_avg"][0], *grads[1:]], [*grads[:2], state["exp_avg_sq"][2], grads[3]]):
+        with pytest.raises(ValueError, match="gradient"):
+            llp.adamw_step(params, bad, **state, step=1)
+    assert all(torch.equal(a, b) for a, b in zip(params, kept))
+    # one gradient for two parameters is read twice; tensors without elements share no place
+    llp.adamw_step([params[0], params[1], params[2]], [grads[0], grads[1], grads[0][:32]],
+                   state["exp_avg"][:3], state["exp_avg_sq"][:3], 1)
+    assert not torch.equal(params[2], kept[2])
