@@ -1467,10 +1467,10 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
   const bool f16 = dtype == llp::kDtypeF16;
   CUtensorMap tm_x, tm_wg, tm_wu, tm_y, tm_pre;
   llp::GatedSmallParams q = {};
-  // one map may reach both weights where they do not start at one place (nor 2^40 bytes apart)
+  // one map may reach both weights where they do not overlap (nor start 2^40 bytes apart)
   const uintptr_t at_g = reinterpret_cast<uintptr_t>(w_gate), at_u = reinterpret_cast<uintptr_t>(w_up);
   const uint64_t apart = at_u > at_g ? at_u - at_g : at_g - at_u;
-  q.joint = apart > 0 && apart < (uint64_t(1) << 40) ? 1 : 0;
+  q.joint = apart >= static_cast<uint64_t>(F) * D * 2 && apart < (uint64_t(1) << 40) ? 1 : 0;
   q.up_first = at_u < at_g ? 1 : 0;
   if (llp::gated_small_plan(static_cast<int>(N), static_cast<int>(D), static_cast<int>(F), dev->num_sms, &q)) {
     // few tokens: the weights' rows on the MMA's M side
@@ -1797,7 +1797,9 @@ namespace {
 int adamw_head(const llp::AdamTensor& t) {
   const uintptr_t ps = dtype_bytes(t.param_dtype), gs = dtype_bytes(t.grad_dtype);
   for (int e = 0; e < 8 && e <= t.n; ++e) {
-    auto at = [&](const void* p, uintptr_t size) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) + e * size) % 16 == 0; };
+    auto at = [&](const void* p, uintptr_t size) {
+      return p == nullptr || (reinterpret_cast<uintptr_t>(p) + e * size) % 16 == 0;
+    };
     if (at(t.p, ps) && at(t.g, gs) && at(t.m, 4) && at(t.v, 4) && at(t.master, 4)) return e;
   }
   return -1;
@@ -1844,7 +1846,9 @@ int adamw_checked(int64_t count, void* const* params, const void* const* grads, 
         !aligned(t.v, ss) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4) || !aligned(t.master, 4))
       return LLP_ERR_MISALIGNED;
     if (bits == 8)
-      t.head = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.master, 16) && aligned(t.m, 16) && aligned(t.v, 16) ? 0 : -1;
+      t.head = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.master, 16) && aligned(t.m, 16) && aligned(t.v, 16)
+                   ? 0
+                   : -1;
     else
       t.head = static_cast<short>(adamw_head(t));
     all->push_back(t);
@@ -1905,7 +1909,8 @@ int adamw_step(int64_t count, void* const* params, const void* const* grads, voi
       int64_t chunks = 0;
       while (last < all.size() && last - first < static_cast<size_t>(llp::kAdamMany)) {
         const int64_t head = all[last].head > 0 ? all[last].head : 0;
-        const int64_t own = all[last].n > head ? cdiv(all[last].n - head, state_bits == 8 ? llp::kAdamPackedChunk : llp::kAdamChunk) : 1;
+        const int64_t chunk = state_bits == 8 ? llp::kAdamPackedChunk : llp::kAdamChunk;
+        const int64_t own = all[last].n > head ? cdiv(all[last].n - head, chunk) : 1;
         if (last > first && chunks + own > (int64_t(1) << 30)) break;
         all[last].first_chunk = static_cast<int>(chunks);
         chunks += own;

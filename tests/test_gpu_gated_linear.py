@@ -254,3 +254,14 @@ def test_refusals():
                        (lambda: llp.gated_linear_bwd(gy, pre, x, wg, wu, workspace=torch.empty(8, dtype=torch.uint8, device=DEV)), ValueError)):
         with pytest.raises(error):
             bad()
+
+
+@pytest.mark.parametrize("N", [1, 5, 300])
+def test_weights_that_overlap(N):
+    D, F = 64, 128
+    x, flat, _, _ = inputs(N, D, 2 * F, torch.bfloat16)
+    flat = flat.reshape(-1)
+    for at in (8, D, 8 * D, F * D - 8, F * D):
+        first, second = flat[:F * D].view(F, D), flat[at:at + F * D].view(F, D)
+        for wg, wu in ((first, second), (second, first)):
+            assert torch.equal(llp.gated_linear(x, wg, wu), llp.gated_linear(x, wg.clone(), wu.clone())), at
