@@ -1528,15 +1528,18 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
 namespace {
 struct GatedLayout {
   size_t sched, dpre, part, total;
-  int nseg;  // segments of grad_x's sum
+  llp::GatedSplit x, w;  // segments of grad_x's sum and of the weights' gradients'; one after the other in `part`
 };
 GatedLayout gated_layout(int64_t N, int64_t D, int64_t F) {
   Carver c;
   GatedLayout L;
   L.sched = c.take(llp::kNumSchedCounters * sizeof(int));
   L.dpre = c.take(static_cast<size_t>(N) * 2 * gated_pad(F) * 2);
-  L.nseg = llp::gated_segments(N, D, gated_pad(F));
-  L.part = L.nseg > 1 ? c.take(static_cast<size_t>(L.nseg) * N * D * sizeof(float)) : 0;
+  L.x = llp::gated_split_x(N, D, gated_pad(F));
+  L.w = llp::gated_split_w(N, D, F);
+  const size_t of_x = L.x.nseg > 1 ? static_cast<size_t>(L.x.nseg) * N * D * sizeof(float) : 0;
+  const size_t of_w = L.w.nseg > 1 ? static_cast<size_t>(L.w.nseg) * 2 * F * D * sizeof(float) : 0;
+  L.part = of_x + of_w > 0 ? c.take(of_x > of_w ? of_x : of_w) : 0;
   L.total = c.off;
   return L;
 }
@@ -1606,9 +1609,9 @@ int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const v
     p.K = static_cast<int>(2 * P);
     p.num_m = static_cast<int>(cdiv(N, llp::kUnitM));
     p.num_d = static_cast<int>(cdiv(D, llp::kTileN));
-    p.nseg = L.nseg;
-    p.kseg_blocks = static_cast<int>(cdiv(2 * P / llp::kTileK, L.nseg));
-    p.part = L.nseg > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+    p.nseg = L.x.nseg;
+    p.kseg_blocks = L.x.per;
+    p.part = L.x.nseg > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;
     p.half_blocks = static_cast<int>(P / llp::kTileK);
     p.out = static_cast<__nv_bfloat16*>(grad_x);
     p.err = dev->status_ptr;
@@ -1641,16 +1644,22 @@ int gated_linear_bwd(const void* grad_y, const void* pre, const void* x, const v
     p.num_m = grad_w_gate != nullptr && grad_w_up != nullptr ? 2 * p.tiles : p.tiles;
     p.F_pad = static_cast<int>(P);
     p.num_d = static_cast<int>(cdiv(D, llp::kTileN));
-    p.nseg = 1;
-    p.kseg_blocks = static_cast<int>(cdiv(N, llp::kTileK));
+    p.nseg = L.w.nseg;
+    p.kseg_blocks = L.w.per;
     p.err = dev->status_ptr;
     p.f16 = f16 ? 1 : 0;
     p.sched = !force_static_schedule() && max_unit_kblocks(p) >= llp::kDynMinKBlocks ? sched + 1 : nullptr;
+    float* const part = p.nseg > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;  // [2][nseg][F][D]
     p.out = static_cast<__nv_bfloat16*>(grad_w_gate != nullptr ? grad_w_gate : grad_w_up);
+    p.part = part;
     if (make_map_grad_out(&tm_g, p) != LLP_OK) return fail_cuda(__LINE__);
     p.out = static_cast<__nv_bfloat16*>(grad_w_up != nullptr ? grad_w_up : grad_w_gate);
+    p.part = part == nullptr ? nullptr : part + static_cast<size_t>(p.nseg) * F * D;
     if (make_map_grad_out(&tm_u, p) != LLP_OK) return fail_cuda(__LINE__);
     if (llp::launch_gated_grad_w(tm_d, tm_x, tm_g, tm_u, p, dev->gated, s) != cudaSuccess) return fail_cuda(__LINE__);
+    if (part != nullptr && llp::launch_gated_join(part, p.nseg, static_cast<long long>(F) * D, grad_w_gate, grad_w_up,
+                                                  f16, dev->num_sms, s) != cudaSuccess)
+      return fail_cuda(__LINE__);
   }
   return LLP_OK;
 }

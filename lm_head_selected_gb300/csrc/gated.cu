@@ -250,7 +250,35 @@ cudaError_t dpre(const GatedBwdParams& p, int blocks, cudaStream_t s) {
   return launch_result();
 }
 
+// The segments' partials of the weights' gradients, part [2][nseg][count], one weight to each blockIdx.y.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) gated_join_kernel(const float4* __restrict__ part, int nseg,
+                                                                  long long count4, uint2* gate, uint2* up, bool f16) {
+  uint2* const out = blockIdx.y == 0 ? gate : up;
+  if (out == nullptr) return;
+  part += static_cast<size_t>(blockIdx.y) * nseg * count4;
+  const long long step = static_cast<long long>(gridDim.x) * kJoinThreads;
+  for (long long i = static_cast<long long>(blockIdx.x) * kJoinThreads + threadIdx.x; i < count4; i += step) {
+    float4 sum = __ldg(part + i);
+#pragma unroll 8
+    for (int s = 1; s < nseg; ++s) {
+      const float4 v = __ldg(part + s * count4 + i);
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
+    out[i] = make_uint2(pack16x2(f16, sum.x, sum.y), pack16x2(f16, sum.z, sum.w));
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_gated_join(const float* part, int nseg, long long count, void* gate, void* up, bool f16, int num_sms,
+                              cudaStream_t s) {
+  const long long want = (count / 4 + kJoinThreads - 1) / kJoinThreads, most = 4LL * num_sms;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most), 2);
+  gated_join_kernel<<<grid, kJoinThreads, 0, s>>>(reinterpret_cast<const float4*>(part), nseg, count / 4,
+                                                  static_cast<uint2*>(gate), static_cast<uint2*>(up), f16);
+  return launch_result();
+}
 
 cudaError_t gated_setup(GatedCaps* caps) {
   cudaError_t e = note_cuda(setup_gemm<GatedFwdCfg<128>>(&caps->fwd_groups[0]));
@@ -284,8 +312,8 @@ cudaError_t launch_gated_grad_x(const CUtensorMap& dpre, const CUtensorMap& wg, 
 cudaError_t launch_gated_grad_w(const CUtensorMap& dpre, const CUtensorMap& x, const CUtensorMap& gwg,
                                 const CUtensorMap& gwu, const GatedGradWParams& p, const GatedCaps& caps,
                                 cudaStream_t s) {
-  return launch_units<GatedGradWCfg>({dpre, x, gwg, gwu}, p, static_cast<long long>(p.num_m) * p.num_d, caps.gw_groups,
-                                     s);
+  const long long units = static_cast<long long>(p.nseg) * p.num_m * p.num_d;
+  return launch_units<GatedGradWCfg>({dpre, x, gwg, gwu}, p, units, caps.gw_groups, s);
 }
 
 }  // namespace llp

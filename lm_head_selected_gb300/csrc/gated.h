@@ -20,20 +20,32 @@ inline int gated_cols(long long N, long long F) {
   return ((N + kUnitM - 1) / kUnitM) * ((F + 63) / 64) <= kGatedPairs ? 64 : 128;
 }
 
-// Segments of the long sum of grad_x: with fewer tiles than pairs, the K blocks are split among pairs, and
-// the segments' fp32 partials are summed in ascending order.  In units of a K block's time on a pair
-// (0.27 us): a segment's blocks and about 8 for its start and end, for each wave; the partials' way
-// through memory at 5 TB/s.
-inline int gated_segments(long long N, long long D, long long F_pad) {
-  const long long tiles = ((N + kUnitM - 1) / kUnitM) * ((D + kTileN - 1) / kTileN), blocks = 2 * F_pad / kTileK;
-  long long best = 1, best_cost = ((tiles + kGatedPairs - 1) / kGatedPairs) * (blocks + 8);
+// Segments of a gradient's long sum: with fewer tiles than pairs, the K blocks are split among pairs, and
+// the segments' fp32 partials of its `count` elements are summed in ascending order.  In units of a K block's
+// time on a pair (0.27 us): a segment's blocks and about 8 for its start and end, for each wave; the
+// partials' way through memory at 5 TB/s.  `per`: blocks of a segment, a multiple of `step`.
+struct GatedSplit {
+  int nseg, per;
+};
+inline GatedSplit gated_split(long long tiles, long long blocks, long long count, long long step) {
+  long long best = 1, best_per = blocks, best_cost = ((tiles + kGatedPairs - 1) / kGatedPairs) * (blocks + 8);
   for (long long n = 2; n <= 16 && n * tiles <= 2 * kGatedPairs; ++n) {
-    const long long per = (blocks + n - 1) / n;
+    const long long per = ((blocks + n - 1) / n + step - 1) / step * step;
     if ((blocks + per - 1) / per != n) continue;
-    const long long cost = ((tiles * n + kGatedPairs - 1) / kGatedPairs) * (per + 8) + 16 + n * N * D * 8 / 1350000;
-    if (cost < best_cost) best = n, best_cost = cost;
+    const long long cost = ((tiles * n + kGatedPairs - 1) / kGatedPairs) * (per + 8) + 16 + n * count * 8 / 1350000;
+    if (cost < best_cost) best = n, best_per = per, best_cost = cost;
   }
-  return static_cast<int>(best);
+  return {static_cast<int>(best), static_cast<int>(best_per)};
+}
+inline long long gated_tiles(long long rows, long long cols) {
+  return ((rows + kUnitM - 1) / kUnitM) * ((cols + kTileN - 1) / kTileN);
+}
+inline GatedSplit gated_split_x(long long N, long long D, long long F_pad) {
+  return gated_split(gated_tiles(N, D), 2 * F_pad / kTileK, N * D, 1);
+}
+// Of both weights' gradients, whichever is asked for: the same bits then.  A stage may hold two blocks.
+inline GatedSplit gated_split_w(long long N, long long D, long long F) {
+  return gated_split(2 * gated_tiles(F, D), (N + kTileK - 1) / kTileK, 2 * F * D, 2);
 }
 
 struct GatedFwdParams {
@@ -106,6 +118,9 @@ cudaError_t launch_gated_dpre(const GatedBwdParams& p, int num_sms, cudaStream_t
 cudaError_t launch_gated_grad_x(const CUtensorMap& dpre, const CUtensorMap& wg, const CUtensorMap& wu,
                                 const CUtensorMap& gx, const GatedGradXParams& p, const GatedCaps& caps,
                                 cudaStream_t s);
+// out[k][i] = the sum over s of part[k][s][i], rounded; either may be null.
+cudaError_t launch_gated_join(const float* part, int nseg, long long count, void* gate, void* up, bool f16, int num_sms,
+                              cudaStream_t s);
 cudaError_t launch_gated_grad_w(const CUtensorMap& dpre, const CUtensorMap& x, const CUtensorMap& gwg,
                                 const CUtensorMap& gwu, const GatedGradWParams& p, const GatedCaps& caps,
                                 cudaStream_t s);

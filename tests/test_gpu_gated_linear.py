@@ -265,3 +265,24 @@ def test_weights_that_overlap(N):
         first, second = flat[:F * D].view(F, D), flat[at:at + F * D].view(F, D)
         for wg, wu in ((first, second), (second, first)):
             assert torch.equal(llp.gated_linear(x, wg, wu), llp.gated_linear(x, wg.clone(), wu.clone())), at
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,D,F", [(5000, 72, 200), (4999, 264, 520), (16391, 120, 360), (2049, 64, 8), (1537, 8, 64)])
+def test_long_sums_of_few_tiles(N, D, F, dtype):
+    """The weights' gradients in segments of the tokens: the same bits whichever is asked for, in every run and
+    whatever the workspace holds."""
+    from lm_head_selected_gb300 import _lib
+    act = ACTS[N % 3]
+    x, wg, wu, gy = inputs(N, D, F, dtype)
+    _, pre = llp.gated_linear_fwd(x, wg, wu, act, keep=True)
+    every = llp.gated_linear_bwd(gy, pre, x, wg, wu, act)
+    check_backward(every, gy, pre, x, wg, wu, act)
+    nbytes = _lib.load().gated_linear_bwd_workspace_bytes(N, D, F)
+    ws = torch.full((nbytes + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+    for need in itertools.product([False, True], repeat=3):
+        got = llp.gated_linear_bwd(gy, pre, x, wg, wu, act, *need, workspace=ws[:nbytes])
+        for n, a, b in zip(need, got, every):
+            assert torch.equal(a, b) if n else a is None
+    assert bool((ws[nbytes:] == 0xFF).all())
+    assert llp.device_status() == 0
