@@ -53,7 +53,7 @@ struct GatedFwdCfg : PlainOperands {
   static __device__ __forceinline__ const CUtensorMap* b_map(const Maps& m, const Params&, uint32_t rank, int) {
     return rank == 0 ? &m.b : &m.b2;
   }
-  static __device__ __forceinline__ int b_row(int n0, int, int, int, int) { return n0; }
+  static __device__ __forceinline__ int b_row(const Params&, int n0, int, int, int, int) { return n0; }
   static __device__ __forceinline__ const CUtensorMap* c_map2(const Maps& m) { return &m.c2; }
   static __device__ __forceinline__ uint64_t policy_a() { return l2_policy_evict_last(); }
   static __device__ __forceinline__ uint64_t policy_b() { return l2_policy_evict_normal(); }

@@ -88,7 +88,8 @@ struct PlainOperands {
     return kb * kTileK;
   }
   // first B row that the pair's CTA `rank` loads for the unit's tile j
-  static __device__ __forceinline__ int b_row(int n0, int j, int bn, int rank, int rows) {
+  template <class P>
+  static __device__ __forceinline__ int b_row(const P&, int n0, int j, int bn, int rank, int rows) {
     return n0 + j * bn + rank * rows;
   }
   template <class M>
@@ -309,7 +310,7 @@ __device__ __forceinline__ void run_producer_k(const SharedState& st, const type
     // hides behind the loads still to issue
     const int draw_at = ui.nkb > 4 ? ui.nkb - 4 : 0;
     for (int j = 0; j < ui.ntiles; ++j) {
-      const int b_row = Cfg::b_row(ui.n0, j, Cfg::BN, static_cast<int>(st.rank), b_rows);
+      const int b_row = Cfg::b_row(p, ui.n0, j, Cfg::BN, static_cast<int>(st.rank), b_rows);
       for (int kb = 0; kb < ui.nkb; kb += kps) {
         if (dyn && leader && j == ui.ntiles - 1 && kb <= draw_at && draw_at < kb + kps)
           ticket = atomicAdd(Cfg::sched_counter(p), 1);

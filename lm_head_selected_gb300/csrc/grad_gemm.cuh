@@ -57,6 +57,14 @@ struct GradCfg : PlainOperands {
   // grad_weight's B is the hidden states
   static __device__ __forceinline__ void on_launch(const Params&) {}
 
+  // The odd CTA's half of a last column tile may lie past the end: it loads the even one's columns then, for
+  // accumulator columns that no one reads.  A copy from outside the tensor is not free: those of all pairs went
+  // to the same few lines of L2 (the gated layer's elementwise pass and grad_x at 16384 x 128 x 384 27 us, 16
+  // with this).
+  static __device__ __forceinline__ int b_row(const Params& p, int n0, int, int, int rank, int rows) {
+    return n0 + rank * rows < p.D ? n0 + rank * rows : n0;
+  }
+
   static __device__ __forceinline__ int num_units(const Params& p) { return p.nseg * p.num_m * p.num_d; }
 
   // Segment is the slowest index, then M tile, then the output column tile, so the
