@@ -18,7 +18,8 @@
 // Bound by the tensor cores for batches.  16384 x 2688 x 10752 bf16: forward with both projections kept
 // 1.05 to 1.17 ms as the power-capped clock has it (1.61 to 1.8 PFLOP/s, 94 to 105% of the measured sustained
 // rate); gradient 2.52 to 2.65 ms: the elementwise pass 0.275 (6.4 TB/s), the GEMMs 1.07 each (1.77
-// PFLOP/s).  512 x 2688 x 10752: gradient 104 us, 158 without the split of grad_x's sum.
+// PFLOP/s).  512 x 2688 x 10752: gradient 104 us, 158 without the split of grad_x's sum.  24772 x 544 x 360: 71
+// us, 169 without the split of the weights' sums over the tokens.
 #include "gated.h"
 
 #include "grad_gemm.cuh"
