@@ -8,6 +8,7 @@ from __future__ import annotations
 import array
 import math
 import operator
+from itertools import compress
 from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
@@ -74,7 +75,7 @@ def _codes(params: list, grads: list, index: int):
         p_code = list(map(_DTYPE_CODES.__getitem__, map(_dtype, params)))
         g_code = list(map(_DTYPE_CODES.__getitem__, map(_dtype, grads)))
         n = len(params)
-        if ((p_code == g_code or all(g == c or g == 1 for c, g in zip(p_code, g_code))) and
+        if ((p_code == g_code or g_code.count(1) == n or all(g == c or g == 1 for c, g in zip(p_code, g_code))) and
                 list(map(_shape, params)) == list(map(_shape, grads)) and
                 list(map(_device_of, params)).count(index) == list(map(_device_of, grads)).count(index) == n and
                 all(map(_contiguous, params)) and all(map(_contiguous, grads))):
@@ -157,13 +158,14 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         masters = list(masters)
         if len(masters) != count:
             raise ValueError(f"masters must have {count} entries, got {len(masters)}")
-        there = [i for i, t in enumerate(masters) if t is not None]
-        _need_all("masters", [masters[i] for i in there], [sizes[i] for i in there], index, torch.float32)
-        words += [0 if t is None else t.data_ptr() for t in masters]
+        there = [t is not None for t in masters]
+        _need_all("masters", compress(masters, there), list(compress(sizes, there)), index, torch.float32)
+        at = map(_data_ptr, compress(masters, there))
+        words += [next(at) if b else 0 for b in there]
     # what is written must be somewhere of its own
     written, read = words[:count] + words[2 * count:], words[count:2 * count]
-    places = set(written)
-    if len(places) != len(written) or not places.isdisjoint(read):
+    places, none = set(written), written.count(0)  # tensors without elements, masters that are not there
+    if len(places) != len(written) - max(none - 1, 0) or not places.isdisjoint(read):
         written = [a for a, n in zip(written, sizes * (len(words) // count)) if n and a]
         places = set(written)
         if len(places) != len(written):
