@@ -31,13 +31,35 @@ def inputs(N, D, dtype, pdt, gate, post, norm, branch=True, seed=0):
 
 def within(name, got, ref, bound):
     """within(), for outputs that may pass the type's range: half a step past its largest value and
-    further out, rounding to nearest gives infinity (65520 in fp16, whose largest is 65504)."""
+    further out, rounding to nearest gives infinity (65520 in fp16, whose largest is 65504).  bound is the
+    one rounding's error and that of the value v in fp32 before it, |v - ref| <= err.  The output is infinite
+    where |v| >= edge: surely where |ref| - err >= edge, never where |ref| + err < edge, and between the two
+    either that or, as everywhere else, a value within the bound."""
     top = torch.finfo(got.dtype).max
     edge = top + 2.0 ** np.floor(np.log2(top)) * torch.finfo(got.dtype).eps / 2
-    over = np.abs(ref) - bound >= edge
-    value = np64(got)
-    assert (value[over] == np.sign(ref[over]) * np.inf).all(), name
+    err = bound - rounded(ref, got.dtype)
+    value, infinite = np64(got), np.copysign(np.inf, ref)
+    surely = np.abs(ref) - err >= edge
+    assert (value[surely] == infinite[surely]).all(), name
+    over = surely | ((np.abs(ref) + err >= edge) & (value == infinite))
     within_range(name, torch.from_numpy(np.where(over, ref, value)), ref, bound)
+
+
+def test_what_counts_as_infinite():
+    half, inf = torch.float16, float("inf")
+
+    def passes(got, ref, err):
+        ref = np.array([ref])
+        try:
+            within("", torch.tensor([got], dtype=half), ref, rounded(ref, half) + err)
+        except AssertionError:
+            return False
+        return True
+
+    assert passes(inf, 65524.3, 0.1) and not passes(65504.0, 65524.3, 0.1)   # past the edge
+    assert passes(65504.0, 65516.0, 0.1) and not passes(inf, 65516.0, 0.1)   # before it
+    assert passes(inf, 65518.0, 4.0) and passes(65504.0, 65518.0, 4.0)       # either side of it within err
+    assert passes(-inf, -65524.3, 0.1) and not passes(inf, -65524.3, 0.1) and not passes(inf, 100.0, 0.1)
 
 
 def n64(t):
