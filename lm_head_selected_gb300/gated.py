@@ -2,7 +2,8 @@
 
 Argument marshalling only; the computation runs in ``liblinear_logp.so``.  x [N, D]
 and the weights [F, D] are all bf16 or all fp16, contiguous, on a CUDA device, with D
-and F multiples of 8.
+and F multiples of 8.  Every tensor starts on a 16-byte boundary; ``gated_linear`` copies an
+input, or a gradient that autograd brings, which does not.
 """
 from __future__ import annotations
 
@@ -22,6 +23,20 @@ def _activation(name: str) -> int:
     if code is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
     return code
+
+
+def _finish(fn: str, status: int, **tensors) -> None:
+    if status == _lib.LLP_ERR_MISALIGNED:
+        for name, t in tensors.items():
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{name} must start on a 16-byte boundary")
+    _lib.check(fn, status)
+
+
+def _movable(t: torch.Tensor) -> torch.Tensor:
+    """The tensor, contiguous and on a 16-byte boundary: itself, or a copy."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
 
 
 def _check(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor) -> int:
@@ -54,7 +69,7 @@ def gated_linear_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     pre = torch.empty((2, N, F), dtype=x.dtype, device=dev) if keep else None
     st = _lib.load().gated_linear_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), code, act, N, D, F,
                                       y.data_ptr(), None if pre is None else pre.data_ptr(), _raw_stream(dev.index))
-    _lib.check("gated_linear_fwd", st)
+    _finish("gated_linear_fwd", st, x=x, w_gate=w_gate, w_up=w_up, out=out)
     return (y, pre) if keep else y
 
 
@@ -81,7 +96,7 @@ def gated_linear_bwd(grad_y: torch.Tensor, pre: torch.Tensor, x: torch.Tensor, w
     st = lib.gated_linear_bwd(grad_y.data_ptr(), pre.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
                               code, act, N, D, F, *(None if t is None else t.data_ptr() for t in (gx, gg, gu)),
                               ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
-    _lib.check("gated_linear_bwd", st)
+    _finish("gated_linear_bwd", st, grad_y=grad_y, pre=pre, x=x, w_gate=w_gate, w_up=w_up)
     return gx, gg, gu
 
 
@@ -99,18 +114,19 @@ class _GatedLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y):
         x, w_gate, w_up, pre = ctx.saved_tensors
-        return (*gated_linear_bwd(grad_y.contiguous(), pre, x, w_gate, w_up, ctx.activation,
+        return (*gated_linear_bwd(_movable(grad_y), pre, x, w_gate, w_up, ctx.activation,
                                   *ctx.needs_input_grad[:3]), None, None)
 
 
 def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu") -> torch.Tensor:
     """act(x w_gate^T) * (x w_up^T) over the last dimension, with autograd: x [..., D] -> [..., F].
-    Where a gradient is wanted, both projections [2, N, F] are kept for it."""
+    Where a gradient is wanted, both projections [2, N, F] are kept for it.  The weights must start on a
+    16-byte boundary; an x that does not is copied."""
     _need_cuda(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have at least one column")
     _need_cuda(w_gate, "w_gate")
     _need_cuda(w_up, "w_up")
     keep = torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad)
-    x2 = x.reshape(-1, x.shape[-1]).contiguous()
+    x2 = _movable(x.reshape(-1, x.shape[-1]))
     return _GatedLinear.apply(x2, w_gate, w_up, activation, keep).reshape(*x.shape[:-1], w_gate.shape[0])
