@@ -11,6 +11,8 @@
  *
  * in fp32, from the fp32 master copy where there is one (which is then updated,
  * and the parameter is its rounding), else from the parameter itself.
+ * Decay and update are summed and subtracted from the parameter in one rounding, so
+ * that a small rate times decay keeps its digits.
  *
  * States in 32 bits are fp32.  States in 8 bits are e4m3 values (one sign, four
  * exponent and three fraction bits) times a scale that ADAMW_BLOCK consecutive

@@ -9,6 +9,8 @@
 // 1123 us: the blocks to come in a ring of shared memory (828), codes in 16-byte copies and scales not
 // loaded by themselves (755), scales stored 64 bytes at a time (698), fewer warps with deeper rings and no
 // spills (652), codes exact to the border (669), the warps' rings on banks of their own (600).
+#include <cfloat>
+
 #include <cuda_fp8.h>
 
 #include "adamw_internal.h"
@@ -91,18 +93,26 @@ __device__ __forceinline__ void store_few(typename Elem<DT>::T* p, int n, const 
     if (i < n) p[i] = Elem<DT>::put(v[i]);
 }
 
+// The parameter less decay * p and the update, one rounding for the three: a factor 1 - decay would be rounded to
+// 2^-25 beforehand, for every element and step alike (a decay of 1e-7 19% too large, one of 1e-8 lost).  An
+// infinite parameter stays what it is.
+__device__ __forceinline__ float bounded(float p) { return fminf(fmaxf(p, -FLT_MAX), FLT_MAX); }
+__device__ __forceinline__ F2 moved(F2 p, float decay, F2 minus_update) {
+  return add2(p, fma2(f2(bounded(p.x), bounded(p.y)), f2(-decay), minus_update));
+}
+
 // The moments and the parameter's new value.
-__device__ __forceinline__ void update(const Step& s, float shrink, float g, float& m, float& v, float& root, float& p) {
+__device__ __forceinline__ void update(const Step& s, float decay, float g, float& m, float& v, float& root, float& p) {
   g *= s.scale;
   m = fmaf(s.b1, m, s.c1 * g);
   v = fmaf(s.b2, v, s.c2 * g * g);
   root = sqrtf(v);
-  p = fmaf(p, shrink, -s.rate_m * __fdividef(m, fmaf(root, s.root_v, s.eps)));
+  p -= fmaf(bounded(p), decay, s.rate_m * __fdividef(m, fmaf(root, s.root_v, s.eps)));
 }
 
 // 32-bit states: N elements from `at`; VEC: all of them, whole vectors.
 template <int PD, int GD, int N, bool VEC>
-__device__ __forceinline__ void plain_elements(const AdamTensor& t, const Step& s, float shrink, long long at, int n) {
+__device__ __forceinline__ void plain_elements(const AdamTensor& t, const Step& s, float decay, long long at, int n) {
   using P = typename Elem<PD>::T;
   using G = typename Elem<GD>::T;
   P* const p = static_cast<P*>(t.p) + at;
@@ -127,7 +137,7 @@ __device__ __forceinline__ void plain_elements(const AdamTensor& t, const Step& 
       load_few<PD, N>(p, n, pv);
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) update(s, shrink, gv[i], mv[i], vv[i], root, pv[i]);
+  for (int i = 0; i < N; ++i) update(s, decay, gv[i], mv[i], vv[i], root, pv[i]);
   if (VEC) {
     store_wide<kDtypeF32, N>(m, mv);
     store_wide<kDtypeF32, N>(v, vv);
@@ -144,22 +154,22 @@ __device__ __forceinline__ void plain_elements(const AdamTensor& t, const Step& 
 template <int PD, int GD>
 __device__ __forceinline__ void plain_chunk(const AdamTensor& t, const Step* shared, int chunk) {
   const Step s = *shared;
-  const float shrink = 1.f - s.rate * t.decay;
+  const float decay = s.rate * t.decay;
   const int head = t.head < 0 ? 0 : t.head;
   const long long at = head + static_cast<long long>(chunk) * kAdamChunk;
   const int n = static_cast<int>(t.n - at < kAdamChunk ? t.n - at : kAdamChunk);  // head <= t.n: never below 0
   if (chunk == 0 && static_cast<int>(threadIdx.x) < head)
-    plain_elements<PD, GD, 1, false>(t, s, shrink, threadIdx.x, 1);
+    plain_elements<PD, GD, 1, false>(t, s, decay, threadIdx.x, 1);
   if (t.head < 0) {
-    for (int i = threadIdx.x; i < n; i += kAdamThreads) plain_elements<PD, GD, 1, false>(t, s, shrink, at + i, 1);
+    for (int i = threadIdx.x; i < n; i += kAdamThreads) plain_elements<PD, GD, 1, false>(t, s, decay, at + i, 1);
     return;
   }
 #pragma unroll 1
   for (int i = threadIdx.x * W; i < n; i += kAdamThreads * W) {
     if (i + W <= n)
-      plain_elements<PD, GD, W, true>(t, s, shrink, at + i, W);
+      plain_elements<PD, GD, W, true>(t, s, decay, at + i, W);
     else
-      plain_elements<PD, GD, W, false>(t, s, shrink, at + i, n - i);
+      plain_elements<PD, GD, W, false>(t, s, decay, at + i, n - i);
   }
 }
 
@@ -394,7 +404,7 @@ __device__ __forceinline__ F2 second_moment(const Step& s, F2 code, float scale,
 // definition in fp32 gives, which a value next to the border between two codes would otherwise miss by
 // an eighth.  The warp's lanes share the two maxima; all of them must come here.
 template <int PD, int GD, bool MASTER, bool WHOLE>
-__device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, float shrink, long long block, int n,
+__device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, float decay, long long block, int n,
                                          const Packed<PD, GD, MASTER>& r) {
   constexpr int H = W / 2;
   F2 p[H], m[H], u[H];
@@ -407,7 +417,7 @@ __device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, flo
     m[i] = first_moment(s, codes_to_f2(i < 2 ? r.m.x : r.m.y, i & 1), r.ms, g);
     u[i] = f2(sqrtf(v.x), sqrtf(v.y));
     const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
-    p[i] = fma2(p[i], f2(shrink), mul2(f2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y)), f2(-s.rate_m)));
+    p[i] = moved(p[i], decay, mul2(f2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y)), f2(-s.rate_m)));
     mt = nan_max(mt, nan_max(fabsf(m[i].x), fabsf(m[i].y)));
     ut = nan_max(ut, nan_max(u[i].x, u[i].y));
   }
@@ -431,14 +441,14 @@ __device__ __forceinline__ void step_any(const AdamTensor& t, const Step& s, flo
 // block is left to step_any (about one in a hundred).  The new scales are the caller's to store.  False,
 // and nothing written, where this form will not do.
 template <int PD, int GD, bool MASTER, bool WHOLE>
-__device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, float shrink, long long block,
+__device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, float decay, long long block,
                                            const Packed<PD, GD, MASTER>& r, float& ms, float& us) {
   constexpr int H = W / 2;
   constexpr float kLow = 1e-15f, kHigh = 1e15f, kMargin = 1.f / 524288.f;
   if (!(r.vs > kLow && r.vs < kHigh && r.ms < kHigh)) return false;  // the same in all lanes
   F2 p[H], m[H], u[H];
   unpack_packed(r, p, u);
-  float mt = 0.f, vt = 0.f, least = kHigh;
+  float mt = 0.f, vt = 0.f, pt = 0.f, least = kHigh;
 #pragma unroll
   for (int i = 0; i < H; ++i) {
     const F2 g = mul2(u[i], f2(s.scale));
@@ -449,11 +459,13 @@ __device__ __forceinline__ bool step_usual(const AdamTensor& t, const Step& s, f
     mt = nan_max3_abs(mt, m[i].x, m[i].y);
     u[i] = f2(root_ftz(v.x), root_ftz(v.y));
     const F2 d = fma2(u[i], f2(s.root_v), f2(s.eps));
-    p[i] = fma2(mul2(m[i], f2(inverse_ftz(d.x), inverse_ftz(d.y))), f2(-s.rate_m), mul2(p[i], f2(shrink)));
+    pt = nan_max3_abs(pt, p[i].x, p[i].y);
+    const F2 update = mul2(mul2(m[i], f2(inverse_ftz(d.x), inverse_ftz(d.y))), f2(-s.rate_m));
+    p[i] = add2(p[i], fma2(p[i], f2(-decay), update));
   }
   mt = warp_top(mt);
   vt = warp_top(vt);
-  bool fine = least > 1e-36f && mt > 1e-25f && mt < kHigh && vt < kHigh * kHigh;  // no: a NaN too
+  bool fine = least > 1e-36f && mt > 1e-25f && mt < kHigh && vt < kHigh * kHigh && pt < kHigh;  // no: a NaN too
   const float ut = __fsqrt_rn(vt);  // the largest root
   ms = mt * (1.f / kTop8);
   us = ut * (1.f / kTop8);
@@ -484,7 +496,7 @@ template <int PD, int GD, bool MASTER>
 __device__ __noinline__ void packed_rest(const AdamTensor& t, const Step* shared, long long mine, long long end,
                                          long long stop, unsigned done) {
   const Step s = *shared;
-  const float shrink = 1.f - s.rate * t.decay;
+  const float decay = s.rate * t.decay;
   Packed<PD, GD, MASTER> r;
 #pragma unroll 1
   for (int i = 0; i < kWarpBlocks && mine + i < end; ++i) {
@@ -492,17 +504,17 @@ __device__ __noinline__ void packed_rest(const AdamTensor& t, const Step* shared
     if (done >> i & 1) continue;
     if (b < stop) {
       load_packed(t, b, r);
-      step_any<PD, GD, MASTER, true>(t, s, shrink, b, W, r);
+      step_any<PD, GD, MASTER, true>(t, s, decay, b, W, r);
     } else {
       const long long left = t.n - (b * kAdamBlock + (threadIdx.x & 31) * W);
       const int n = left < W ? (left > 0 ? static_cast<int>(left) : 0) : W;
       load_packed_few(t, b, n, r);
       // wherever a block lies, the same steps give the same bits
       float ms, us;
-      if ((b + 1) * kAdamBlock <= t.n && step_usual<PD, GD, MASTER, false>(t, s, shrink, b, r, ms, us))
+      if ((b + 1) * kAdamBlock <= t.n && step_usual<PD, GD, MASTER, false>(t, s, decay, b, r, ms, us))
         store_scales(t, b, ms, us);
       else
-        step_any<PD, GD, MASTER, false>(t, s, shrink, b, n, r);
+        step_any<PD, GD, MASTER, false>(t, s, decay, b, n, r);
     }
   }
 }
@@ -527,7 +539,7 @@ __device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* sh
   unsigned done = 0;
   if (mine < stop) {
     const Step s = *shared;
-    const float shrink = 1.f - s.rate * t.decay;
+    const float decay = s.rate * t.decay;
     const int count = static_cast<int>(stop - mine);
 #pragma unroll
     for (int i = 0; i < kAhead - 1; ++i) {
@@ -555,7 +567,7 @@ __device__ __forceinline__ void packed_chunk(const AdamTensor& t, const Step* sh
         r.ms = __shfl_sync(0xffffffffu, scales, k);
         r.vs = __shfl_sync(0xffffffffu, scales, 16 + k);
         float ms, us;
-        if (step_usual<PD, GD, MASTER, true>(t, s, shrink, mine + k, r, ms, us)) {
+        if (step_usual<PD, GD, MASTER, true>(t, s, decay, mine + k, r, ms, us)) {
           done |= 1u << k;
           if (j == k) scales = lane < 16 ? ms : us;
         }
