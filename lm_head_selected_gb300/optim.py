@@ -8,7 +8,7 @@ from __future__ import annotations
 import array
 import math
 import operator
-from itertools import compress
+from itertools import chain, compress
 from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
@@ -201,7 +201,10 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
         with torch.cuda.device(device):
             call()
     # autograd learns that they have changed
+    changed = list(chain(params, *lists[2:]))
+    if masters is not None:
+        changed += compress(masters, there)
     try:
-        torch.autograd.graph.increment_version(params)
+        torch.autograd.graph.increment_version(changed)
     except RuntimeError:  # tensors made under inference mode have no version to count
-        torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])
+        torch.autograd.graph.increment_version([t for t in changed if not t.is_inference()])
