@@ -28,6 +28,7 @@ def adamw_state(params: Tensors, bits: int = 32, masters: bool = False) -> dict:
     copy of every parameter that is not fp32 itself."""
     if bits not in (32, 8):
         raise ValueError(f"bits must be 32 or 8, got {bits}")
+    params = list(params)
     for i, p in enumerate(params):
         _need_cuda(p, f"params[{i}]")
 
