@@ -26,8 +26,8 @@
  *
  * Sums and statistics are fp32, every output is rounded once; h and rstd come from
  * the unrounded s, the gradient from the s it is given.  The order of a row's sums
- * depends on D, the types and the gate's kind alone, the order of the sums over rows on N, D and the
- * types: rows are bitwise the same for any batch, and all results in every run.
+ * depends on D, the types and the gate's kind alone, the order of the sums over rows on these and
+ * N: rows are bitwise the same for any batch, and all results in every run.
  *
  * Conventions as in linear_logp.h: device pointers, caller-owned buffers, work
  * enqueued on `stream`, arguments checked before anything is enqueued, the same
