@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_bwd_kernel(const
       const int t = i % N_IN;
       const bool there = t == 0 ? has_gs : t <= 2 ? has_w : t == 3 ? has_b : true;
       if (!AL || !on(k) || !there) mine[(i * K + k) * threads] = make_uint4(0, 0, 0, 0);
+      if (S::FIVE) fifth[(i * K + k) * threads] = 0;  // read wherever a row starts in the middle of a word
     }
   auto copy = [&](int t, const void* base, long long stride, unsigned n, int stage) {
     const T* const lo = static_cast<const T*>(base);

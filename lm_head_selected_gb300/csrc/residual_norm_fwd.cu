@@ -45,8 +45,10 @@ __global__ void __launch_bounds__(kResThreads, 1) residual_norm_fwd_kernel(const
   const bool has_b = p.branch != nullptr, f32 = p.param_dtype == kDtypeF32;
   for (int i = 0; i < stages * N_IN; ++i)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
       if (!AL || !on(k) || (!has_b && i % N_IN == 1)) mine[(i * K + k) * threads] = make_uint4(0, 0, 0, 0);
+      if (S::FIVE) fifth[(i * K + k) * threads] = 0;  // read wherever a row starts in the middle of a word
+    }
   auto copy = [&](const void* base, long long stride, unsigned n, int at) {
     const T* const lo = static_cast<const T*>(base);
     const T* const src = lo + static_cast<long long>(n) * stride + first * W;
