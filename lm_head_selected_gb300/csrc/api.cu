@@ -270,19 +270,19 @@ int make_map_part(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows
   return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
 }
 
-// One map over two row-major 16-bit matrices [rows][cols] of the same shape, `apart` bytes from the first
-// to the second: box {64, box_rows, 2, box_chunks} of {64, rows, 2, cols / 64} with chunks (cols a
-// multiple of 64), else {64, box_rows, 2} of {cols, rows, 2}.  Nothing between the two is reached.
-int make_map_two(CUtensorMap* m, const void* first, uint64_t apart, uint64_t cols, uint64_t rows, uint32_t box_rows,
-                 uint32_t box_chunks, bool chunked, bool f16) {
-  cuuint64_t dims[4] = {chunked ? 64 : cols, rows, 2, cols / 64};
-  cuuint64_t strides[3] = {cols * 2, apart, 128};
-  cuuint32_t box[4] = {64, box_rows, 2, box_chunks};
+// 4-D map of a row-major 16-bit matrix [rows][cols], rows a multiple of 8 and cols one of 64, in groups of 8 rows:
+// {64, 8, cols / 64, rows / 8}.  A box {64, 8, box_chunks, box_rows / 8} lands in shared memory as the groups, each
+// the 1024 bytes of its 64-column chunks one after the other.
+int make_map_groups(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                    uint32_t box_chunks, bool f16) {
+  cuuint64_t dims[4] = {64, 8, cols / 64, rows / 8};
+  cuuint64_t strides[3] = {cols * 2, 128, cols * 16};
+  cuuint32_t box[4] = {64, 8, box_chunks, box_rows / 8};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                              chunked ? 4 : 3, const_cast<void*>(first), dims, strides, box, es,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) g_last_driver_result = static_cast<int>(r);
   return r == CUDA_SUCCESS ? LLP_OK : fail_cuda(__LINE__);
 }
@@ -1467,25 +1467,16 @@ int gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, int dt
   const bool f16 = dtype == llp::kDtypeF16;
   CUtensorMap tm_x, tm_wg, tm_wu, tm_y, tm_pre;
   llp::GatedSmallParams q = {};
-  // one map may reach both weights where they do not overlap (nor start 2^40 bytes apart)
-  const uintptr_t at_g = reinterpret_cast<uintptr_t>(w_gate), at_u = reinterpret_cast<uintptr_t>(w_up);
-  const uint64_t apart = at_u > at_g ? at_u - at_g : at_g - at_u;
-  q.joint = apart >= static_cast<uint64_t>(F) * D * 2 && apart < (uint64_t(1) << 40) ? 1 : 0;
-  q.up_first = at_u < at_g ? 1 : 0;
   if (llp::gated_small_plan(static_cast<int>(N), static_cast<int>(D), static_cast<int>(F), dev->num_sms, &q)) {
     // few tokens: the weights' rows on the MMA's M side
-    q.chunked = (D % 64) == 0 ? 1 : 0;
     const void* const base[3] = {w_gate, w_up, x};
     CUtensorMap* const map[3] = {&tm_wg, &tm_wu, &tm_x};
-    if (q.joint && make_map_two(&tm_wg, q.up_first ? w_up : w_gate, apart, D, F, static_cast<uint32_t>(q.R),
-                                static_cast<uint32_t>(q.c), q.chunked != 0, f16) != LLP_OK)
-      return fail_cuda(__LINE__);
-    if (q.joint) tm_wu = tm_wg;  // not loaded through
-    for (int i = q.joint ? 2 : 0; i < 3; ++i) {
+    for (int i = 0; i < 3; ++i) {
       const int64_t rows = i == 2 ? N : F;
-      const uint32_t box = static_cast<uint32_t>(i == 2 ? q.BN : q.R);
-      const int r = q.chunked ? make_map_chunked(map[i], base[i], D, rows, D * 2, box, static_cast<uint32_t>(q.c), f16)
-                              : make_map(map[i], base[i], D, rows, D * 2, 64, box, f16);
+      const uint32_t box = static_cast<uint32_t>(i == 2 ? q.BN : q.R), chunks = static_cast<uint32_t>(q.c);
+      const int r = !q.chunked         ? make_map(map[i], base[i], D, rows, D * 2, 64, box, f16)
+                    : i < 2 && q.joint ? make_map_groups(map[i], base[i], D, rows, box, chunks, f16)
+                                       : make_map_chunked(map[i], base[i], D, rows, D * 2, box, chunks, f16);
       if (r != LLP_OK) return fail_cuda(__LINE__);
     }
     q.act = act;

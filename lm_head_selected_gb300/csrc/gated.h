@@ -74,19 +74,18 @@ struct GatedSmallParams {
   int N, D, F;
   int BN;      // MMA N: N rounded up to 16
   int R;       // rows of each weight to a CTA (height of the weights' boxes)
-  int joint;   // both weights' rows in one MMA: asked for by the caller, kept where R is at most 64
-  int up_first;  // of the joint map: Wu lies below Wg in memory
+  int joint;   // both weights' rows in one MMA: where R is at most 64
   int units;   // of R rows
   int c;       // K blocks of a stage
   int stages;
   int tmem_cols;
-  int chunked;  // the maps are 3-D {64, rows, D / 64}: one copy per operand and stage (D % 64 == 0), else 2-D
+  int chunked;  // the maps reach several K blocks: one copy per operand and stage (D % 64 == 0), else 2-D
   int act, f16;
   uint16_t* y;
   uint16_t* pre;  // [2][N][F], or nullptr
   unsigned int* err;
 };
-// Fills all up to tmem_cols, from joint as asked for; false when the batch is too large for the kernel.
+// Fills all up to chunked; false when the batch is too large for the kernel.
 bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p);
 cudaError_t gated_small_setup();
 cudaError_t launch_gated_small(const CUtensorMap& wg, const CUtensorMap& wu, const CUtensorMap& x,

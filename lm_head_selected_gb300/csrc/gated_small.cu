@@ -13,11 +13,16 @@
 // Where R is at most 64 (JOINT) both weights' rows go into one MMA, lanes 0..R-1 and R..2R-1: an MMA of few
 // tokens takes about 80 cycles, mostly to read its 128 rows, and with two of them a step the K loop took
 // 0.34 us per K block whatever the weights' size (2048 x 4096 of one token 15.6 us, together 11.9).
-// One tensor map reaches both: its third dimension steps from one weight to the other.
+// The rows lie in groups of 8 (1024 bytes of a K block) at one stride: a copy of several K blocks brings each
+// group's blocks side by side, so that the up projection's first group follows the gate's last.
 // The epilogue then brings the two halves together through shared memory.
 //
+// Each weight has a map of its own.  One map over both, its third dimension stepping from one to the other,
+// needed a copy less for each stage, but the copies' columns past D were then fetched behind the lower weight's
+// last row, which faults where a mapped region ends there.
+//
 // An SM issues only about four tensor copies per microsecond whatever their size, so a stage is c K blocks
-// of 64 (c = 1, 2 or 4) and comes as three 3-D copies: the gate's rows, the up projection's, x (in L2).
+// of 64 (c = 1, 2 or 4) and comes as three copies: the gate's rows, the up projection's, x (in L2).
 // Every element accumulates the same 16-wide steps in the same ascending order as in the CTA-pair GEMM,
 // so that a token's row is bitwise the same in any batch.
 //
@@ -125,17 +130,10 @@ __global__ void __launch_bounds__(kGsThreads, 1)
           const uint32_t base = smem_u32(ring + st * stage_bytes);
           const uint32_t up = base + p.R * 128 * p.c, x = up + p.R * 128 * p.c;
           mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(stage_bytes));
-          if (JOINT) {
-            if (p.chunked) {
-              tma_load_4d(base, &tm_g, &full[st], 0, u * p.R, 0, g * p.c, pol_w);
-              tma_load_3d(x, &tm_x, &full[st], 0, 0, g * p.c, pol_x);
-            } else {
-              for (int c = 0; c < p.c; ++c) {
-                const int kx = (g * p.c + c) * 64;
-                tma_load_3d(base + c * 2 * p.R * 128, &tm_g, &full[st], kx, u * p.R, 0, pol_w);
-                tma_load_2d(x + c * p.BN * 128, &tm_x, &full[st], kx, 0, pol_x);
-              }
-            }
+          if (JOINT && p.chunked) {
+            tma_load_4d(base, &tm_g, &full[st], 0, 0, g * p.c, u * (p.R / 8), pol_w);
+            tma_load_4d(up, &tm_u, &full[st], 0, 0, g * p.c, u * (p.R / 8), pol_w);
+            tma_load_3d(x, &tm_x, &full[st], 0, 0, g * p.c, pol_x);
           } else if (p.chunked) {
             tma_load_3d(base, &tm_g, &full[st], 0, u * p.R, g * p.c, pol_w);
             tma_load_3d(up, &tm_u, &full[st], 0, u * p.R, g * p.c, pol_w);
@@ -143,8 +141,9 @@ __global__ void __launch_bounds__(kGsThreads, 1)
           } else {
             for (int c = 0; c < p.c; ++c) {
               const int kx = (g * p.c + c) * 64;
-              tma_load_2d(base + c * p.R * 128, &tm_g, &full[st], kx, u * p.R, pol_w);
-              tma_load_2d(up + c * p.R * 128, &tm_u, &full[st], kx, u * p.R, pol_w);
+              const uint32_t at = c * p.R * 128;  // JOINT: the two weights' rows of a K block lie together
+              tma_load_2d(JOINT ? base + 2 * at : base + at, &tm_g, &full[st], kx, u * p.R, pol_w);
+              tma_load_2d(JOINT ? base + 2 * at + p.R * 128 : up + at, &tm_u, &full[st], kx, u * p.R, pol_w);
               tma_load_2d(x + c * p.BN * 128, &tm_x, &full[st], kx, 0, pol_x);
             }
           }
@@ -158,6 +157,8 @@ __global__ void __launch_bounds__(kGsThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = make_idesc_16_f32(128, p.BN, false, false, p.f16 != 0);
+      // JOINT: from a K block to the next, and between groups of 8 rows
+      const uint32_t w_step = p.chunked ? 1024 : 2 * p.R * 128, w_group = p.chunked ? p.c * 1024 : 1024;
       int st = 0;
       uint32_t ph = 0, acc_ph = 0;
       for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kGsThreads, 1)
           const uint32_t base = smem_u32(ring + st * stage_bytes);
           for (int c = 0; c < p.c; ++c) {
             if (JOINT) {
-              const uint64_t wd = make_smem_desc_sw128(base + c * 2 * p.R * 128, 16, 1024);
+              const uint64_t wd = make_smem_desc_sw128(base + c * w_step, 16, w_group);
               const uint64_t xd = make_smem_desc_sw128(base + 2 * p.c * p.R * 128 + c * p.BN * 128, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -221,8 +222,8 @@ __global__ void __launch_bounds__(kGsThreads, 1)
         const int r = tid & 63, half = tid >> 6;
         const long long f = static_cast<long long>(u) * p.R + r;
         const bool mine = r < p.R && f < p.F;
-        const float* const gate_row = xch + (p.up_first ? p.R + r : r) * kXchPitch;
-        const float* const up_row = xch + (p.up_first ? r : p.R + r) * kXchPitch;
+        const float* const gate_row = xch + r * kXchPitch;
+        const float* const up_row = xch + (p.R + r) * kXchPitch;
         for (int n0 = 0; n0 < p.N; n0 += 32) {
           if ((warp & 3) * 32 < 2 * p.R) {  // warp-uniform
             float v[32];
@@ -302,10 +303,13 @@ __global__ void __launch_bounds__(kGsThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, p.tmem_cols);
 }
 
-// What an MMA reads behind the last stage's last rows.
+// What an MMA reads behind the last stage's last rows: it takes 16 groups, p.c K blocks apart in the joint maps'
+// layout, from the last K block's first.
 int gs_slack(const GatedSmallParams& p) {
-  const int behind = (p.joint ? 2 : 1) * p.R * 128 + p.c * p.BN * 128;
-  return behind < 16384 ? 16384 - behind : 0;
+  const bool apart = p.joint && p.chunked;
+  const int reads = apart ? 16384 * p.c : 16384;
+  const int there = apart ? gs_stage_bytes(p) : (p.joint ? 2 : 1) * p.R * 128 + p.c * p.BN * 128;
+  return there < reads ? reads - there : 0;
 }
 int gs_smem(const GatedSmallParams& p) { return 2048 + p.stages * gs_stage_bytes(p) + gs_slack(p); }
 
@@ -322,7 +326,8 @@ bool gated_small_plan(int N, int D, int F, int num_sms, GatedSmallParams* p) {
   const long long rows = (F + sms * waves - 1) / (sms * waves);
   p->R = static_cast<int>((rows + 7) / 8 * 8);
   p->units = (F + p->R - 1) / p->R;
-  if (p->R > 64) p->joint = 0;
+  p->joint = p->R <= 64 ? 1 : 0;
+  p->chunked = D % 64 == 0 ? 1 : 0;
   // K blocks per stage: as few as make a stage of 40 KB, at most four, and no more than there are
   const int blocks = (D + 63) / 64;
   p->c = 1;
