@@ -12,7 +12,7 @@
 //
 // Where R is at most 64 (JOINT) both weights' rows go into one MMA, lanes 0..R-1 and R..2R-1: an MMA of few
 // tokens takes about 80 cycles, mostly to read its 128 rows, and with two of them a step the K loop took
-// 0.34 us per K block whatever the weights' size (2048 x 4096 of one token 15.6 us, together 11.9).
+// 0.34 us per K block whatever the weights' size (2048 x 4096 of one token 15.6 us, together 11.1).
 // The rows lie in groups of 8 (1024 bytes of a K block) at one stride: a copy of several K blocks brings each
 // group's blocks side by side, so that the up projection's first group follows the gate's last.
 // The epilogue then brings the two halves together through shared memory.

@@ -120,11 +120,12 @@ def adamw_step(params: Tensors, grads: Tensors, exp_avg: Tensors, exp_avg_sq: Te
                device_step: Optional[torch.Tensor] = None, device_lr: Optional[torch.Tensor] = None,
                grad_scale: Optional[torch.Tensor] = None) -> None:
     """One AdamW step, in place, over all tensors (bf16, fp16 or fp32, each its own; gradients of the same
-    dtype or fp32; contiguous, on one CUDA device; none listed twice, no gradient a parameter or a state
-    too).  ``step`` counts from 1 (with device_step, their sum does).  States as ``adamw_state`` makes
-    them, in 8 bits where the scales are given.  ``weight_decay``: one value, or one per tensor.  On the device, read when the kernel runs, so that a captured graph can advance them:
-    ``device_step`` (int64, added to step), ``device_lr`` and ``grad_scale`` (fp32, factors of lr and of the
-    gradients)."""
+    dtype or fp32; contiguous, on one CUDA device).  None may be listed twice, no gradient be a parameter or a
+    state too: that is refused.  Nor may what is written overlap anything else in part, which is not looked for.
+    ``step`` counts from 1 (with device_step, their sum does).  States as ``adamw_state`` makes them, in 8 bits
+    where the scales are given.  ``weight_decay``: one value, or one per tensor.  On the device, read when the
+    kernel runs, so that a captured graph can advance them: ``device_step`` (int64, added to step), ``device_lr``
+    and ``grad_scale`` (fp32, factors of lr and of the gradients)."""
     params, grads = list(params), list(grads)
     count = len(params)
     if len(grads) != count:
